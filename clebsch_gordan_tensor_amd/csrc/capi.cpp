@@ -1,12 +1,11 @@
 // C ABI of libcgtp: argument checks, error translation, dispatch to launchers.
 // Nothing here computes; every step of the path runs in the HIP kernels.
 #include <cstring>
-#include <exception>
-#include <new>
 #include <string>
 
 #include "common.hpp"
 #include "graph.hpp"
+#include "guard.hpp"
 #include "linear.hpp"
 
 namespace cgtp {
@@ -16,33 +15,6 @@ thread_local std::string g_last_error;
 }
 
 void set_error(const std::string& msg) { g_last_error = msg; }
-
-template <typename F>
-cgtp_status guarded(F&& f) {
-  try {
-    g_last_error.clear();
-    f();
-    return CGTP_OK;
-  } catch (const Error& e) {
-    g_last_error = e.msg;
-    return e.code;
-  } catch (const std::bad_alloc&) {
-    g_last_error = "host allocation failed";
-    return CGTP_ERR_ALLOC;
-  } catch (const std::exception& e) {
-    g_last_error = e.what();
-    return CGTP_ERR_INVALID_ARG;
-  } catch (...) {
-    g_last_error = "unknown error";
-    return CGTP_ERR_INVALID_ARG;
-  }
-}
-
-inline void need(bool ok, const char* what) {
-  if (!ok) throw Error{CGTP_ERR_INVALID_ARG, what};
-}
-
-inline hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 
 // uvw plans and uvu plans with y multiplicity > 1 run the tensor product's
 // forward and backward only (their own kernels).

@@ -29,6 +29,7 @@ Modules:
   linear  - equivariant linear map (channel mixing)             [E3J A.3; COURSE 03b]
   modes   - connection modes uvu (any y multiplicity) and uvw   [COURSE 03b; E3J E.1]
   radial  - radial network's last layer joined to the convolution [COURSE 06a; E3J E.4, F.1; XNN]
+  layers  - group norm with activation, dropout, cross attention on irreps rows (their definitions)
 
 Parity status: every function here is pinned by tests/test_oracle_*.py against
 closed forms, textbook values, invariants or brute force; none is "parity
