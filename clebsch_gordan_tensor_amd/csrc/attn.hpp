@@ -1,0 +1,144 @@
+// Cross attention: argument blocks, work lists, handles.
+#pragma once
+
+#include "layers.hpp"
+
+namespace cgtp {
+namespace attn {
+
+// 32 consecutive rows: context rows, or query rows (token * G + head in group).
+struct Tile {
+  int32_t row0, n;
+};
+
+// Work of one workgroup: up to four tiles a0 .. a0 + tiles - 1 of one side for
+// context head hk, against tiles b0 .. b1 - 1 of the other. slot >= 0: the
+// result is part `slot` of a split, at tile slot * stride of the partial buffer;
+// tiles = 0: nothing (padding of the list).
+struct alignas(16) Item {
+  int32_t a0, tiles, b0, b1;
+  int32_t hk, slot, stride, pad;
+};
+
+// One tile whose result is the sum of parts slot .. slot + parts - 1, number
+// `within` of the `stride` tiles of each.
+struct alignas(16) Join {
+  int32_t tile, hk, slot, parts;
+  int32_t stride, within, pad0, pad1;
+};
+
+struct PackTensor {
+  const void* src;
+  int64_t ld;
+  void *row_frags, *col_frags;  // either may be NULL
+  float* rows_out;              // gradient rows: lse and delta (else NULL)
+  float* bias;                  // context: 0 or -inf for every key (one tensor of a call)
+  bool vec;                     // 16-byte gathers
+};
+
+struct PackArgs {
+  PackTensor t[2];
+  const Tile* tiles;
+  const int4* table;
+  const uint8_t* mask;  // context rows, or NULL
+  const void* out;      // forward's output (for delta)
+  int64_t ldo;
+  const float* lse;
+  int G, heads, groups;  // G = 0: context rows
+  bool out_vec;
+};
+
+struct FwdArgs {
+  const Item* items;
+  const Join* joins;
+  const Tile* qtiles;
+  const int4* table;
+  const void *q, *kf, *vf;
+  const float* bias;
+  void* out;
+  float *lse, *part, *part_ml;
+  int64_t ldq, ldo;
+  float scale2;  // scale log2 e
+  int G, heads, groups;
+  bool q_vec, out_quad;
+};
+
+struct BwdArgs {
+  const Item* items;
+  const Join* joins;
+  const Tile *qtiles, *ktiles;
+  const int4* table;
+  const void *kr, *kc, *vr, *qr, *qc, *gr, *gc;  // r: row fragments, c: column fragments; g: grad_out
+  const float *bias, *rows;
+  void *dq, *dk, *dv;
+  float *part, *part_v;
+  int64_t ldq, ldk;
+  float scale, scale2;
+  int G, heads, groups;
+  bool q_quad, k_quad;
+};
+
+struct KernelTable {
+  void (*pack)(const PackArgs&, int tiles, int tensors, hipStream_t);
+  void (*fwd)(const FwdArgs&, int items, bool few, hipStream_t);
+  void (*fwd_join)(const FwdArgs&, int joins, hipStream_t);
+  void (*dq)(const BwdArgs&, int items, hipStream_t);
+  void (*dkv)(const BwdArgs&, int items, hipStream_t);  // grad_k and grad_v, each unless NULL
+  void (*grad_join)(const BwdArgs&, int joins, bool query, const float* part, void* dst, int64_t ld, bool quad,
+                    hipStream_t);
+};
+
+// Kernels of a padded head size (a multiple of 32 up to 256); inst/attn_*.hip.
+KernelTable kernels_f32(int dp);
+KernelTable kernels_bf16(int dp);
+
+// A list of work items on the device with the joins of its splits.
+struct WorkList {
+  int items = 0, joins = 0;
+  int64_t part_tiles = 0;  // tiles of partial results
+  DevMem item_mem, join_mem;
+};
+
+}  // namespace attn
+}  // namespace cgtp
+
+struct cgtp_attn_s {
+  cgtp::RowLayout qrow, krow;
+  int heads = 1, kv_heads = 1, G = 1, D = 0, DP = 0;
+  bool vec16 = false, quad = false;  // every head's run is a multiple of 16 bytes / of 4 elements
+  cgtp_dtype dtype = CGTP_F32;
+  int device = 0;
+  cgtp::attn::KernelTable k{};
+  cgtp::DevMem table;  // int4 [DP]
+};
+
+struct cgtp_attn_batch_s {
+  cgtp_attn attn = nullptr;
+  int64_t nq = 0, nk = 0;            // rows
+  int64_t qtiles = 0, ktiles = 0;
+  int device = 0;
+  cgtp::DevMem qtile_mem, ktile_mem;
+  cgtp::attn::WorkList fwd, few, dq, dkv;
+};
+
+namespace cgtp {
+
+cgtp_attn_s* build_attn(const char* irreps, int64_t heads, int64_t kv_heads, cgtp_dtype dtype);
+cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, const cgtp_samples_s* k);
+size_t attn_context_bytes(const cgtp_attn_batch_s* b);
+size_t attn_forward_ws_bytes(const cgtp_attn_batch_s* b, bool packed);
+size_t attn_backward_ws_bytes(const cgtp_attn_batch_s* b);
+
+struct RowsIn {  // rows with a stride in elements
+  const void* p;
+  int64_t ld;
+};
+void attn_pack_launch(const cgtp_attn_batch_s* b, RowsIn k, RowsIn v, const uint8_t* mask, void* context,
+                      hipStream_t s);
+void attn_forward_launch(const cgtp_attn_batch_s* b, RowsIn q, const void* context, double scale, void* out,
+                         float* lse, void* ws, hipStream_t s);
+void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn v, const uint8_t* mask, double scale,
+                          const void* out, const float* lse, RowsIn g, void* dq, void* dk, void* dv, void* ws,
+                          hipStream_t s);
+
+}  // namespace cgtp

@@ -1,0 +1,848 @@
+// Cross attention on irreps rows: kernels templated on storage type and padded
+// head size (instantiated in inst/attn_*.hip, launched by attn_kernels.hip).
+//
+// For a query row (one query, one head) and the keys of its sample:
+//   s_j = scale q.k_j,  p = softmax s,  o = sum_j p_j v_j
+// A row of 32 queries x a tile of 32 keys is one matrix-core tile. The kernels
+// compute S^T = K Q^T, so that a lane holds one query (column lane % 32) and 16
+// of the tile's keys, reduces over keys mostly inside the lane, and feeds the
+// same registers as the B operand of O^T += V^T P^T: no exchange between lanes
+// and no shared memory for P.
+//
+// The keys come packed in "fragments", the order in which a wave reads a matrix
+// operand: 1 KB units of 64 lanes x 16 bytes (VE = 8 bf16 or 4 fp32 values).
+//   row fragment t of a 32 x DP tile:    lane l holds [l % 32][2 VE t + VE h + j]
+//   column fragment (dt, f) of the tile: lane l holds, for column 32 dt + l % 32,
+//       the rows 8 (r / 4) + 4 h + r % 4 with r = VE f + j
+// (h = l / 32, j = 0 .. VE - 1; the row order of the second is the one in which
+// the accumulator registers of S^T hold the keys). Packing gathers a head's
+// channels out of the irreps blocks, pads heads to DP and tiles to 32 rows with
+// zeros and writes zeros for masked rows, so the matrix kernels read straight
+// 1 KB runs and never see a masked value.
+#pragma once
+
+#include "attn.hpp"
+#include "device_util.hpp"
+
+namespace cgtp {
+namespace attn {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kThreads = 256;  // 4 waves
+
+// Matrix operands: 16 bytes a lane.
+template <typename T>
+struct Op;
+template <>
+struct Op<bf16> {
+  static constexpr int VE = 8;
+  using Frag = bf16x8;
+  static __device__ __forceinline__ f32x16 mma(Frag a, Frag b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+  // accumulator registers VE f .. VE f + 7 rounded to an operand
+  static __device__ __forceinline__ Frag from_acc(const f32x16& s, int f) {
+    Frag r;
+#pragma unroll
+    for (int j = 0; j < VE; ++j) r[j] = static_cast<__bf16>(s[VE * f + j]);
+    return r;
+  }
+};
+template <>
+struct Op<float> {
+  static constexpr int VE = 4;
+  using Frag = f32x4;
+  static __device__ __forceinline__ f32x16 mma(Frag a, Frag b, f32x16 c) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
+    return c;
+  }
+  static __device__ __forceinline__ Frag from_acc(const f32x16& s, int f) {
+    Frag r;
+#pragma unroll
+    for (int j = 0; j < VE; ++j) r[j] = s[VE * f + j];
+    return r;
+  }
+};
+
+template <typename T, int DP>
+struct Dims {
+  static constexpr int VE = Op<T>::VE;
+  static constexpr int KSTEPS = DP / (2 * VE);  // row fragments of a tile
+  static constexpr int DT = DP / 32;            // column groups of a tile
+  static constexpr int FR = 16 / VE;            // column fragments of a column group
+  static constexpr int TILE = DP * 32;          // elements of a packed tile
+  static constexpr int UNITS = TILE * int(sizeof(T)) / 1024;
+  // the widest heads (fp32, 256) leave too few registers for whole operands: some
+  // are read again from memory as they are used
+  static constexpr bool kShort = DP * int(sizeof(T)) > 896;
+};
+
+__device__ __forceinline__ f32x16 zero16() {
+  f32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+  return z;
+}
+
+// max and sum over the two halves of a wave (the two lanes of one query).
+__device__ __forceinline__ float half_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Unit u of a packed tile, this lane's 16 bytes.
+template <typename T>
+__device__ __forceinline__ u32x4 unit16(const T* tile, int u, int lane) {
+  return *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(tile) + u * 1024 + lane * 16);
+}
+template <typename F>
+__device__ __forceinline__ F as_frag(const u32x4& v) {
+  return __builtin_bit_cast(F, v);
+}
+
+// One 1 KB unit copied from memory to shared memory without passing the
+// registers; complete after wait_copies() and a barrier. dst is uniform over the
+// wave.
+template <typename T>
+__device__ __forceinline__ void copy_unit(const T* tile, int u, int lane, u32x4* dst) {
+  __builtin_amdgcn_global_load_lds(
+      (const __attribute__((address_space(1))) void*)(reinterpret_cast<const char*>(tile) + u * 1024 + lane * 16),
+      (__attribute__((address_space(3))) void*)(dst), 16, 0, 0);
+}
+__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(int(threadIdx.x) / 64); }
+
+// Element address of head-vector element d of query row (token, head) or of
+// context row (token, head): table entry (query offset, context offset,
+// channels per head, 1 inside the head).
+__device__ __forceinline__ int64_t elem(const int4& e, bool query, int head) {
+  return (query ? e.x : e.y) + int64_t(head) * e.z;
+}
+
+// 16 bytes (VE elements from d0 on) of a row; zeros outside the head.
+template <typename T>
+__device__ __forceinline__ u32x4 gather16(const T* row, const int4* table, int d0, bool query, int head, bool vec) {
+  constexpr int VE = Op<T>::VE;
+  u32x4 v = {0, 0, 0, 0};
+  const int4 e = table[d0];
+  if (vec) {
+    if (e.w) v = *reinterpret_cast<const u32x4*>(row + elem(e, query, head));
+  } else if (e.w) {
+    T t[VE];
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+      const int4 ej = table[d0 + j];
+      t[j] = T{};
+      if (ej.w) t[j] = row[elem(ej, query, head)];
+    }
+    __builtin_memcpy(&v, t, 16);
+  }
+  return v;
+}
+
+// Four consecutive head elements d0 .. d0 + 3 of one row, from fp32.
+template <typename T>
+__device__ __forceinline__ void scatter4(T* row, const int4* table, int d0, bool query, int head, bool quad,
+                                         const float (&v)[4]) {
+  const int4 e = table[d0];
+  if (!e.w) return;
+  if (quad) {
+    VecIO<T, 4>::store(row + elem(e, query, head), v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int4 ej = table[d0 + j];
+      if (ej.w) from_acc(row[elem(ej, query, head)], v[j]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ packing
+//
+// One workgroup packs one 32-row tile of one head group: gather into shared
+// memory (16 bytes a lane), write row and/or column fragments (1 KB runs).
+// Bound: memory (each element read once and written once per form).
+template <typename T, int DP>
+__global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
+  using D = Dims<T, DP>;
+  constexpr int VE = D::VE, LD = DP + VE;  // an odd count of 16-byte pieces a row: no bank conflicts
+  __shared__ __attribute__((aligned(16))) T sh[32 * LD];
+  __shared__ float red[32][9];
+  const int tile = int(blockIdx.x), hk = int(blockIdx.y);
+  const PackTensor p = a.t[blockIdx.z];
+  const Tile tl = a.tiles[tile];
+  const int tid = int(threadIdx.x);
+  const bool query = a.G > 0;
+  const int G = query ? a.G : 1;
+  constexpr int PIECES = DP / VE;
+  // rows a query cannot see, or that see nothing, count as zero
+  float partial = 0.0f;
+  const int r = tid / 8;  // 8 threads a row
+  const bool in = r < tl.n;
+  const int grow = tl.row0 + (in ? r : 0);
+  const int token = grow / G, head = hk * G + grow % G;
+  bool live = in && (a.mask == nullptr || a.mask[token] != 0);
+  float lse = 0.0f;
+  if (p.rows_out && in) {
+    lse = a.lse[int64_t(token) * a.heads + head];
+    live = lse > -INFINITY;
+  }
+  for (int c = tid % 8; c < PIECES; c += 8) {
+    u32x4 v = {0, 0, 0, 0};
+    if (live) {
+      v = gather16(static_cast<const T*>(p.src) + int64_t(token) * p.ld, a.table, c * VE, query, head, p.vec);
+      if (p.rows_out) {
+        const u32x4 o = gather16(static_cast<const T*>(a.out) + int64_t(token) * a.ldo, a.table, c * VE, query, head,
+                                 a.out_vec);
+        T tv[VE], to[VE];
+        __builtin_memcpy(tv, &v, 16);
+        __builtin_memcpy(to, &o, 16);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) partial += to_acc<float>(tv[j]) * to_acc<float>(to[j]);
+      }
+    }
+    *reinterpret_cast<u32x4*>(&sh[r * LD + c * VE]) = v;
+  }
+  if (p.rows_out) red[r][tid % 8] = partial;
+  __syncthreads();
+  const int64_t at = (int64_t(tile) * a.groups + hk);
+  if (tid < 32) {
+    if (p.rows_out) {
+      // log2-domain lse (+inf: the row contributes nothing) and rowsum(grad_out out)
+      float d = 0.0f;
+      for (int k = 0; k < 8; ++k) d += red[tid][k];
+      const int gr = tl.row0 + (tid < tl.n ? tid : 0);
+      const float l = a.lse[int64_t(gr / G) * a.heads + hk * G + gr % G];
+      p.rows_out[at * 64 + tid] = tid < tl.n && l > -INFINITY ? l * 1.44269504088896341f : INFINITY;
+      p.rows_out[at * 64 + 32 + tid] = d;
+    }
+    if (p.bias && hk == 0)
+      p.bias[int64_t(tile) * 32 + tid] =
+          tid < tl.n && (a.mask == nullptr || a.mask[tl.row0 + tid] != 0) ? 0.0f : -INFINITY;
+  }
+  const int lane = tid % 64, wave = tid / 64, n = lane % 32, h = lane / 32;
+  if (p.row_frags) {
+    u32x4* o = reinterpret_cast<u32x4*>(static_cast<T*>(p.row_frags) + at * D::TILE);
+    for (int t = wave; t < D::KSTEPS; t += 4)
+      o[t * 64 + lane] = *reinterpret_cast<const u32x4*>(&sh[n * LD + 2 * VE * t + VE * h]);
+  }
+  if (p.col_frags) {
+    u32x4* o = reinterpret_cast<u32x4*>(static_cast<T*>(p.col_frags) + at * D::TILE);
+    for (int u = wave; u < D::DT * D::FR; u += 4) {
+      const int dt = u / D::FR, f = u % D::FR;
+      T t[VE];
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        const int rr = VE * f + j;
+        t[j] = sh[(8 * (rr / 4) + 4 * h + rr % 4) * LD + 32 * dt + n];
+      }
+      u32x4 v;
+      __builtin_memcpy(&v, t, 16);
+      o[u * 64 + lane] = v;
+    }
+  }
+}
+
+// ------------------------------------------------------------------- forward
+
+// Running softmax of one wave's 32 queries: a lane holds its query's reference
+// m (log2 domain), its own keys' sum l and O^T.
+template <int DT>
+struct Running {
+  float m = -INFINITY, l = 0.0f;
+  f32x16 o[DT];
+};
+
+// Folds a tile's scores into the running state and leaves exp2(s - m) in s. The
+// reference follows the maximum only when that grows by more than 2^8: the
+// weights stay below 2^8 (exact enough in either type, their sum is fp32), and
+// most tiles need no rescaling of O.
+template <int DT>
+__device__ __forceinline__ void fold_scores(Running<DT>& st, f32x16& s, float scale2, const float* bias, int h) {
+  float mx = -INFINITY;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const f32x4 bv = *reinterpret_cast<const f32x4*>(bias + 8 * b + 4 * h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[4 * b + i] = fmaf(s[4 * b + i], scale2, bv[i]);
+      mx = fmaxf(mx, s[4 * b + i]);
+    }
+  }
+  mx = half_max(mx);
+  if (__any(mx > st.m + 8.0f)) {
+    const float mn = fmaxf(st.m, mx);
+    const float alpha = mn == -INFINITY ? 1.0f : exp2_fast(st.m - mn);
+    st.m = mn;
+    st.l *= alpha;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) st.o[d] *= alpha;
+  }
+  const float ref = st.m == -INFINITY ? 0.0f : st.m;
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    s[i] = exp2_fast(s[i] - ref);
+    sum += s[i];
+  }
+  st.l += sum;
+}
+
+// Query fragments of tile `tl` straight from the rows.
+template <typename T, int DP>
+__device__ __forceinline__ void load_queries(const FwdArgs& a, const Tile& tl, int hk, int lane,
+                                             typename Op<T>::Frag (&q)[Dims<T, DP>::KSTEPS]) {
+  using D = Dims<T, DP>;
+  const int n = lane % 32, h = lane / 32;
+  const int row = tl.row0 + (n < tl.n ? n : tl.n - 1);
+  const int token = row / a.G, head = hk * a.G + row % a.G;
+  const T* src = static_cast<const T*>(a.q) + int64_t(token) * a.ldq;
+#pragma unroll
+  for (int t = 0; t < D::KSTEPS; ++t)
+    q[t] = as_frag<typename Op<T>::Frag>(gather16(src, a.table, 2 * D::VE * t + D::VE * h, true, head, a.q_vec));
+}
+
+// With few registers left: keeps the scheduler from reading operands far ahead.
+template <typename T, int DP>
+__device__ __forceinline__ void pace(int u) {
+  if (Dims<T, DP>::kShort && u % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+}
+
+// Stages kept in shared memory: two where they fit, the next one on its way
+// while this one is worked on, else one.
+constexpr int stage_buffers(int units) { return 2 * units <= 152 ? 2 : 1; }
+
+// Writes a wave's result: final rows, or an unnormalised part of a split.
+template <typename T, int DP>
+__device__ __forceinline__ void finish(const FwdArgs& a, const Item& it, const Tile& tl, int tile_in_item, int lane,
+                                       const Running<DP / 32>& st) {
+  const int n = lane % 32, h = lane / 32;
+  const float l = half_sum(st.l);
+  if (it.slot >= 0) {
+    const int64_t r = (int64_t(it.slot) * it.stride + tile_in_item) * 32 + n;
+    float* o = a.part + r * DP;
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        f32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = st.o[d][4 * b + i];
+        *reinterpret_cast<f32x4*>(o + 32 * d + 8 * b + 4 * h) = v;
+      }
+    if (h == 0) {
+      a.part_ml[2 * r] = st.m;
+      a.part_ml[2 * r + 1] = l;
+    }
+    return;
+  }
+  if (n >= tl.n) return;
+  const int row = tl.row0 + n, token = row / a.G, head = it.hk * a.G + row % a.G;
+  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  T* out = static_cast<T*>(a.out) + int64_t(token) * a.ldo;
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = st.o[d][4 * b + i] * inv;
+      scatter4(out, a.table, 32 * d + 8 * b + 4 * h, true, head, a.out_quad, v);
+    }
+  if (a.lse && h == 0)
+    a.lse[int64_t(token) * a.heads + head] = l > 0.0f || l != l ? (st.m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// Four waves with 32 query rows each share the keys through shared memory, the
+// next stage on its way while this one is worked on.
+template <typename T, int DP>
+__global__ __launch_bounds__(kThreads) void fwd_kernel(FwdArgs a) {
+  using D = Dims<T, DP>;
+  using Frag = typename Op<T>::Frag;
+  constexpr int KT = DP * int(sizeof(T)) <= 256 ? 2 : 1;  // key tiles a stage
+  constexpr int STAGE = 2 * KT * D::UNITS;                // 1 KB units: K tiles, then V tiles
+  constexpr int PER = STAGE / 4;                          // of a wave
+  __shared__ u32x4 sh[2][STAGE * 64];
+  __shared__ __attribute__((aligned(16))) float bias[2][KT * 32];
+  const Item it = a.items[blockIdx.x];
+  if (it.tiles == 0) return;
+  const int lane = int(threadIdx.x) % 64, wave = wave_id(), h = lane / 32;
+  const bool active = wave < it.tiles;
+  const Tile tl = a.qtiles[it.a0 + (active ? wave : 0)];
+  Frag q[D::KSTEPS];
+  load_queries<T, DP>(a, tl, it.hk, lane, q);
+  Running<D::DT> st;
+#pragma unroll
+  for (int d = 0; d < D::DT; ++d) st.o[d] = zero16();
+
+  const int stages = (it.b1 - it.b0 + KT - 1) / KT;
+  const auto fetch = [&](int s, int buf) {
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int u = k * 4 + wave, which = u / (KT * D::UNITS), rest = u % (KT * D::UNITS);
+      const int tile = min(it.b0 + s * KT + rest / D::UNITS, it.b1 - 1);
+      const T* base = static_cast<const T*>(which ? a.vf : a.kf) + (int64_t(tile) * a.groups + it.hk) * D::TILE;
+      copy_unit(base, rest % D::UNITS, lane, &sh[buf][u * 64]);
+    }
+    if (int(threadIdx.x) < KT * 32)
+      bias[buf][threadIdx.x] =
+          a.bias[int64_t(min(it.b0 + s * KT + int(threadIdx.x) / 32, it.b1 - 1)) * 32 + threadIdx.x % 32];
+  };
+  if (stages > 0) fetch(0, 0);
+  wait_copies();
+  __syncthreads();
+  for (int s = 0; s < stages; ++s) {
+    const int buf = s & 1;
+    if (s + 1 < stages) fetch(s + 1, buf ^ 1);
+    if (active) {
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        if (it.b0 + s * KT + k >= it.b1) break;
+        f32x16 sc = zero16();
+#pragma unroll
+        for (int t = 0; t < D::KSTEPS; ++t)
+          sc = Op<T>::mma(as_frag<Frag>(sh[buf][(k * D::UNITS + t) * 64 + lane]), q[t], sc);
+        fold_scores(st, sc, a.scale2, &bias[buf][k * 32], h);
+        Frag p[D::FR];
+#pragma unroll
+        for (int f = 0; f < D::FR; ++f) p[f] = Op<T>::from_acc(sc, f);
+#pragma unroll
+        for (int d = 0; d < D::DT; ++d)
+#pragma unroll
+          for (int f = 0; f < D::FR; ++f)
+            st.o[d] = Op<T>::mma(as_frag<Frag>(sh[buf][((KT + k) * D::UNITS + d * D::FR + f) * 64 + lane]), p[f],
+                                 st.o[d]);
+      }
+    }
+    wait_copies();
+    __syncthreads();
+  }
+  if (active) finish<T, DP>(a, it, tl, wave, lane, st);
+}
+
+// At most 32 query rows against a long context (single tokens): the four waves
+// take every fourth key tile, read straight into registers, and join.
+template <typename T, int DP>
+__global__ __launch_bounds__(kThreads) void fwd_few_kernel(FwdArgs a) {
+  using D = Dims<T, DP>;
+  using Frag = typename Op<T>::Frag;
+  __shared__ f32x4 sh[2][D::DT * 4 * 64];
+  __shared__ float ml[4][2][64];
+  const Item it = a.items[blockIdx.x];
+  if (it.tiles == 0) return;
+  const int lane = int(threadIdx.x) % 64, wave = wave_id(), h = lane / 32;
+  const Tile tl = a.qtiles[it.a0];
+  Frag q[D::KSTEPS];
+  load_queries<T, DP>(a, tl, it.hk, lane, q);
+  Running<D::DT> st;
+#pragma unroll
+  for (int d = 0; d < D::DT; ++d) st.o[d] = zero16();
+  for (int t = it.b0 + wave; t < it.b1; t += 4) {
+    const T* kf = static_cast<const T*>(a.kf) + (int64_t(t) * a.groups + it.hk) * D::TILE;
+    const T* vf = static_cast<const T*>(a.vf) + (int64_t(t) * a.groups + it.hk) * D::TILE;
+    f32x16 sc = zero16();
+    u32x4 v[D::UNITS];
+    if constexpr (D::kShort) {
+#pragma unroll
+      for (int u = 0; u < D::KSTEPS; ++u) {
+        sc = Op<T>::mma(as_frag<Frag>(unit16(kf, u, lane)), q[u], sc);
+        pace<T, DP>(u);
+      }
+    } else {
+      u32x4 k[D::UNITS];
+#pragma unroll
+      for (int u = 0; u < D::UNITS; ++u) k[u] = unit16(kf, u, lane);
+#pragma unroll
+      for (int u = 0; u < D::UNITS; ++u) v[u] = unit16(vf, u, lane);
+#pragma unroll
+      for (int u = 0; u < D::KSTEPS; ++u) sc = Op<T>::mma(as_frag<Frag>(k[u]), q[u], sc);
+    }
+    fold_scores(st, sc, a.scale2, a.bias + int64_t(t) * 32, h);
+    Frag p[D::FR];
+#pragma unroll
+    for (int f = 0; f < D::FR; ++f) p[f] = Op<T>::from_acc(sc, f);
+#pragma unroll
+    for (int d = 0; d < D::DT; ++d)
+#pragma unroll
+      for (int f = 0; f < D::FR; ++f) {
+        const int u = d * D::FR + f;
+        if constexpr (D::kShort) v[u] = unit16(vf, u, lane);
+        st.o[d] = Op<T>::mma(as_frag<Frag>(v[u]), p[f], st.o[d]);
+        pace<T, DP>(u);
+      }
+  }
+  // join: common reference, then waves 2, 3 into 0, 1 and 1 into 0
+  ml[wave][0][lane] = st.m;
+  __syncthreads();
+  float m = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) m = fmaxf(m, ml[w][0][lane]);
+  const float f = m == -INFINITY ? 1.0f : exp2_fast(st.m - m);
+  st.m = m;
+  st.l *= f;
+#pragma unroll
+  for (int d = 0; d < D::DT; ++d) st.o[d] *= f;
+  ml[wave][1][lane] = st.l;
+#pragma unroll
+  for (int round = 2; round >= 1; --round) {
+    // the upper `round` waves write, the lower ones add
+    if (wave >= round && wave < 2 * round)
+#pragma unroll
+      for (int d = 0; d < D::DT; ++d)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          f32x4 v;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = st.o[d][4 * b + i];
+          sh[wave - round][(d * 4 + b) * 64 + lane] = v;
+        }
+    __syncthreads();
+    if (wave < round)
+#pragma unroll
+      for (int d = 0; d < D::DT; ++d)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const f32x4 v = sh[wave][(d * 4 + b) * 64 + lane];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st.o[d][4 * b + i] += v[i];
+        }
+    __syncthreads();
+  }
+  if (wave == 0) {
+    st.l = ml[0][1][lane] + ml[2][1][lane] + (ml[1][1][lane] + ml[3][1][lane]);
+    finish<T, DP>(a, it, tl, 0, lane, st);
+  }
+}
+
+// Joins the parts of split rows: 8 threads a row.
+template <typename T, int DP>
+__global__ __launch_bounds__(kThreads) void fwd_join_kernel(FwdArgs a) {
+  const Join j = a.joins[blockIdx.x];
+  const Tile tl = a.qtiles[j.tile];
+  const int n = int(threadIdx.x) / 8, c = int(threadIdx.x) % 8;
+  if (n >= tl.n) return;
+  const auto at = [&](int k) { return (int64_t(j.slot + k) * j.stride + j.within) * 32 + n; };
+  float m = -INFINITY, l = 0.0f;
+  for (int k = 0; k < j.parts; ++k) m = fmaxf(m, a.part_ml[2 * at(k)]);
+  const float ref = m == -INFINITY ? 0.0f : m;
+  for (int k = 0; k < j.parts; ++k) l += a.part_ml[2 * at(k) + 1] * exp2_fast(a.part_ml[2 * at(k)] - ref);
+  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  const int row = tl.row0 + n, token = row / a.G, head = j.hk * a.G + row % a.G;
+  T* out = static_cast<T*>(a.out) + int64_t(token) * a.ldo;
+  for (int d = 4 * c; d < DP; d += 32) {
+    float v[4] = {0, 0, 0, 0};
+    for (int k = 0; k < j.parts; ++k) {
+      const float w = exp2_fast(a.part_ml[2 * at(k)] - ref);
+      const f32x4 o = *reinterpret_cast<const f32x4*>(a.part + at(k) * DP + d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += w * o[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] *= inv;
+    scatter4(out, a.table, d, true, head, a.out_quad, v);
+  }
+  if (a.lse && c == 0)
+    a.lse[int64_t(token) * a.heads + head] = l > 0.0f || l != l ? (ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// ------------------------------------------------------------------ backward
+
+// A wave's 32 x DP gradient (transposed accumulators): final rows or a part.
+template <typename T, int DP>
+__device__ __forceinline__ void finish_grad(const BwdArgs& a, const Item& it, const Tile& tl, int within, int lane,
+                                            bool query, void* dst, int64_t ld, float* part, bool quad,
+                                            const f32x16 (&g)[DP / 32], float scale) {
+  const int n = lane % 32, h = lane / 32;
+  if (it.slot >= 0) {
+    float* o = part + ((int64_t(it.slot) * it.stride + within) * 32 + n) * DP;
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        f32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = g[d][4 * b + i] * scale;
+        *reinterpret_cast<f32x4*>(o + 32 * d + 8 * b + 4 * h) = v;
+      }
+    return;
+  }
+  if (n >= tl.n) return;
+  const int row = tl.row0 + n, G = query ? a.G : 1, token = row / G, head = it.hk * G + row % G;
+  T* out = static_cast<T*>(dst) + int64_t(token) * ld;
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = g[d][4 * b + i] * scale;
+      scatter4(out, a.table, 32 * d + 8 * b + 4 * h, query, head, quad, v);
+    }
+}
+
+// grad_q: as the forward, a wave keeps 32 query rows and walks the key tiles:
+// S^T = K Q^T, P^T = exp2(S^T - lse), dP^T = V dO^T, dS^T = P^T (dP^T - delta),
+// dQ^T += K^T dS^T. Three packed forms of a tile pass through shared memory: K
+// rows, V rows, K columns.
+template <typename T, int DP>
+__global__ __launch_bounds__(kThreads) void dq_kernel(BwdArgs a) {
+  using D = Dims<T, DP>;
+  using Frag = typename Op<T>::Frag;
+  constexpr int STAGE = 3 * D::UNITS, PER = (STAGE + 3) / 4;
+  constexpr int BUFS = stage_buffers(STAGE);
+  __shared__ u32x4 sh[BUFS][STAGE * 64];
+  __shared__ __attribute__((aligned(16))) float bias[BUFS][32];
+  const Item it = a.items[blockIdx.x];
+  if (it.tiles == 0) return;
+  const int lane = int(threadIdx.x) % 64, wave = wave_id(), n = lane % 32, h = lane / 32;
+  const bool active = wave < it.tiles;
+  const int qt = it.a0 + (active ? wave : 0);
+  const Tile tl = a.qtiles[qt];
+  const int64_t qat = int64_t(qt) * a.groups + it.hk;
+  const T* const qrows = static_cast<const T*>(a.qr) + qat * D::TILE;
+  Frag q[D::kShort ? 1 : D::KSTEPS], g[D::KSTEPS];
+#pragma unroll
+  for (int t = 0; t < D::KSTEPS; ++t) {
+    if constexpr (!D::kShort) q[t] = as_frag<Frag>(unit16(qrows, t, lane));
+    g[t] = as_frag<Frag>(unit16(static_cast<const T*>(a.gr) + qat * D::TILE, t, lane));
+  }
+  const float lse2 = a.rows[qat * 64 + n], delta = a.rows[qat * 64 + 32 + n];
+  f32x16 dq[D::DT];
+#pragma unroll
+  for (int d = 0; d < D::DT; ++d) dq[d] = zero16();
+
+  const auto fetch = [&](int tile, int buf) {
+    const int64_t at = (int64_t(tile) * a.groups + it.hk) * D::TILE;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int u = k * 4 + wave, which = u / D::UNITS;
+      if (u >= STAGE) break;
+      const T* base = static_cast<const T*>(which == 0 ? a.kr : which == 1 ? a.vr : a.kc);
+      copy_unit(base + at, u % D::UNITS, lane, &sh[buf][u * 64]);
+    }
+    if (threadIdx.x < 32) bias[buf][threadIdx.x] = a.bias[int64_t(tile) * 32 + threadIdx.x];
+  };
+  if (it.b0 < it.b1) fetch(it.b0, 0);
+  wait_copies();
+  __syncthreads();
+  for (int t = it.b0; t < it.b1; ++t) {
+    const int buf = BUFS == 2 ? (t - it.b0) & 1 : 0;
+    if (BUFS == 2 && t + 1 < it.b1) fetch(t + 1, buf ^ 1);
+    if (active) {
+      f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+      for (int u = 0; u < D::KSTEPS; ++u) {
+        const Frag qu = D::kShort ? as_frag<Frag>(unit16(qrows, u, lane)) : q[D::kShort ? 0 : u];
+        s = Op<T>::mma(as_frag<Frag>(sh[buf][u * 64 + lane]), qu, s);
+        dp = Op<T>::mma(as_frag<Frag>(sh[buf][(D::UNITS + u) * 64 + lane]), g[u], dp);
+        pace<T, DP>(u);
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const f32x4 bv = *reinterpret_cast<const f32x4*>(&bias[buf][8 * b + 4 * h]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p = exp2_fast(fmaf(s[4 * b + i], a.scale2, bv[i]) - lse2);
+          s[4 * b + i] = p * (dp[4 * b + i] - delta);
+        }
+      }
+      Frag ds[D::FR];
+#pragma unroll
+      for (int f = 0; f < D::FR; ++f) ds[f] = Op<T>::from_acc(s, f);
+#pragma unroll
+      for (int d = 0; d < D::DT; ++d)
+#pragma unroll
+        for (int f = 0; f < D::FR; ++f) {
+          dq[d] = Op<T>::mma(as_frag<Frag>(sh[buf][(2 * D::UNITS + d * D::FR + f) * 64 + lane]), ds[f], dq[d]);
+          pace<T, DP>(f);
+        }
+    }
+    if (BUFS == 1) {
+      __syncthreads();
+      if (t + 1 < it.b1) fetch(t + 1, 0);
+    }
+    wait_copies();
+    __syncthreads();
+  }
+  if (active)
+    finish_grad<T, DP>(a, it, tl, wave, lane, true, a.dq, a.ldq, a.part, a.q_quad, dq, a.scale);
+}
+
+// grad_k and grad_v: a wave keeps 32 keys and walks the query tiles (all heads
+// of the group): S = Q K^T, P = exp2(S - lse), dV^T += dO^T P, dP = dO V^T,
+// dS = P (dP - delta), dK^T += Q^T dS. PART 0: both; heads whose operands and
+// accumulators do not fit the registers run it as PART 1 (grad_v) and 2 (grad_k).
+template <typename T, int DP, int PART>
+__global__ __launch_bounds__(kThreads) void dkv_kernel(BwdArgs a) {
+  using D = Dims<T, DP>;
+  using Frag = typename Op<T>::Frag;
+  constexpr bool WANT_V = PART != 2, WANT_K = PART != 1;
+  // Q rows, dO columns [grad_v], dO rows and Q columns [grad_k]
+  constexpr int FORMS = 1 + (WANT_V ? 1 : 0) + (WANT_K ? 2 : 0);
+  constexpr int GC = 1, GR = WANT_V ? 2 : 1, QC = GR + 1;
+  constexpr int STAGE = FORMS * D::UNITS, PER = (STAGE + 3) / 4;
+  constexpr int BUFS = stage_buffers(STAGE);
+  __shared__ u32x4 sh[BUFS][STAGE * 64];
+  __shared__ __attribute__((aligned(16))) float rows[BUFS][64];
+  const Item it = a.items[blockIdx.x];
+  if (it.tiles == 0) return;
+  const int lane = int(threadIdx.x) % 64, wave = wave_id(), n = lane % 32, h = lane / 32;
+  const bool active = wave < it.tiles;
+  const int kt = it.a0 + (active ? wave : 0);
+  const Tile tl = a.ktiles[kt];
+  const int64_t kat = (int64_t(kt) * a.groups + it.hk) * D::TILE;
+  constexpr bool kReread = D::kShort && WANT_K;
+  const T* const krows = static_cast<const T*>(a.kr) + kat;
+  Frag k[kReread ? 1 : D::KSTEPS], v[WANT_K ? D::KSTEPS : 1];
+#pragma unroll
+  for (int t = 0; t < D::KSTEPS; ++t) {
+    if constexpr (!kReread) k[t] = as_frag<Frag>(unit16(krows, t, lane));
+    if (WANT_K) v[t] = as_frag<Frag>(unit16(static_cast<const T*>(a.vr) + kat, t, lane));
+  }
+  const float bias = a.bias[int64_t(kt) * 32 + n];
+  f32x16 dk[WANT_K ? D::DT : 1], dv[WANT_V ? D::DT : 1];
+#pragma unroll
+  for (int d = 0; d < D::DT; ++d) {
+    if (WANT_K) dk[d] = zero16();
+    if (WANT_V) dv[d] = zero16();
+  }
+  const auto fetch = [&](int tile, int buf) {
+    const int64_t at = int64_t(tile) * a.groups + it.hk;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int u = i * 4 + wave, which = u / D::UNITS;
+      if (u >= STAGE) break;
+      const void* base = which == 0 ? a.qr : (WANT_V && which == GC) ? a.gc : which == GR ? a.gr : a.qc;
+      copy_unit(static_cast<const T*>(base) + at * D::TILE, u % D::UNITS, lane, &sh[buf][u * 64]);
+    }
+    if (threadIdx.x < 64) rows[buf][threadIdx.x] = a.rows[at * 64 + threadIdx.x];
+  };
+  if (it.b0 < it.b1) fetch(it.b0, 0);
+  wait_copies();
+  __syncthreads();
+  for (int t = it.b0; t < it.b1; ++t) {
+    const int buf = BUFS == 2 ? (t - it.b0) & 1 : 0;
+    if (BUFS == 2 && t + 1 < it.b1) fetch(t + 1, buf ^ 1);
+    if (active) {
+      f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+      for (int u = 0; u < D::KSTEPS; ++u) {
+        const Frag ku = kReread ? as_frag<Frag>(unit16(krows, u, lane)) : k[kReread ? 0 : u];
+        s = Op<T>::mma(as_frag<Frag>(sh[buf][u * 64 + lane]), ku, s);
+        if (WANT_K) dp = Op<T>::mma(as_frag<Frag>(sh[buf][(GR * D::UNITS + u) * 64 + lane]), v[u], dp);
+        pace<T, DP>(u);
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const f32x4 l2 = *reinterpret_cast<const f32x4*>(&rows[buf][8 * b + 4 * h]);
+        const f32x4 de = *reinterpret_cast<const f32x4*>(&rows[buf][32 + 8 * b + 4 * h]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[4 * b + i] = exp2_fast(fmaf(s[4 * b + i], a.scale2, bias) - l2[i]);
+          if (WANT_K) dp[4 * b + i] = s[4 * b + i] * (dp[4 * b + i] - de[i]);
+        }
+      }
+      Frag p[D::FR], ds[D::FR];
+#pragma unroll
+      for (int f = 0; f < D::FR; ++f) {
+        if (WANT_V) p[f] = Op<T>::from_acc(s, f);
+        if (WANT_K) ds[f] = Op<T>::from_acc(dp, f);
+      }
+#pragma unroll
+      for (int d = 0; d < D::DT; ++d)
+#pragma unroll
+        for (int f = 0; f < D::FR; ++f) {
+          if (WANT_V)
+            dv[d] = Op<T>::mma(as_frag<Frag>(sh[buf][(GC * D::UNITS + d * D::FR + f) * 64 + lane]), p[f], dv[d]);
+          if (WANT_K)
+            dk[d] = Op<T>::mma(as_frag<Frag>(sh[buf][(QC * D::UNITS + d * D::FR + f) * 64 + lane]), ds[f], dk[d]);
+          pace<T, DP>(f);
+        }
+    }
+    if (BUFS == 1) {
+      __syncthreads();
+      if (t + 1 < it.b1) fetch(t + 1, 0);
+    }
+    wait_copies();
+    __syncthreads();
+  }
+  if (!active) return;
+  if constexpr (WANT_V)
+    if (a.dv) finish_grad<T, DP>(a, it, tl, wave, lane, false, a.dv, a.ldk, a.part_v, a.k_quad, dv, 1.0f);
+  if constexpr (WANT_K)
+    if (a.dk) finish_grad<T, DP>(a, it, tl, wave, lane, false, a.dk, a.ldk, a.part, a.k_quad, dk, a.scale);
+}
+
+// Adds the parts of split gradient rows in order: 8 threads a row.
+template <typename T, int DP>
+__global__ __launch_bounds__(kThreads) void grad_join_kernel(BwdArgs a, bool query, const float* part, void* dst,
+                                                             int64_t ld, bool quad) {
+  const Join j = a.joins[blockIdx.x];
+  const Tile tl = query ? a.qtiles[j.tile] : a.ktiles[j.tile];
+  const int n = int(threadIdx.x) / 8, c = int(threadIdx.x) % 8;
+  if (n >= tl.n) return;
+  const int row = tl.row0 + n, G = query ? a.G : 1, token = row / G, head = j.hk * G + row % G;
+  T* out = static_cast<T*>(dst) + int64_t(token) * ld;
+  for (int d = 4 * c; d < DP; d += 32) {
+    float v[4] = {0, 0, 0, 0};
+    for (int k = 0; k < j.parts; ++k) {
+      const f32x4 o =
+          *reinterpret_cast<const f32x4*>(part + ((int64_t(j.slot + k) * j.stride + j.within) * 32 + n) * DP + d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += o[i];
+    }
+    scatter4(out, a.table, d, query, head, quad, v);
+  }
+}
+
+// -------------------------------------------------------------------- launch
+
+template <typename T, int DP>
+struct Kernels {
+  // whether both gradients of the keys fit the 512 registers of a lane in one
+  // pass: two accumulators and two operands (measured: no spills up to 160)
+  static constexpr bool kOnePass = DP <= 160;
+
+  static void pack(const PackArgs& a, int tiles, int tensors, hipStream_t s) {
+    hipLaunchKernelGGL((pack_kernel<T, DP>), dim3(unsigned(tiles), unsigned(a.groups), unsigned(tensors)),
+                       dim3(kThreads), 0, s, a);
+  }
+  static void fwd(const FwdArgs& a, int items, bool few, hipStream_t s) {
+    if (few) hipLaunchKernelGGL((fwd_few_kernel<T, DP>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL((fwd_kernel<T, DP>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
+  }
+  static void fwd_join(const FwdArgs& a, int joins, hipStream_t s) {
+    hipLaunchKernelGGL((fwd_join_kernel<T, DP>), dim3(unsigned(joins)), dim3(kThreads), 0, s, a);
+  }
+  static void dq(const BwdArgs& a, int items, hipStream_t s) {
+    hipLaunchKernelGGL((dq_kernel<T, DP>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
+  }
+  static void dkv(const BwdArgs& a, int items, hipStream_t s) {
+    if constexpr (kOnePass) {
+      hipLaunchKernelGGL((dkv_kernel<T, DP, 0>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
+    } else {
+      if (a.dv) hipLaunchKernelGGL((dkv_kernel<T, DP, 1>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
+      if (a.dk) hipLaunchKernelGGL((dkv_kernel<T, DP, 2>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
+    }
+  }
+  static void grad_join(const BwdArgs& a, int joins, bool query, const float* part, void* dst, int64_t ld, bool quad,
+                        hipStream_t s) {
+    hipLaunchKernelGGL((grad_join_kernel<T, DP>), dim3(unsigned(joins)), dim3(kThreads), 0, s, a, query, part, dst, ld,
+                       quad);
+  }
+  static KernelTable table() { return {pack, fwd, fwd_join, dq, dkv, grad_join}; }
+};
+
+}  // namespace attn
+}  // namespace cgtp

@@ -4,8 +4,8 @@
 #include <cmath>
 #include <cstring>
 
+#include "attn.hpp"
 #include "guard.hpp"
-#include "layers.hpp"
 
 namespace cgtp {
 
@@ -71,6 +71,17 @@ void need_ws(const void* ws, size_t have, size_t want, const char* what) {
   if (!ws || have < want)
     throw Error{CGTP_ERR_WORKSPACE, std::string(what) + " needs " + std::to_string(want) + " workspace bytes"};
   need(reinterpret_cast<uintptr_t>(ws) % 16 == 0, "the workspace must be 16-byte aligned");
+}
+
+void need_rows(int64_t rows, const void* p, int64_t ld, int64_t dim, const char* name) {
+  if (ld < dim) throw Error{CGTP_ERR_INVALID_ARG, std::string(name) + ": row stride below the row size"};
+  if (rows > 0 && !p) throw Error{CGTP_ERR_INVALID_ARG, std::string(name) + " is NULL"};
+}
+
+void need_batch(const cgtp_attn_batch_s* b, double scale) {
+  need(b != nullptr, "batch is NULL");
+  need(std::isfinite(scale), "scale must be finite");
+  need_device(b->device, "the batch");
 }
 
 // Rows in a run of the norm: long enough that a workgroup's work outweighs its
@@ -267,6 +278,115 @@ cgtp_status cgtp_dropout_forward(cgtp_dropout drop, int64_t B, const void* x, do
 cgtp_status cgtp_dropout_backward(cgtp_dropout drop, int64_t B, const void* grad_y, double p, uint64_t seed,
                                   uint32_t offset, void* grad_x, void* stream) {
   return cgtp_dropout_forward(drop, B, grad_y, p, seed, offset, nullptr, grad_x, stream);
+}
+
+cgtp_status cgtp_attn_create(const char* irreps, int64_t heads, int64_t kv_heads, cgtp_dtype dtype, cgtp_attn* out) {
+  return guarded([&] {
+    need(out != nullptr, "out handle is NULL");
+    *out = nullptr;
+    *out = build_attn(irreps, heads, kv_heads, dtype);
+  });
+}
+
+cgtp_status cgtp_attn_destroy(cgtp_attn attn) {
+  return guarded([&] { delete attn; });
+}
+
+cgtp_status cgtp_attn_query(cgtp_attn attn, int64_t* dim_q, int64_t* dim_kv, int64_t* head_dim) {
+  return guarded([&] {
+    need(attn != nullptr, "attn is NULL");
+    if (dim_q) *dim_q = attn->qrow.dim;
+    if (dim_kv) *dim_kv = attn->krow.dim;
+    if (head_dim) *head_dim = attn->D;
+  });
+}
+
+cgtp_status cgtp_attn_batch_create(cgtp_attn attn, cgtp_samples queries, cgtp_samples context, cgtp_attn_batch* out) {
+  return guarded([&] {
+    need(out != nullptr, "out handle is NULL");
+    *out = nullptr;
+    need(attn != nullptr && queries != nullptr && context != nullptr, "NULL handle");
+    need_device(attn->device, "the attention");
+    *out = build_attn_batch(attn, queries, context);
+  });
+}
+
+cgtp_status cgtp_attn_batch_destroy(cgtp_attn_batch batch) {
+  return guarded([&] { delete batch; });
+}
+
+cgtp_status cgtp_attn_workspace_size(cgtp_attn_batch batch, int op, size_t* bytes) {
+  return guarded([&] {
+    need(batch != nullptr && bytes != nullptr, "NULL argument");
+    switch (op) {
+      case CGTP_ATTN_FORWARD: *bytes = attn_forward_ws_bytes(batch, false); break;
+      case CGTP_ATTN_BACKWARD: *bytes = attn_backward_ws_bytes(batch); break;
+      case CGTP_ATTN_CONTEXT: *bytes = attn_context_bytes(batch); break;
+      case CGTP_ATTN_FORWARD_PACKED: *bytes = attn_forward_ws_bytes(batch, true); break;
+      default: throw Error{CGTP_ERR_INVALID_ARG, "unknown op"};
+    }
+  });
+}
+
+cgtp_status cgtp_attn_forward(cgtp_attn_batch batch, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                              const void* v, int64_t ldv, const uint8_t* key_mask, double scale, void* out, float* lse,
+                              void* ws, size_t ws_bytes, void* stream) {
+  return guarded([&] {
+    need_batch(batch, scale);
+    need_rows(batch->nq, q, ldq, batch->attn->qrow.dim, "q");
+    need_rows(batch->nk, k, ldk, batch->attn->krow.dim, "k");
+    need_rows(batch->nk, v, ldv, batch->attn->krow.dim, "v");
+    if (batch->nq == 0) return;
+    need(out != nullptr, "out is NULL");
+    need_ws(ws, ws_bytes, attn_forward_ws_bytes(batch, false), "attention forward");
+    // the partial results, then the packed context
+    void* context = static_cast<char*>(ws) + attn_forward_ws_bytes(batch, true);
+    attn_pack_launch(batch, {k, ldk}, {v, ldv}, key_mask, context, as_stream(stream));
+    attn_forward_launch(batch, {q, ldq}, context, scale, out, lse, ws, as_stream(stream));
+  });
+}
+
+cgtp_status cgtp_attn_pack(cgtp_attn_batch batch, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                           const uint8_t* key_mask, void* context, size_t context_bytes, void* stream) {
+  return guarded([&] {
+    need_batch(batch, 1.0);
+    need_rows(batch->nk, k, ldk, batch->attn->krow.dim, "k");
+    need_rows(batch->nk, v, ldv, batch->attn->krow.dim, "v");
+    need_ws(context, context_bytes, attn_context_bytes(batch), "the packed context");
+    attn_pack_launch(batch, {k, ldk}, {v, ldv}, key_mask, context, as_stream(stream));
+  });
+}
+
+cgtp_status cgtp_attn_forward_packed(cgtp_attn_batch batch, const void* q, int64_t ldq, const void* context,
+                                     size_t context_bytes, double scale, void* out, float* lse, void* ws,
+                                     size_t ws_bytes, void* stream) {
+  return guarded([&] {
+    need_batch(batch, scale);
+    need_rows(batch->nq, q, ldq, batch->attn->qrow.dim, "q");
+    need_ws(context, context_bytes, attn_context_bytes(batch), "the packed context");
+    if (batch->nq == 0) return;
+    need(out != nullptr, "out is NULL");
+    need_ws(ws, ws_bytes, attn_forward_ws_bytes(batch, true), "attention forward");
+    attn_forward_launch(batch, {q, ldq}, context, scale, out, lse, ws, as_stream(stream));
+  });
+}
+
+cgtp_status cgtp_attn_backward(cgtp_attn_batch batch, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                               const void* v, int64_t ldv, const uint8_t* key_mask, double scale, const void* out,
+                               const float* lse, const void* grad_out, int64_t ldg, void* grad_q, void* grad_k,
+                               void* grad_v, void* ws, size_t ws_bytes, void* stream) {
+  return guarded([&] {
+    need_batch(batch, scale);
+    need_rows(batch->nq, q, ldq, batch->attn->qrow.dim, "q");
+    need_rows(batch->nk, k, ldk, batch->attn->krow.dim, "k");
+    need_rows(batch->nk, v, ldv, batch->attn->krow.dim, "v");
+    need_rows(batch->nq, grad_out, ldg, batch->attn->qrow.dim, "grad_out");
+    need(batch->nq == 0 || (out && lse), "NULL out or lse");
+    if (!grad_q && !grad_k && !grad_v) return;
+    need_ws(ws, ws_bytes, attn_backward_ws_bytes(batch), "attention backward");
+    attn_backward_launch(batch, {q, ldq}, {k, ldk}, {v, ldv}, key_mask, scale, out, lse, {grad_out, ldg}, grad_q,
+                         grad_k, grad_v, ws, as_stream(stream));
+  });
 }
 
 }  // extern "C"

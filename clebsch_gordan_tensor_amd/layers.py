@@ -31,6 +31,17 @@ _SIGS = {
     "cgtp_dropout_query": [_vp, _i64p],
     "cgtp_dropout_forward": [_vp, _i64, _vp, _dbl, _u64, _u32, _vp, _vp, _vp],
     "cgtp_dropout_backward": [_vp, _i64, _vp, _dbl, _u64, _u32, _vp, _vp],
+    "cgtp_attn_create": [ctypes.c_char_p, _i64, _i64, ctypes.c_int, _vpp],
+    "cgtp_attn_destroy": [_vp],
+    "cgtp_attn_query": [_vp, _i64p, _i64p, _i64p],
+    "cgtp_attn_batch_create": [_vp, _vp, _vp, _vpp],
+    "cgtp_attn_batch_destroy": [_vp],
+    "cgtp_attn_workspace_size": [_vp, ctypes.c_int, _sizep],
+    "cgtp_attn_forward": [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _dbl, _vp, _vp, _vp, _size, _vp],
+    "cgtp_attn_pack": [_vp, _vp, _i64, _vp, _i64, _vp, _vp, _size, _vp],
+    "cgtp_attn_forward_packed": [_vp, _vp, _i64, _vp, _size, _dbl, _vp, _vp, _vp, _size, _vp],
+    "cgtp_attn_backward": [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _dbl, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp,
+                           _size, _vp],
 }
 for _name, _args in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -209,3 +220,153 @@ class Dropout(_Handle):
         _check(_lib.cgtp_dropout_backward(self._h, grad_y.shape[0], _ptr(grad_y), float(p), seed, offset, _ptr(out),
                                           _stream(grad_y)), "cgtp_dropout_backward")
         return out
+
+
+ATTN_FORWARD, ATTN_BACKWARD, ATTN_CONTEXT, ATTN_FORWARD_PACKED = 1, 2, 3, 4
+
+
+class AttentionBatch(_Handle):
+    """The work lists of one pair of sample layouts (cgtp_attn_batch_create);
+    made by CrossAttention.batch, reusable for every call on these layouts."""
+
+    def __init__(self, attn, queries, context):
+        self.attn, self.nq, self.nk = attn, queries.rows, context.rows     # attn outlives the handle
+        h = _vp()
+        _check(_lib.cgtp_attn_batch_create(attn._h, queries._h, context._h, ctypes.byref(h)),
+               "cgtp_attn_batch_create")
+        self._own(h, "cgtp_attn_batch_destroy")
+        self._sizes = {}
+
+    def workspace_size(self, op):
+        if op not in self._sizes:
+            n = _size()
+            _check(_lib.cgtp_attn_workspace_size(self._h, op, ctypes.byref(n)), "cgtp_attn_workspace_size")
+            self._sizes[op] = n.value
+        return self._sizes[op]
+
+
+class CrossAttention(_Handle):
+    """Attention of irreps rows to a context of another length, sample by sample
+    (cgtp_attn_create). ``irreps`` are the queries'; the context's have
+    multiplicities kv_heads / heads as large (``dim_kv`` elements a row). q, k, v
+    and grad_out may be slices of wider rows (unit stride within a row)."""
+
+    def __init__(self, irreps, heads, kv_heads=None, dtype="f32"):
+        self.irreps, self.heads = irreps, int(heads)
+        self.kv_heads = self.heads if kv_heads is None else int(kv_heads)
+        self.dtype_code = _DT[dtype]
+        h = _vp()
+        _check(_lib.cgtp_attn_create(irreps.encode(), self.heads, self.kv_heads, self.dtype_code, ctypes.byref(h)),
+               "cgtp_attn_create")
+        self._own(h, "cgtp_attn_destroy")
+        v = [_i64() for _ in range(3)]
+        _check(_lib.cgtp_attn_query(h, *[ctypes.byref(a) for a in v]), "cgtp_attn_query")
+        self.dim_q, self.dim_kv, self.head_dim = (a.value for a in v)
+        self.scale = self.head_dim ** -0.5
+
+    @property
+    def torch_dtype(self):
+        return _torch_dtype(self.dtype_code)
+
+    def batch(self, queries, context):
+        return AttentionBatch(self, queries, context)
+
+    def _rows(self, t, rows, dim, name):
+        """(pointer, row stride) of rows with unit stride inside a row."""
+        if t is None:
+            raise ValueError("%s is required" % name)
+        if not t.is_cuda:
+            raise ValueError("%s must be a device tensor" % name)
+        if tuple(t.shape) != (rows, dim):
+            raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (rows, dim)))
+        if t.dtype != self.torch_dtype:
+            raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, self.torch_dtype))
+        ld = t.stride(0) if rows > 1 else dim
+        if (dim > 1 and t.stride(1) != 1) or ld < dim:
+            raise ValueError("%s must have unit stride within its rows, which may not overlap" % name)
+        return _ptr(t), ld
+
+    def _mask(self, m, rows):
+        if m is None:
+            return _vp(0)
+        torch = _torch()
+        if m.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("key_mask must be bool or uint8")
+        return _ptr(_need(m, (rows,), m.dtype, "key_mask"))
+
+    def _batch(self, batch):
+        if batch.attn is not self:
+            raise ValueError("the batch belongs to another CrossAttention")
+
+    def _outputs(self, batch, q, out, lse, need_lse):
+        torch = _torch()
+        if out is None:
+            out = torch.empty((batch.nq, self.dim_q), dtype=self.torch_dtype, device=q.device)
+        _need(out, (batch.nq, self.dim_q), self.torch_dtype, "out")
+        if need_lse and lse is None:
+            lse = torch.empty((batch.nq, self.heads), dtype=torch.float32, device=q.device)
+        if lse is not None:
+            _need(lse, (batch.nq, self.heads), torch.float32, "lse")
+        return out, lse
+
+    def forward(self, batch, q, k, v, scale=None, key_mask=None, need_lse=False, out=None, lse=None, ws=None):
+        """out, or (out, lse) with ``need_lse``; scale defaults to head_dim ** -0.5."""
+        self._batch(batch)
+        pq, ldq = self._rows(q, batch.nq, self.dim_q, "q")
+        pk, ldk = self._rows(k, batch.nk, self.dim_kv, "k")
+        pv, ldv = self._rows(v, batch.nk, self.dim_kv, "v")
+        mask = self._mask(key_mask, batch.nk)
+        out, lse = self._outputs(batch, q, out, lse, need_lse)
+        ws, nws = _workspace(ws, batch.workspace_size(ATTN_FORWARD), q.device)
+        _check(_lib.cgtp_attn_forward(batch._h, pq, ldq, pk, ldk, pv, ldv, mask,
+                                      self.scale if scale is None else float(scale), _ptr(out), _ptr(lse), _ptr(ws),
+                                      nws, _stream(q)), "cgtp_attn_forward")
+        return (out, lse) if need_lse else out
+
+    def pack(self, batch, k, v, key_mask=None, out=None):
+        """The context laid out once for any number of forward_packed calls (a uint8 tensor)."""
+        self._batch(batch)
+        pk, ldk = self._rows(k, batch.nk, self.dim_kv, "k")
+        pv, ldv = self._rows(v, batch.nk, self.dim_kv, "v")
+        mask = self._mask(key_mask, batch.nk)
+        out, n = _workspace(out, batch.workspace_size(ATTN_CONTEXT), k.device)
+        _check(_lib.cgtp_attn_pack(batch._h, pk, ldk, pv, ldv, mask, _ptr(out), n, _stream(k)), "cgtp_attn_pack")
+        return out
+
+    def forward_packed(self, batch, q, context, scale=None, need_lse=False, out=None, lse=None, ws=None):
+        """forward on a packed context (of this batch or one with the same context samples)."""
+        self._batch(batch)
+        pq, ldq = self._rows(q, batch.nq, self.dim_q, "q")
+        out, lse = self._outputs(batch, q, out, lse, need_lse)
+        ws, nws = _workspace(ws, batch.workspace_size(ATTN_FORWARD_PACKED), q.device)
+        _check(_lib.cgtp_attn_forward_packed(batch._h, pq, ldq, _ptr(context), _ws_bytes(context),
+                                             self.scale if scale is None else float(scale), _ptr(out), _ptr(lse),
+                                             _ptr(ws), nws, _stream(q)), "cgtp_attn_forward_packed")
+        return (out, lse) if need_lse else out
+
+    def backward(self, batch, q, k, v, out, lse, grad_out, scale=None, key_mask=None, need=(True, True, True),
+                 grads=(None, None, None), ws=None):
+        """(grad_q, grad_k, grad_v) from the forward's out and lse."""
+        torch = _torch()
+        self._batch(batch)
+        dt = self.torch_dtype
+        pq, ldq = self._rows(q, batch.nq, self.dim_q, "q")
+        pk, ldk = self._rows(k, batch.nk, self.dim_kv, "k")
+        pv, ldv = self._rows(v, batch.nk, self.dim_kv, "v")
+        pg, ldg = self._rows(grad_out, batch.nq, self.dim_q, "grad_out")
+        mask = self._mask(key_mask, batch.nk)
+        _need(out, (batch.nq, self.dim_q), dt, "out")
+        _need(lse, (batch.nq, self.heads), torch.float32, "lse")
+        shapes = [(batch.nq, self.dim_q), (batch.nk, self.dim_kv), (batch.nk, self.dim_kv)]
+        res = []
+        for i in range(3):
+            if not need[i]:
+                res.append(None)
+                continue
+            t = grads[i] if grads[i] is not None else torch.empty(shapes[i], dtype=dt, device=q.device)
+            res.append(_need(t, shapes[i], dt, "grad"))
+        ws, nws = _workspace(ws, batch.workspace_size(ATTN_BACKWARD), q.device)
+        _check(_lib.cgtp_attn_backward(batch._h, pq, ldq, pk, ldk, pv, ldv, mask,
+                                       self.scale if scale is None else float(scale), _ptr(out), _ptr(lse), pg, ldg,
+                                       *[_ptr(t) for t in res], _ptr(ws), nws, _stream(q)), "cgtp_attn_backward")
+        return tuple(res)
