@@ -33,6 +33,7 @@ struct PackTensor {
   void *row_frags, *col_frags;  // either may be NULL
   float* rows_out;              // gradient rows: lse and delta (else NULL)
   float* bias;                  // context: 0 or -inf for every key (one tensor of a call)
+  int32_t* flags;               // context: whether a tile has a masked or missing key
   bool vec;                     // 16-byte gathers
 };
 
@@ -55,10 +56,12 @@ struct FwdArgs {
   const int4* table;
   const void *q, *kf, *vf;
   const float* bias;
+  const int32_t* flags;
   void* out;
   float *lse, *part, *part_ml;
   int64_t ldq, ldo;
-  float scale2;  // scale log2 e
+  float scale2;     // |scale| log2 e
+  uint32_t q_sign;  // flips the queries' signs where the scale is negative
   int G, heads, groups;
   bool q_vec, out_quad;
 };
@@ -80,7 +83,7 @@ struct BwdArgs {
 
 struct KernelTable {
   void (*pack)(const PackArgs&, int tiles, int tensors, hipStream_t);
-  void (*fwd)(const FwdArgs&, int items, bool few, hipStream_t);
+  void (*fwd)(const FwdArgs&, int items, int tiles, hipStream_t);  // items of up to 1, 4 or 8 tiles
   void (*fwd_join)(const FwdArgs&, int joins, hipStream_t);
   void (*dq)(const BwdArgs&, int items, hipStream_t);
   void (*dkv)(const BwdArgs&, int items, hipStream_t);  // grad_k and grad_v, each unless NULL
@@ -91,6 +94,10 @@ struct KernelTable {
 // Kernels of a padded head size (a multiple of 32 up to 256); inst/attn_*.hip.
 KernelTable kernels_f32(int dp);
 KernelTable kernels_bf16(int dp);
+
+// Whether the forward has a form of 64 query rows a wave (8 tiles an item): its
+// operands and accumulators fit the registers.
+constexpr bool wide_forward(int dp, size_t size) { return size == 2 && dp <= 96; }
 
 // A list of work items on the device with the joins of its splits.
 struct WorkList {
@@ -118,7 +125,8 @@ struct cgtp_attn_batch_s {
   int64_t qtiles = 0, ktiles = 0;
   int device = 0;
   cgtp::DevMem qtile_mem, ktile_mem;
-  cgtp::attn::WorkList fwd, few, dq, dkv;
+  cgtp::attn::WorkList few, fwd, wide;  // forward, items of up to 1, 4 and 8 query tiles
+  cgtp::attn::WorkList dq, dkv;
 };
 
 namespace cgtp {

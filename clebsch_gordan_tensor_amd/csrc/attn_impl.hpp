@@ -21,6 +21,8 @@
 // 1 KB runs and never see a masked value.
 #pragma once
 
+#include <type_traits>
+
 #include "attn.hpp"
 #include "device_util.hpp"
 
@@ -33,6 +35,15 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;  // 4 waves
+
+// The kernels ask for two waves a SIMD, i.e. at most 256 registers a lane: their
+// accumulators then sit in ordinary registers, where with a budget of 512 the
+// compiler keeps them in the accumulation file and moves them to and fro for
+// every vector operation (the forward of a head of 128 took 1.3 times as long).
+// The heads whose whole tiles do not fit 256 registers take one wave.
+constexpr int few_waves(int dp, size_t size) { return dp * int(size) <= (size == 2 ? 384 : 512) ? 2 : 1; }
+// two workgroups a compute unit, where its 160 KB of shared memory hold `units` KB twice
+constexpr int lds_waves(int units) { return units < 80 ? 2 : 1; }
 
 // Matrix operands: 16 bytes a lane.
 template <typename T>
@@ -227,9 +238,12 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
       p.rows_out[at * 64 + tid] = tid < tl.n && l > -INFINITY ? l * 1.44269504088896341f : INFINITY;
       p.rows_out[at * 64 + 32 + tid] = d;
     }
-    if (p.bias && hk == 0)
-      p.bias[int64_t(tile) * 32 + tid] =
-          tid < tl.n && (a.mask == nullptr || a.mask[tl.row0 + tid] != 0) ? 0.0f : -INFINITY;
+    if (p.bias && hk == 0) {
+      const bool seen = tid < tl.n && (a.mask == nullptr || a.mask[tl.row0 + tid] != 0);
+      p.bias[int64_t(tile) * 32 + tid] = seen ? 0.0f : -INFINITY;
+      const bool some = __any(!seen);
+      if (p.flags && tid == 0) p.flags[tile] = some;
+    }
   }
   const int lane = tid % 64, wave = tid / 64, n = lane % 32, h = lane / 32;
   if (p.row_frags) {
@@ -256,31 +270,24 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
 
 // ------------------------------------------------------------------- forward
 
-// Running softmax of one wave's 32 queries: a lane holds its query's reference
-// m (log2 domain), its own keys' sum l and O^T.
+// Running softmax of 32 queries: a lane holds its query's reference m (log2
+// domain), its own keys' sum l and O^T.
 template <int DT>
 struct Running {
   float m = -INFINITY, l = 0.0f;
   f32x16 o[DT];
 };
 
-// Folds a tile's scores into the running state and leaves exp2(s - m) in s. The
-// reference follows the maximum only when that grows by more than 2^8: the
-// weights stay below 2^8 (exact enough in either type, their sum is fp32), and
-// most tiles need no rescaling of O.
+// Turns a tile's products q.k into weights exp2(scale2 q.k - m). The reference
+// follows the maximum only when that grows by more than 2^8: the weights stay
+// below 2^8 (their sum is fp32), and most tiles need no rescaling of O. scale2 is
+// positive, so the maximum is taken before scaling.
 template <int DT>
-__device__ __forceinline__ void fold_scores(Running<DT>& st, f32x16& s, float scale2, const float* bias, int h) {
-  float mx = -INFINITY;
+__device__ __forceinline__ void fold_scores(Running<DT>& st, f32x16& s, float scale2) {
+  float mx = s[0];
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const f32x4 bv = *reinterpret_cast<const f32x4*>(bias + 8 * b + 4 * h);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s[4 * b + i] = fmaf(s[4 * b + i], scale2, bv[i]);
-      mx = fmaxf(mx, s[4 * b + i]);
-    }
-  }
-  mx = half_max(mx);
+  for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
+  mx = half_max(mx) * scale2;
   if (__any(mx > st.m + 8.0f)) {
     const float mn = fmaxf(st.m, mx);
     const float alpha = mn == -INFINITY ? 1.0f : exp2_fast(st.m - mn);
@@ -293,10 +300,20 @@ __device__ __forceinline__ void fold_scores(Running<DT>& st, f32x16& s, float sc
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    s[i] = exp2_fast(s[i] - ref);
+    s[i] = exp2_fast(fmaf(s[i], scale2, -ref));
     sum += s[i];
   }
   st.l += sum;
+}
+
+// Adds 0 or -inf for every key of a tile with masked or missing keys.
+__device__ __forceinline__ void mask_scores(f32x16& s, const float* bias, int h) {
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const f32x4 bv = *reinterpret_cast<const f32x4*>(bias + 8 * b + 4 * h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[4 * b + i] += bv[i];
+  }
 }
 
 // Query fragments of tile `tl` straight from the rows.
@@ -310,7 +327,11 @@ __device__ __forceinline__ void load_queries(const FwdArgs& a, const Tile& tl, i
   const T* src = static_cast<const T*>(a.q) + int64_t(token) * a.ldq;
 #pragma unroll
   for (int t = 0; t < D::KSTEPS; ++t)
-    q[t] = as_frag<typename Op<T>::Frag>(gather16(src, a.table, 2 * D::VE * t + D::VE * h, true, head, a.q_vec));
+  {
+    u32x4 v = gather16(src, a.table, 2 * D::VE * t + D::VE * h, true, head, a.q_vec);
+    v ^= a.q_sign;  // a negative scale: the sign goes to the queries
+    q[t] = as_frag<typename Op<T>::Frag>(v);
+  }
 }
 
 // With few registers left: keeps the scheduler from reading operands far ahead.
@@ -322,6 +343,10 @@ __device__ __forceinline__ void pace(int u) {
 // Stages kept in shared memory: two where they fit, the next one on its way
 // while this one is worked on, else one.
 constexpr int stage_buffers(int units) { return 2 * units <= 152 ? 2 : 1; }
+constexpr int stage_units(int units) { return stage_buffers(units) * units; }
+// Tiles of a stage of dkv_kernel: Q rows, dO columns [grad_v], dO rows and Q
+// columns [grad_k].
+constexpr int dkv_forms(int part) { return part == 0 ? 4 : part == 1 ? 2 : 3; }
 
 // Writes a wave's result: final rows, or an unnormalised part of a split.
 template <typename T, int DP>
@@ -364,77 +389,106 @@ __device__ __forceinline__ void finish(const FwdArgs& a, const Item& it, const T
     a.lse[int64_t(token) * a.heads + head] = l > 0.0f || l != l ? (st.m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// Four waves with 32 query rows each share the keys through shared memory, the
-// next stage on its way while this one is worked on.
-template <typename T, int DP>
-__global__ __launch_bounds__(kThreads) void fwd_kernel(FwdArgs a) {
+// Four waves of RT x 32 query rows share the keys through shared memory. A wave's
+// turn t computes the scores of tile t + 1 (matrix cores) next to the softmax of
+// tile t (vector units), then adds tile t's values; the tiles after that are on
+// their way to shared memory meanwhile. Bound: matrix cores and vector units
+// together (16 exponentials a lane and tile); RT = 2 halves the operand reads
+// from shared memory per product, which else take as long as the products.
+template <typename T, int DP, int RT>
+__global__ __launch_bounds__(kThreads, lds_waves(4 * Dims<T, DP>::UNITS)) void fwd_kernel(FwdArgs a) {
   using D = Dims<T, DP>;
   using Frag = typename Op<T>::Frag;
-  constexpr int KT = DP * int(sizeof(T)) <= 256 ? 2 : 1;  // key tiles a stage
-  constexpr int STAGE = 2 * KT * D::UNITS;                // 1 KB units: K tiles, then V tiles
-  constexpr int PER = STAGE / 4;                          // of a wave
-  __shared__ u32x4 sh[2][STAGE * 64];
-  __shared__ __attribute__((aligned(16))) float bias[2][KT * 32];
+  __shared__ u32x4 kb[2][D::UNITS * 64], vb[2][D::UNITS * 64];
   const Item it = a.items[blockIdx.x];
   if (it.tiles == 0) return;
   const int lane = int(threadIdx.x) % 64, wave = wave_id(), h = lane / 32;
-  const bool active = wave < it.tiles;
-  const Tile tl = a.qtiles[it.a0 + (active ? wave : 0)];
-  Frag q[D::KSTEPS];
-  load_queries<T, DP>(a, tl, it.hk, lane, q);
-  Running<D::DT> st;
+  const int mine = min(max(it.tiles - wave * RT, 0), RT);  // query tiles of this wave
+  Frag q[RT][D::KSTEPS];
+  Running<D::DT> st[RT];
 #pragma unroll
-  for (int d = 0; d < D::DT; ++d) st.o[d] = zero16();
-
-  const int stages = (it.b1 - it.b0 + KT - 1) / KT;
-  const auto fetch = [&](int s, int buf) {
+  for (int r = 0; r < RT; ++r) {
+    load_queries<T, DP>(a, a.qtiles[it.a0 + (r < mine ? wave * RT + r : 0)], it.hk, lane, q[r]);
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      const int u = k * 4 + wave, which = u / (KT * D::UNITS), rest = u % (KT * D::UNITS);
-      const int tile = min(it.b0 + s * KT + rest / D::UNITS, it.b1 - 1);
-      const T* base = static_cast<const T*>(which ? a.vf : a.kf) + (int64_t(tile) * a.groups + it.hk) * D::TILE;
-      copy_unit(base, rest % D::UNITS, lane, &sh[buf][u * 64]);
+    for (int d = 0; d < D::DT; ++d) st[r].o[d] = zero16();
+  }
+  // tile kt of the keys and tile vt of the values, a quarter by each wave
+  const auto copy = [&](int kt, u32x4* kdst, int vt, u32x4* vdst) {
+    const T* kf = static_cast<const T*>(a.kf) + (int64_t(kt) * a.groups + it.hk) * D::TILE;
+    const T* vf = static_cast<const T*>(a.vf) + (int64_t(vt) * a.groups + it.hk) * D::TILE;
+#pragma unroll
+    for (int k = 0; k < D::UNITS / 2; ++k) {
+      const int u = k * 4 + wave;
+      if (u < D::UNITS) copy_unit(kf, u, lane, kdst + u * 64);
+      else copy_unit(vf, u - D::UNITS, lane, vdst + (u - D::UNITS) * 64);
     }
-    if (int(threadIdx.x) < KT * 32)
-      bias[buf][threadIdx.x] =
-          a.bias[int64_t(min(it.b0 + s * KT + int(threadIdx.x) / 32, it.b1 - 1)) * 32 + threadIdx.x % 32];
   };
-  if (stages > 0) fetch(0, 0);
-  wait_copies();
-  __syncthreads();
-  for (int s = 0; s < stages; ++s) {
-    const int buf = s & 1;
-    if (s + 1 < stages) fetch(s + 1, buf ^ 1);
-    if (active) {
+  f32x16 s[RT];
+  const auto scores = [&](const u32x4* kt, f32x16 (&o)[RT]) {
 #pragma unroll
-      for (int k = 0; k < KT; ++k) {
-        if (it.b0 + s * KT + k >= it.b1) break;
-        f32x16 sc = zero16();
+    for (int r = 0; r < RT; ++r) o[r] = zero16();
 #pragma unroll
-        for (int t = 0; t < D::KSTEPS; ++t)
-          sc = Op<T>::mma(as_frag<Frag>(sh[buf][(k * D::UNITS + t) * 64 + lane]), q[t], sc);
-        fold_scores(st, sc, a.scale2, &bias[buf][k * 32], h);
-        Frag p[D::FR];
+    for (int u = 0; u < D::KSTEPS; ++u) {
+      const Frag kf = as_frag<Frag>(kt[u * 64 + lane]);
 #pragma unroll
-        for (int f = 0; f < D::FR; ++f) p[f] = Op<T>::from_acc(sc, f);
-#pragma unroll
-        for (int d = 0; d < D::DT; ++d)
-#pragma unroll
-          for (int f = 0; f < D::FR; ++f)
-            st.o[d] = Op<T>::mma(as_frag<Frag>(sh[buf][((KT + k) * D::UNITS + d * D::FR + f) * 64 + lane]), p[f],
-                                 st.o[d]);
-      }
+      for (int r = 0; r < RT; ++r) o[r] = Op<T>::mma(kf, q[r][u], o[r]);
     }
+  };
+  const auto turn = [&](int t, auto last) {
+    constexpr bool kLast = decltype(last)::value;
+    const int tile = it.b0 + t;
+    if (!kLast) copy(min(tile + 2, it.b1 - 1), kb[t & 1], tile + 1, vb[(t + 1) & 1]);
+    if (mine > 0) {
+      if (a.flags[tile])
+#pragma unroll
+        for (int r = 0; r < RT; ++r) mask_scores(s[r], a.bias + int64_t(tile) * 32, h);
+      f32x16 next[RT];
+      if (!kLast) scores(kb[(t + 1) & 1], next);
+      Frag p[RT][D::FR];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        fold_scores(st[r], s[r], a.scale2);
+#pragma unroll
+        for (int f = 0; f < D::FR; ++f) p[r][f] = Op<T>::from_acc(s[r], f);
+      }
+#pragma unroll
+      for (int d = 0; d < D::DT; ++d)
+#pragma unroll
+        for (int f = 0; f < D::FR; ++f) {
+          const Frag vf = as_frag<Frag>(vb[t & 1][(d * D::FR + f) * 64 + lane]);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) st[r].o[d] = Op<T>::mma(vf, p[r][f], st[r].o[d]);
+        }
+      if (!kLast)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) s[r] = next[r];
+    }
+    if (!kLast) {
+      wait_copies();
+      __syncthreads();
+    }
+  };
+  const int n = it.b1 - it.b0;
+  if (n > 0) {
+    // (the second copy's values are tile 1's, which turn 0 copies again)
+    copy(it.b0, kb[0], it.b0, vb[0]);
+    copy(min(it.b0 + 1, it.b1 - 1), kb[1], min(it.b0 + 1, it.b1 - 1), vb[1]);
     wait_copies();
     __syncthreads();
+    if (mine > 0) scores(kb[0], s);
+    __syncthreads();
+    for (int t = 0; t + 1 < n; ++t) turn(t, std::false_type{});
+    turn(n - 1, std::true_type{});
   }
-  if (active) finish<T, DP>(a, it, tl, wave, lane, st);
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+    if (r < mine) finish<T, DP>(a, it, a.qtiles[it.a0 + wave * RT + r], wave * RT + r, lane, st[r]);
 }
 
 // At most 32 query rows against a long context (single tokens): the four waves
 // take every fourth key tile, read straight into registers, and join.
 template <typename T, int DP>
-__global__ __launch_bounds__(kThreads) void fwd_few_kernel(FwdArgs a) {
+__global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void fwd_few_kernel(FwdArgs a) {
   using D = Dims<T, DP>;
   using Frag = typename Op<T>::Frag;
   __shared__ f32x4 sh[2][D::DT * 4 * 64];
@@ -468,7 +522,8 @@ __global__ __launch_bounds__(kThreads) void fwd_few_kernel(FwdArgs a) {
 #pragma unroll
       for (int u = 0; u < D::KSTEPS; ++u) sc = Op<T>::mma(as_frag<Frag>(k[u]), q[u], sc);
     }
-    fold_scores(st, sc, a.scale2, a.bias + int64_t(t) * 32, h);
+    if (a.flags[t]) mask_scores(sc, a.bias + int64_t(t) * 32, h);
+    fold_scores(st, sc, a.scale2);
     Frag p[D::FR];
 #pragma unroll
     for (int f = 0; f < D::FR; ++f) p[f] = Op<T>::from_acc(sc, f);
@@ -596,7 +651,7 @@ __device__ __forceinline__ void finish_grad(const BwdArgs& a, const Item& it, co
 // dQ^T += K^T dS^T. Three packed forms of a tile pass through shared memory: K
 // rows, V rows, K columns.
 template <typename T, int DP>
-__global__ __launch_bounds__(kThreads) void dq_kernel(BwdArgs a) {
+__global__ __launch_bounds__(kThreads, lds_waves(stage_units(3 * Dims<T, DP>::UNITS))) void dq_kernel(BwdArgs a) {
   using D = Dims<T, DP>;
   using Frag = typename Op<T>::Frag;
   constexpr int STAGE = 3 * D::UNITS, PER = (STAGE + 3) / 4;
@@ -684,12 +739,11 @@ __global__ __launch_bounds__(kThreads) void dq_kernel(BwdArgs a) {
 // dS = P (dP - delta), dK^T += Q^T dS. PART 0: both; heads whose operands and
 // accumulators do not fit the registers run it as PART 1 (grad_v) and 2 (grad_k).
 template <typename T, int DP, int PART>
-__global__ __launch_bounds__(kThreads) void dkv_kernel(BwdArgs a) {
+__global__ __launch_bounds__(kThreads, lds_waves(stage_units(dkv_forms(PART) * Dims<T, DP>::UNITS))) void dkv_kernel(BwdArgs a) {
   using D = Dims<T, DP>;
   using Frag = typename Op<T>::Frag;
   constexpr bool WANT_V = PART != 2, WANT_K = PART != 1;
-  // Q rows, dO columns [grad_v], dO rows and Q columns [grad_k]
-  constexpr int FORMS = 1 + (WANT_V ? 1 : 0) + (WANT_K ? 2 : 0);
+  constexpr int FORMS = dkv_forms(PART);
   constexpr int GC = 1, GR = WANT_V ? 2 : 1, QC = GR + 1;
   constexpr int STAGE = FORMS * D::UNITS, PER = (STAGE + 3) / 4;
   constexpr int BUFS = stage_buffers(STAGE);
@@ -810,17 +864,19 @@ __global__ __launch_bounds__(kThreads) void grad_join_kernel(BwdArgs a, bool que
 
 template <typename T, int DP>
 struct Kernels {
-  // whether both gradients of the keys fit the 512 registers of a lane in one
-  // pass: two accumulators and two operands (measured: no spills up to 160)
-  static constexpr bool kOnePass = DP <= 160;
+  // whether both gradients of the keys fit the registers of a lane in one
+  // pass: two accumulators and two operands
+  static constexpr bool kOnePass = DP <= (sizeof(T) == 2 ? 128 : 160);
 
   static void pack(const PackArgs& a, int tiles, int tensors, hipStream_t s) {
     hipLaunchKernelGGL((pack_kernel<T, DP>), dim3(unsigned(tiles), unsigned(a.groups), unsigned(tensors)),
                        dim3(kThreads), 0, s, a);
   }
-  static void fwd(const FwdArgs& a, int items, bool few, hipStream_t s) {
-    if (few) hipLaunchKernelGGL((fwd_few_kernel<T, DP>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL((fwd_kernel<T, DP>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
+  static void fwd(const FwdArgs& a, int items, int tiles, hipStream_t s) {
+    if (tiles == 1) hipLaunchKernelGGL((fwd_few_kernel<T, DP>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
+    if (tiles == 4) hipLaunchKernelGGL((fwd_kernel<T, DP, 1>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
+    if constexpr (wide_forward(DP, sizeof(T)))
+      if (tiles == 8) hipLaunchKernelGGL((fwd_kernel<T, DP, 2>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
   }
   static void fwd_join(const FwdArgs& a, int joins, hipStream_t s) {
     hipLaunchKernelGGL((fwd_join_kernel<T, DP>), dim3(unsigned(joins)), dim3(kThreads), 0, s, a);

@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kXcds = 8;
 constexpr int kCus = 256;
+constexpr int kWideTiles = 8;
 
 // One side of a batch cut into 32-row tiles, per sample.
 struct Side {
@@ -45,7 +46,8 @@ struct Unit {
   int32_t sample, a0, tiles, b0, b1;
 };
 
-std::vector<Unit> units(const Side& a, const Side& b, int per, bool (*take)(int)) {
+template <typename F>
+std::vector<Unit> units(const Side& a, const Side& b, int per, F&& take) {
   std::vector<Unit> u;
   for (size_t s = 0; s + 1 < a.first.size(); ++s) {
     const int n = a.first[s + 1] - a.first[s];
@@ -161,6 +163,7 @@ size_t tile_bytes(const cgtp_attn_s* a) { return size_t(a->DP) * 32 * dtype_size
 struct Context {
   void *kf, *vf;
   float* bias;
+  int32_t* flags;
   size_t bytes;
 };
 Context carve_context(const cgtp_attn_batch_s* b, void* p) {
@@ -170,6 +173,7 @@ Context carve_context(const cgtp_attn_batch_s* b, void* p) {
   x.kf = c.take(n);
   x.vf = c.take(n);
   x.bias = static_cast<float*>(c.take(size_t(b->ktiles) * 32 * 4));
+  x.flags = static_cast<int32_t*>(c.take(size_t(b->ktiles) * 4));
   x.bytes = c.used;
   return x;
 }
@@ -201,7 +205,9 @@ Backward carve_backward(const cgtp_attn_batch_s* b, void* p) {
   return x;
 }
 
-int64_t fwd_part_tiles(const cgtp_attn_batch_s* b) { return std::max(b->fwd.part_tiles, b->few.part_tiles); }
+int64_t fwd_part_tiles(const cgtp_attn_batch_s* b) {
+  return std::max(std::max(b->fwd.part_tiles, b->few.part_tiles), b->wide.part_tiles);
+}
 
 }  // namespace
 }  // namespace attn
@@ -261,8 +267,11 @@ cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, co
   b->qtile_mem.upload(qs.tiles.data(), qs.tiles.size() * sizeof(Tile));
   b->ktile_mem.upload(ks.tiles.data(), ks.tiles.size() * sizeof(Tile));
   const int g = at->kv_heads;
-  // samples with one query tile take the kernel whose waves share the queries
-  build(b->fwd, units(qs, ks, 4, [](int n) { return n > 1; }), 4, g, 2 * kCus, 8);
+  // samples with one query tile take the kernel whose waves share the queries,
+  // those with enough rows the one of 64 rows a wave
+  const int wide = wide_forward(at->DP, dtype_size(at->dtype)) ? kWideTiles : INT32_MAX;
+  build(b->fwd, units(qs, ks, 4, [&](int n) { return n > 1 && n < wide; }), 4, g, 2 * kCus, 8);
+  build(b->wide, units(qs, ks, 8, [&](int n) { return n >= wide; }), 8, g, kCus, 8);
   build(b->few, units(qs, ks, 1, [](int n) { return n == 1; }), 1, g, 4 * kCus, 16);
   build(b->dq, units(qs, ks, 4, [](int) { return true; }), 4, g, 2 * kCus, 8);
   build(b->dkv, units(ks, qs, 4, [](int) { return true; }), 4, g, 2 * kCus, 8);
@@ -314,6 +323,7 @@ void attn_pack_launch(const cgtp_attn_batch_s* b, RowsIn k, RowsIn v, const uint
   PackArgs p = context_pack(b, k, v, mask);
   p.t[0].row_frags = c.kf;
   p.t[0].bias = c.bias;
+  p.t[0].flags = c.flags;
   p.t[1].col_frags = c.vf;
   b->attn->k.pack(p, int(b->ktiles), 2, s);
   CGTP_CHECK_HIP(hipGetLastError());
@@ -332,23 +342,26 @@ void attn_forward_launch(const cgtp_attn_batch_s* b, RowsIn q, const void* conte
   f.kf = c.kf;
   f.vf = c.vf;
   f.bias = c.bias;
+  f.flags = c.flags;
   f.out = out;
   f.ldo = a->qrow.dim;
   f.out_quad = quad_rows(a, out);
   f.lse = lse;
   f.part_ml = static_cast<float*>(ws);
   f.part = f.part_ml + size_t(fwd_part_tiles(b)) * 64;
-  f.scale2 = float(scale * 1.4426950408889634);
+  // a zero scale stays a small positive one: every score is then 0 all the same
+  f.scale2 = std::max(float(std::fabs(scale) * 1.4426950408889634), 1e-37f);
+  f.q_sign = scale < 0.0 ? (a->dtype == CGTP_BF16 ? 0x80008000u : 0x80000000u) : 0u;
   f.G = a->G;
   f.heads = a->heads;
   f.groups = a->kv_heads;
-  // the two lists share the partial buffers: each is joined before the next starts
-  for (const bool few : {false, true}) {
-    const WorkList& w = few ? b->few : b->fwd;
+  // the lists share the partial buffers: each is joined before the next starts
+  for (const int tiles : {8, 4, 1}) {
+    const WorkList& w = tiles == 8 ? b->wide : tiles == 4 ? b->fwd : b->few;
     if (w.items == 0) continue;
     f.items = w.item_mem.as<Item>();
     f.joins = w.join_mem.as<Join>();
-    a->k.fwd(f, w.items, few, s);
+    a->k.fwd(f, w.items, tiles, s);
     CGTP_CHECK_HIP(hipGetLastError());
     if (w.joins) {
       a->k.fwd_join(f, w.joins, s);
