@@ -46,6 +46,7 @@ struct PackArgs {
   int64_t ldo;
   const float* lse;
   int G, heads, groups;  // G = 0: context rows
+  int ntiles;
   bool out_vec;
 };
 
@@ -82,7 +83,7 @@ struct BwdArgs {
 };
 
 struct KernelTable {
-  void (*pack)(const PackArgs&, int tiles, int tensors, hipStream_t);
+  void (*pack)(const PackArgs&, hipStream_t);
   void (*fwd)(const FwdArgs&, int items, int tiles, hipStream_t);  // items of up to 1, 4 or 8 tiles
   void (*fwd_join)(const FwdArgs&, int joins, hipStream_t);
   void (*dq)(const BwdArgs&, int items, hipStream_t);

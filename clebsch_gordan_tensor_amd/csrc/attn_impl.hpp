@@ -190,8 +190,11 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
   constexpr int VE = D::VE, LD = DP + VE;  // an odd count of 16-byte pieces a row: no bank conflicts
   __shared__ __attribute__((aligned(16))) T sh[32 * LD];
   __shared__ float red[32][9];
-  const int tile = int(blockIdx.x), hk = int(blockIdx.y);
-  const PackTensor p = a.t[blockIdx.z];
+  // A head's channels are short runs of a row: the heads of one tile share its
+  // cache lines, so they go to one die (workgroup index modulo 8), one after another
+  const int turn = int(blockIdx.x) / 8, tile = turn / a.groups * 8 + int(blockIdx.x) % 8, hk = turn % a.groups;
+  if (tile >= a.ntiles) return;
+  const PackTensor p = a.t[blockIdx.y];
   const Tile tl = a.tiles[tile];
   const int tid = int(threadIdx.x);
   const bool query = a.G > 0;
@@ -868,9 +871,9 @@ struct Kernels {
   // pass: two accumulators and two operands
   static constexpr bool kOnePass = DP <= (sizeof(T) == 2 ? 128 : 160);
 
-  static void pack(const PackArgs& a, int tiles, int tensors, hipStream_t s) {
-    hipLaunchKernelGGL((pack_kernel<T, DP>), dim3(unsigned(tiles), unsigned(a.groups), unsigned(tensors)),
-                       dim3(kThreads), 0, s, a);
+  static void pack(const PackArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL((pack_kernel<T, DP>), dim3(unsigned((a.ntiles + 7) / 8 * 8 * a.groups), 2), dim3(kThreads), 0, s,
+                       a);
   }
   static void fwd(const FwdArgs& a, int items, int tiles, hipStream_t s) {
     if (tiles == 1) hipLaunchKernelGGL((fwd_few_kernel<T, DP>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);

@@ -307,6 +307,7 @@ PackArgs context_pack(const cgtp_attn_batch_s* b, RowsIn k, RowsIn v, const uint
   p.t[1].ld = v.ld;
   p.t[1].vec = vec_rows(a, v.p, v.ld);
   p.tiles = b->ktile_mem.as<Tile>();
+  p.ntiles = int(b->ktiles);
   p.table = a->table.as<int4>();
   p.mask = mask;
   p.heads = a->heads;
@@ -325,7 +326,7 @@ void attn_pack_launch(const cgtp_attn_batch_s* b, RowsIn k, RowsIn v, const uint
   p.t[0].bias = c.bias;
   p.t[0].flags = c.flags;
   p.t[1].col_frags = c.vf;
-  b->attn->k.pack(p, int(b->ktiles), 2, s);
+  b->attn->k.pack(p, s);
   CGTP_CHECK_HIP(hipGetLastError());
 }
 
@@ -381,7 +382,7 @@ void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn
     p.t[0].col_frags = dq ? w.kc : nullptr;
     p.t[0].bias = w.bias;
     p.t[1].row_frags = w.vr;
-    a->k.pack(p, int(b->ktiles), 2, s);
+    a->k.pack(p, s);
     CGTP_CHECK_HIP(hipGetLastError());
   }
   if (b->qtiles) {
@@ -407,7 +408,8 @@ void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn
     p.G = a->G;
     p.heads = a->heads;
     p.groups = a->kv_heads;
-    a->k.pack(p, int(b->qtiles), 2, s);
+    p.ntiles = int(b->qtiles);
+    a->k.pack(p, s);
     CGTP_CHECK_HIP(hipGetLastError());
   }
   BwdArgs x{};
