@@ -442,7 +442,7 @@ __global__ __launch_bounds__(kThreads, lds_waves(4 * Dims<T, DP>::UNITS)) void f
     const int tile = it.b0 + t;
     if (!kLast) copy(min(tile + 2, it.b1 - 1), kb[t & 1], tile + 1, vb[(t + 1) & 1]);
     if (mine > 0) {
-      if (a.flags[tile])
+      if (ldc(a.flags + tile))
 #pragma unroll
         for (int r = 0; r < RT; ++r) mask_scores(s[r], a.bias + int64_t(tile) * 32, h);
       f32x16 next[RT];
@@ -525,7 +525,7 @@ __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void fwd_few_ke
 #pragma unroll
       for (int u = 0; u < D::KSTEPS; ++u) sc = Op<T>::mma(as_frag<Frag>(k[u]), q[u], sc);
     }
-    if (a.flags[t]) mask_scores(sc, a.bias + int64_t(t) * 32, h);
+    if (ldc(a.flags + t)) mask_scores(sc, a.bias + int64_t(t) * 32, h);
     fold_scores(st, sc, a.scale2);
     Frag p[D::FR];
 #pragma unroll

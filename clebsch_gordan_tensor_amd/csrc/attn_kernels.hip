@@ -66,15 +66,16 @@ std::vector<Unit> units(const Side& a, const Side& b, int per, F&& take) {
 // partial result's write and read).
 // Order: workgroups go to the 8 dies in turn, and each die has its own L2, so
 // all items that read the same packed tiles (one sample and context head) are
-// given to one die and follow each other there, longest groups first; a group
-// bigger than a die's share goes round several.
+// given to one die and follow each other there, those with the longest items
+// first, so that the short ones fill the end; a group bigger than a die's share
+// goes round several.
 void build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, int64_t target, int min_len) {
   int64_t work = 0;
   for (const Unit& x : u) work += std::max(1, x.b1 - x.b0);
   work *= groups;
   const int64_t len = std::max<int64_t>(min_len, (work + target - 1) / target);
   struct Group {
-    int64_t work = 0;
+    int64_t work = 0, longest = 0;
     std::vector<Item> items;
   };
   std::vector<Group> gs;
@@ -92,6 +93,7 @@ void build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, int6
           const int32_t b0 = int32_t(x.b0 + n * p / parts), b1 = int32_t(x.b0 + n * (p + 1) / parts);
           g.items.push_back({x.a0, x.tiles, b0, b1, hk, parts > 1 ? int32_t(slots + p) : -1, stride, 0});
           g.work += b1 - b0 + 1;
+          g.longest = std::max<int64_t>(g.longest, b1 - b0);
         }
         if (parts > 1) {
           for (int t = 0; t < x.tiles; ++t)
@@ -113,7 +115,7 @@ void build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, int6
   std::vector<int64_t> load(kXcds, 0);
   std::vector<size_t> order(gs.size());
   std::iota(order.begin(), order.end(), size_t(0));
-  std::stable_sort(order.begin(), order.end(), [&](size_t a, size_t b) { return gs[a].work > gs[b].work; });
+  std::stable_sort(order.begin(), order.end(), [&](size_t a, size_t b) { return gs[a].longest > gs[b].longest; });
   for (size_t gi : order) {
     const Group& g = gs[gi];
     size_t at = 0;
