@@ -31,9 +31,6 @@ struct PackTensor {
   const void* src;
   int64_t ld;
   void *row_frags, *col_frags;  // either may be NULL
-  float* rows_out;              // gradient rows: lse and delta (else NULL)
-  float* bias;                  // context: 0 or -inf for every key (one tensor of a call)
-  int32_t* flags;               // context: whether a tile has a masked or missing key
   bool vec;                     // 16-byte gathers
 };
 
@@ -45,9 +42,24 @@ struct PackArgs {
   const void* out;      // forward's output (for delta)
   int64_t ldo;
   const float* lse;
+  float* rows_out;      // queries and grad_out: lse and delta of every row (else NULL)
+  float* bias;          // context: 0 or -inf for every key (else NULL)
+  int32_t* flags;       // context: whether a tile has a masked or missing key (or NULL)
   int G, heads, groups;  // G = 0: context rows
   int ntiles;
   bool out_vec;
+};
+
+// Up to two tensors of equal layout whose parts are added.
+struct GradJoinArgs {
+  const Join* joins;
+  const Tile* tiles;
+  const int4* table;
+  const float *part0, *part1;
+  void *dst0, *dst1;
+  int64_t ld;
+  int G;  // 1 for context rows
+  bool query, quad;
 };
 
 struct FwdArgs {
@@ -69,7 +81,6 @@ struct FwdArgs {
 
 struct BwdArgs {
   const Item* items;
-  const Join* joins;
   const Tile *qtiles, *ktiles;
   const int4* table;
   const void *kr, *kc, *vr, *qr, *qc, *gr, *gc;  // r: row fragments, c: column fragments; g: grad_out
@@ -88,8 +99,7 @@ struct KernelTable {
   void (*fwd_join)(const FwdArgs&, int joins, hipStream_t);
   void (*dq)(const BwdArgs&, int items, hipStream_t);
   void (*dkv)(const BwdArgs&, int items, hipStream_t);  // grad_k and grad_v, each unless NULL
-  void (*grad_join)(const BwdArgs&, int joins, bool query, const float* part, void* dst, int64_t ld, bool quad,
-                    hipStream_t);
+  void (*grad_join)(const GradJoinArgs&, int joins, int tensors, hipStream_t);
 };
 
 // Kernels of a padded head size (a multiple of 32 up to 256); inst/attn_*.hip.

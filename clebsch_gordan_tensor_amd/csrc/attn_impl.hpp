@@ -181,88 +181,111 @@ __device__ __forceinline__ void scatter4(T* row, const int4* table, int d0, bool
 
 // ------------------------------------------------------------------ packing
 //
-// One workgroup packs one 32-row tile of one head group: gather into shared
-// memory (16 bytes a lane), write row and/or column fragments (1 KB runs).
-// Bound: memory (each element read once and written once per form).
+// One workgroup packs one 32-row tile of one head group of both tensors of a
+// call: 16-byte gathers, row fragments written straight from the registers that
+// received them (a lane's piece of a row is a piece of a fragment), column
+// fragments by way of shared memory. Bound: memory, each element read once and
+// written once per form; both tensors' loads are issued together, since what
+// holds a small workgroup up is the latency of its chain of loads.
 template <typename T, int DP>
 __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
   using D = Dims<T, DP>;
   constexpr int VE = D::VE, LD = DP + VE;  // an odd count of 16-byte pieces a row: no bank conflicts
-  __shared__ __attribute__((aligned(16))) T sh[32 * LD];
+  constexpr int PIECES = DP / VE, PER = (PIECES + 7) / 8;
+  __shared__ __attribute__((aligned(16))) T sh[2][32 * LD];
   __shared__ float red[32][9];
   // A head's channels are short runs of a row: the heads of one tile share its
   // cache lines, so they go to one die (workgroup index modulo 8), one after another
   const int turn = int(blockIdx.x) / 8, tile = turn / a.groups * 8 + int(blockIdx.x) % 8, hk = turn % a.groups;
   if (tile >= a.ntiles) return;
-  const PackTensor p = a.t[blockIdx.y];
-  const Tile tl = a.tiles[tile];
-  const int tid = int(threadIdx.x);
+  const Tile tl = ldc(a.tiles + tile);
+  const int tid = int(threadIdx.x), lane = tid % 64, wave = wave_id();
   const bool query = a.G > 0;
   const int G = query ? a.G : 1;
-  constexpr int PIECES = DP / VE;
-  // rows a query cannot see, or that see nothing, count as zero
-  float partial = 0.0f;
-  const int r = tid / 8;  // 8 threads a row
+  // 8 threads a row, every eighth piece each
+  const int r = tid / 8;
   const bool in = r < tl.n;
   const int grow = tl.row0 + (in ? r : 0);
   const int token = grow / G, head = hk * G + grow % G;
-  bool live = in && (a.mask == nullptr || a.mask[token] != 0);
-  float lse = 0.0f;
-  if (p.rows_out && in) {
-    lse = a.lse[int64_t(token) * a.heads + head];
-    live = lse > -INFINITY;
-  }
-  for (int c = tid % 8; c < PIECES; c += 8) {
-    u32x4 v = {0, 0, 0, 0};
-    if (live) {
-      v = gather16(static_cast<const T*>(p.src) + int64_t(token) * p.ld, a.table, c * VE, query, head, p.vec);
-      if (p.rows_out) {
-        const u32x4 o = gather16(static_cast<const T*>(a.out) + int64_t(token) * a.ldo, a.table, c * VE, query, head,
-                                 a.out_vec);
-        T tv[VE], to[VE];
-        __builtin_memcpy(tv, &v, 16);
-        __builtin_memcpy(to, &o, 16);
+  const bool grads = a.rows_out != nullptr;  // tensor 1 is grad_out
+  // masked rows, and gradients of rows that saw nothing, count as zero
+  const bool live = in && (a.mask == nullptr || a.mask[token] != 0);
+  const float lse = grads && in ? a.lse[int64_t(token) * a.heads + head] : 0.0f;
+  const bool live1 = live && (!grads || lse > -INFINITY);
+  u32x4 v0[PER], v1[PER], vo[PER];
 #pragma unroll
-        for (int j = 0; j < VE; ++j) partial += to_acc<float>(tv[j]) * to_acc<float>(to[j]);
-      }
+  for (int c = 0; c < PER; ++c) {
+    const int p = tid % 8 + 8 * c;
+    v0[c] = v1[c] = vo[c] = u32x4{0, 0, 0, 0};
+    if (PIECES % 8 != 0 && p >= PIECES) break;
+    const auto piece = [&](const void* src, int64_t ld, bool vec) {
+      return gather16(static_cast<const T*>(src) + int64_t(token) * ld, a.table, p * VE, query, head, vec);
+    };
+    if (live) v0[c] = piece(a.t[0].src, a.t[0].ld, a.t[0].vec);
+    if (live1) {
+      v1[c] = piece(a.t[1].src, a.t[1].ld, a.t[1].vec);
+      if (grads) vo[c] = piece(a.out, a.ldo, a.out_vec);
     }
-    *reinterpret_cast<u32x4*>(&sh[r * LD + c * VE]) = v;
   }
-  if (p.rows_out) red[r][tid % 8] = partial;
+  const int64_t at = int64_t(tile) * a.groups + hk;
+  // piece p of row r is lane r + 32 (p % 2) of row fragment p / 2
+  const auto rows = [&](const PackTensor& t, const u32x4 (&v)[PER]) {
+    if (!t.row_frags) return;
+    u32x4* o = reinterpret_cast<u32x4*>(static_cast<T*>(t.row_frags) + at * D::TILE);
+#pragma unroll
+    for (int c = 0; c < PER; ++c) {
+      const int p = tid % 8 + 8 * c;
+      if (PIECES % 8 != 0 && p >= PIECES) break;
+      o[p / 2 * 64 + p % 2 * 32 + r] = v[c];
+    }
+  };
+  rows(a.t[0], v0);
+  rows(a.t[1], v1);
+#pragma unroll
+  for (int c = 0; c < PER; ++c) {
+    const int d0 = (tid % 8 + 8 * c) * VE;
+    if (PIECES % 8 != 0 && d0 >= DP) break;
+    if (a.t[0].col_frags) *reinterpret_cast<u32x4*>(&sh[0][r * LD + d0]) = v0[c];
+    if (a.t[1].col_frags) *reinterpret_cast<u32x4*>(&sh[1][r * LD + d0]) = v1[c];
+  }
+  if (grads) {
+    float partial = 0.0f;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) {
+      T tv[VE], to[VE];
+      __builtin_memcpy(tv, &v1[c], 16);
+      __builtin_memcpy(to, &vo[c], 16);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) partial += to_acc<float>(tv[j]) * to_acc<float>(to[j]);
+    }
+    red[r][tid % 8] = partial;
+  }
   __syncthreads();
-  const int64_t at = (int64_t(tile) * a.groups + hk);
-  if (tid < 32) {
-    if (p.rows_out) {
-      // log2-domain lse (+inf: the row contributes nothing) and rowsum(grad_out out)
-      float d = 0.0f;
-      for (int k = 0; k < 8; ++k) d += red[tid][k];
-      const int gr = tl.row0 + (tid < tl.n ? tid : 0);
-      const float l = a.lse[int64_t(gr / G) * a.heads + hk * G + gr % G];
-      p.rows_out[at * 64 + tid] = tid < tl.n && l > -INFINITY ? l * 1.44269504088896341f : INFINITY;
-      p.rows_out[at * 64 + 32 + tid] = d;
-    }
-    if (p.bias && hk == 0) {
-      const bool seen = tid < tl.n && (a.mask == nullptr || a.mask[tl.row0 + tid] != 0);
-      p.bias[int64_t(tile) * 32 + tid] = seen ? 0.0f : -INFINITY;
-      const bool some = __any(!seen);
-      if (p.flags && tid == 0) p.flags[tile] = some;
-    }
+  if (grads && tid % 8 == 0) {
+    // log2-domain lse (+inf: the row contributes nothing) and rowsum(grad_out out)
+    float d = 0.0f;
+    for (int k = 0; k < 8; ++k) d += red[r][k];
+    a.rows_out[at * 64 + r] = in && lse > -INFINITY ? lse * 1.44269504088896341f : INFINITY;
+    a.rows_out[at * 64 + 32 + r] = d;
   }
-  const int lane = tid % 64, wave = tid / 64, n = lane % 32, h = lane / 32;
-  if (p.row_frags) {
-    u32x4* o = reinterpret_cast<u32x4*>(static_cast<T*>(p.row_frags) + at * D::TILE);
-    for (int t = wave; t < D::KSTEPS; t += 4)
-      o[t * 64 + lane] = *reinterpret_cast<const u32x4*>(&sh[n * LD + 2 * VE * t + VE * h]);
+  if (a.bias && hk == 0 && tid < 32) {
+    const bool seen = tid < tl.n && (a.mask == nullptr || a.mask[tl.row0 + tid] != 0);
+    a.bias[int64_t(tile) * 32 + tid] = seen ? 0.0f : -INFINITY;
+    const bool some = __any(!seen);
+    if (a.flags && tid == 0) a.flags[tile] = some;
   }
-  if (p.col_frags) {
-    u32x4* o = reinterpret_cast<u32x4*>(static_cast<T*>(p.col_frags) + at * D::TILE);
-    for (int u = wave; u < D::DT * D::FR; u += 4) {
+  const int n = lane % 32, h = lane / 32;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (!a.t[k].col_frags) continue;
+    u32x4* o = reinterpret_cast<u32x4*>(static_cast<T*>(a.t[k].col_frags) + at * D::TILE);
+    for (int u = wave; u < D::UNITS; u += 4) {
       const int dt = u / D::FR, f = u % D::FR;
       T t[VE];
 #pragma unroll
       for (int j = 0; j < VE; ++j) {
         const int rr = VE * f + j;
-        t[j] = sh[(8 * (rr / 4) + 4 * h + rr % 4) * LD + 32 * dt + n];
+        t[j] = sh[k][(8 * (rr / 4) + 4 * h + rr % 4) * LD + 32 * dt + n];
       }
       u32x4 v;
       __builtin_memcpy(&v, t, 16);
@@ -583,34 +606,36 @@ __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void fwd_few_ke
   }
 }
 
-// Joins the parts of split rows: 8 threads a row.
+// Joins the parts of split rows: a workgroup takes 32 rows x 32 columns (columns
+// of workgroup y), a thread 4 of them. Bound: the parts' bytes; the loads of all
+// parts are independent, so they overlap.
 template <typename T, int DP>
 __global__ __launch_bounds__(kThreads) void fwd_join_kernel(FwdArgs a) {
-  const Join j = a.joins[blockIdx.x];
-  const Tile tl = a.qtiles[j.tile];
-  const int n = int(threadIdx.x) / 8, c = int(threadIdx.x) % 8;
+  const Join j = ldc(a.joins + blockIdx.x);
+  const Tile tl = ldc(a.qtiles + j.tile);
+  const int n = int(threadIdx.x) / 8, d = int(blockIdx.y) * 32 + int(threadIdx.x) % 8 * 4;
   if (n >= tl.n) return;
-  const auto at = [&](int k) { return (int64_t(j.slot + k) * j.stride + j.within) * 32 + n; };
+  const int64_t first = (int64_t(j.slot) * j.stride + j.within) * 32 + n, step = int64_t(j.stride) * 32;
   float m = -INFINITY, l = 0.0f;
-  for (int k = 0; k < j.parts; ++k) m = fmaxf(m, a.part_ml[2 * at(k)]);
+#pragma unroll 4
+  for (int k = 0; k < j.parts; ++k) m = fmaxf(m, a.part_ml[2 * (first + k * step)]);
   const float ref = m == -INFINITY ? 0.0f : m;
-  for (int k = 0; k < j.parts; ++k) l += a.part_ml[2 * at(k) + 1] * exp2_fast(a.part_ml[2 * at(k)] - ref);
+  float v[4] = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int k = 0; k < j.parts; ++k) {
+    const int64_t r = first + k * step;
+    const float w = exp2_fast(a.part_ml[2 * r] - ref);
+    l += a.part_ml[2 * r + 1] * w;
+    const f32x4 o = *reinterpret_cast<const f32x4*>(a.part + r * DP + d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += w * o[i];
+  }
   const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
   const int row = tl.row0 + n, token = row / a.G, head = j.hk * a.G + row % a.G;
-  T* out = static_cast<T*>(a.out) + int64_t(token) * a.ldo;
-  for (int d = 4 * c; d < DP; d += 32) {
-    float v[4] = {0, 0, 0, 0};
-    for (int k = 0; k < j.parts; ++k) {
-      const float w = exp2_fast(a.part_ml[2 * at(k)] - ref);
-      const f32x4 o = *reinterpret_cast<const f32x4*>(a.part + at(k) * DP + d);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += w * o[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] *= inv;
-    scatter4(out, a.table, d, true, head, a.out_quad, v);
-  }
-  if (a.lse && c == 0)
+  for (int i = 0; i < 4; ++i) v[i] *= inv;
+  scatter4(static_cast<T*>(a.out) + int64_t(token) * a.ldo, a.table, d, true, head, a.out_quad, v);
+  if (a.lse && d == 0)
     a.lse[int64_t(token) * a.heads + head] = l > 0.0f || l != l ? (ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
@@ -841,26 +866,23 @@ __global__ __launch_bounds__(kThreads, lds_waves(stage_units(dkv_forms(PART) * D
     if (a.dk) finish_grad<T, DP>(a, it, tl, wave, lane, false, a.dk, a.ldk, a.part, a.k_quad, dk, a.scale);
 }
 
-// Adds the parts of split gradient rows in order: 8 threads a row.
+// Adds the parts of split gradient rows in order, as fwd_join_kernel.
 template <typename T, int DP>
-__global__ __launch_bounds__(kThreads) void grad_join_kernel(BwdArgs a, bool query, const float* part, void* dst,
-                                                             int64_t ld, bool quad) {
-  const Join j = a.joins[blockIdx.x];
-  const Tile tl = query ? a.qtiles[j.tile] : a.ktiles[j.tile];
-  const int n = int(threadIdx.x) / 8, c = int(threadIdx.x) % 8;
+__global__ __launch_bounds__(kThreads) void grad_join_kernel(GradJoinArgs a) {
+  const Join j = ldc(a.joins + blockIdx.x);
+  const Tile tl = ldc(a.tiles + j.tile);
+  const int n = int(threadIdx.x) / 8, d = int(blockIdx.y) * 32 + int(threadIdx.x) % 8 * 4;
   if (n >= tl.n) return;
-  const int row = tl.row0 + n, G = query ? a.G : 1, token = row / G, head = j.hk * G + row % G;
-  T* out = static_cast<T*>(dst) + int64_t(token) * ld;
-  for (int d = 4 * c; d < DP; d += 32) {
-    float v[4] = {0, 0, 0, 0};
-    for (int k = 0; k < j.parts; ++k) {
-      const f32x4 o =
-          *reinterpret_cast<const f32x4*>(part + ((int64_t(j.slot + k) * j.stride + j.within) * 32 + n) * DP + d);
+  const float* p = (blockIdx.z ? a.part1 : a.part0) + ((int64_t(j.slot) * j.stride + j.within) * 32 + n) * DP + d;
+  float v[4] = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int k = 0; k < j.parts; ++k) {
+    const f32x4 o = *reinterpret_cast<const f32x4*>(p + int64_t(k) * j.stride * 32 * DP);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += o[i];
-    }
-    scatter4(out, a.table, d, query, head, quad, v);
+    for (int i = 0; i < 4; ++i) v[i] += o[i];
   }
+  const int row = tl.row0 + n, token = row / a.G, head = j.hk * a.G + row % a.G;
+  scatter4(static_cast<T*>(blockIdx.z ? a.dst1 : a.dst0) + int64_t(token) * a.ld, a.table, d, a.query, head, a.quad, v);
 }
 
 // -------------------------------------------------------------------- launch
@@ -872,8 +894,7 @@ struct Kernels {
   static constexpr bool kOnePass = DP <= (sizeof(T) == 2 ? 128 : 160);
 
   static void pack(const PackArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL((pack_kernel<T, DP>), dim3(unsigned((a.ntiles + 7) / 8 * 8 * a.groups), 2), dim3(kThreads), 0, s,
-                       a);
+    hipLaunchKernelGGL((pack_kernel<T, DP>), dim3(unsigned((a.ntiles + 7) / 8 * 8 * a.groups)), dim3(kThreads), 0, s, a);
   }
   static void fwd(const FwdArgs& a, int items, int tiles, hipStream_t s) {
     if (tiles == 1) hipLaunchKernelGGL((fwd_few_kernel<T, DP>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
@@ -882,7 +903,7 @@ struct Kernels {
       if (tiles == 8) hipLaunchKernelGGL((fwd_kernel<T, DP, 2>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
   }
   static void fwd_join(const FwdArgs& a, int joins, hipStream_t s) {
-    hipLaunchKernelGGL((fwd_join_kernel<T, DP>), dim3(unsigned(joins)), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((fwd_join_kernel<T, DP>), dim3(unsigned(joins), DP / 32), dim3(kThreads), 0, s, a);
   }
   static void dq(const BwdArgs& a, int items, hipStream_t s) {
     hipLaunchKernelGGL((dq_kernel<T, DP>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
@@ -895,10 +916,9 @@ struct Kernels {
       if (a.dk) hipLaunchKernelGGL((dkv_kernel<T, DP, 2>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
     }
   }
-  static void grad_join(const BwdArgs& a, int joins, bool query, const float* part, void* dst, int64_t ld, bool quad,
-                        hipStream_t s) {
-    hipLaunchKernelGGL((grad_join_kernel<T, DP>), dim3(unsigned(joins)), dim3(kThreads), 0, s, a, query, part, dst, ld,
-                       quad);
+  static void grad_join(const GradJoinArgs& a, int joins, int tensors, hipStream_t s) {
+    hipLaunchKernelGGL((grad_join_kernel<T, DP>), dim3(unsigned(joins), DP / 32, unsigned(tensors)), dim3(kThreads), 0,
+                       s, a);
   }
   static KernelTable table() { return {pack, fwd, fwd_join, dq, dkv, grad_join}; }
 };

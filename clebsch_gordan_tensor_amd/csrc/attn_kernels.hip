@@ -1,7 +1,9 @@
 // Cross attention: handles, work lists and dispatch (kernels: attn_impl.hpp).
 #include <algorithm>
 #include <cmath>
+#include <functional>
 #include <numeric>
+#include <queue>
 
 #include "attn.hpp"
 
@@ -58,29 +60,64 @@ std::vector<Unit> units(const Side& a, const Side& b, int per, F&& take) {
   return u;
 }
 
+// Longest part of a unit, in tiles: of some candidates the one whose parts, the
+// longest first onto `slots` places, end earliest. An item costs its tiles plus
+// about two for its start and end, a part of a split one about three more for
+// its partial result and the join (measured: parts of a ragged batch cut to
+// twice the number cost as much as the better balance gained). Parts have at least
+// min_len tiles, and batches with many more items than places are not split.
+int64_t part_length(const std::vector<Unit>& u, int groups, int slots, int min_len) {
+  int64_t longest = 1;
+  for (const Unit& x : u) longest = std::max<int64_t>(longest, x.b1 - x.b0);
+  if (int64_t(u.size()) * groups > 16 * int64_t(slots)) return longest;
+  int64_t best = longest, best_end = INT64_MAX;
+  for (int64_t parts = 1; parts <= 64; parts += 1 + parts / 8) {
+    const int64_t len = (longest + parts - 1) / parts;
+    if (parts > 1 && len < min_len) break;
+    std::vector<int64_t> cost;
+    for (const Unit& x : u) {
+      const int64_t n = x.b1 - x.b0, k = std::max<int64_t>(1, (n + len - 1) / len);
+      for (int64_t i = 0; i < k * groups; ++i) cost.push_back((n + k - 1) / k + (k > 1 ? 5 : 2));
+    }
+    if (parts > 1 && int64_t(cost.size()) > 16 * int64_t(slots)) break;
+    std::sort(cost.begin(), cost.end(), std::greater<int64_t>());
+    std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> ends;
+    int64_t end = 0;
+    for (int64_t c : cost) {
+      int64_t t = c;
+      if (int64_t(ends.size()) >= slots) {
+        t += ends.top();
+        ends.pop();
+      }
+      ends.push(t);
+      end = std::max(end, t);
+    }
+    if (end < best_end) {
+      best_end = end;
+      best = len;
+    }
+  }
+  return best;
+}
+
 // Splits long units (of at most `stride` tiles) and lays the items out for the
 // device.
 //
-// Splits: the work of all units is cut so that about `target` workgroups share
-// it evenly, but no part is shorter than min_len tiles (a part costs its
-// partial result's write and read).
+// `slots` is the number of workgroups that the device works on at once.
 // Order: workgroups go to the 8 dies in turn, and each die has its own L2, so
 // all items that read the same packed tiles (one sample and context head) are
 // given to one die and follow each other there, those with the longest items
 // first, so that the short ones fill the end; a group bigger than a die's share
 // goes round several.
-void build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, int64_t target, int min_len) {
-  int64_t work = 0;
-  for (const Unit& x : u) work += std::max(1, x.b1 - x.b0);
-  work *= groups;
-  const int64_t len = std::max<int64_t>(min_len, (work + target - 1) / target);
+void build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, int slots, int min_len) {
+  const int64_t len = part_length(u, groups, slots, min_len);
   struct Group {
     int64_t work = 0, longest = 0;
     std::vector<Item> items;
   };
   std::vector<Group> gs;
   std::vector<Join> joins;
-  int64_t slots = 0;
+  int64_t nslot = 0;
   for (size_t i = 0; i < u.size();) {
     size_t j = i;
     while (j < u.size() && u[j].sample == u[i].sample) ++j;
@@ -91,21 +128,21 @@ void build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, int6
         const int64_t n = x.b1 - x.b0, parts = std::max<int64_t>(1, (n + len - 1) / len);
         for (int64_t p = 0; p < parts; ++p) {
           const int32_t b0 = int32_t(x.b0 + n * p / parts), b1 = int32_t(x.b0 + n * (p + 1) / parts);
-          g.items.push_back({x.a0, x.tiles, b0, b1, hk, parts > 1 ? int32_t(slots + p) : -1, stride, 0});
+          g.items.push_back({x.a0, x.tiles, b0, b1, hk, parts > 1 ? int32_t(nslot + p) : -1, stride, 0});
           g.work += b1 - b0 + 1;
           g.longest = std::max<int64_t>(g.longest, b1 - b0);
         }
         if (parts > 1) {
           for (int t = 0; t < x.tiles; ++t)
-            joins.push_back({x.a0 + t, hk, int32_t(slots), int32_t(parts), stride, t, 0, 0});
-          slots += parts;
+            joins.push_back({x.a0 + t, hk, int32_t(nslot), int32_t(parts), stride, t, 0, 0});
+          nslot += parts;
         }
       }
       gs.push_back(std::move(g));
     }
     i = j;
   }
-  w.part_tiles = slots * stride;
+  w.part_tiles = nslot * stride;
   if (w.part_tiles > INT32_MAX / 32) throw Error{CGTP_ERR_UNSUPPORTED, "attention: too many partial tiles"};
 
   int64_t total = 0;
@@ -272,11 +309,15 @@ cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, co
   // samples with one query tile take the kernel whose waves share the queries,
   // those with enough rows the one of 64 rows a wave
   const int wide = wide_forward(at->DP, dtype_size(at->dtype)) ? kWideTiles : INT32_MAX;
-  build(b->fwd, units(qs, ks, 4, [&](int n) { return n > 1 && n < wide; }), 4, g, 2 * kCus, 8);
-  build(b->wide, units(qs, ks, 8, [&](int n) { return n >= wide; }), 8, g, kCus, 8);
-  build(b->few, units(qs, ks, 1, [](int n) { return n == 1; }), 1, g, 4 * kCus, 16);
-  build(b->dq, units(qs, ks, 4, [](int) { return true; }), 4, g, 2 * kCus, 8);
-  build(b->dkv, units(ks, qs, 4, [](int) { return true; }), 4, g, 2 * kCus, 8);
+  // workgroups at once: two a compute unit where registers and shared memory allow
+  const int es = int(dtype_size(at->dtype)), two = 2 * kCus, one = kCus;
+  const int slots = at->DP * es <= 512 ? two : one;
+  build(b->fwd, units(qs, ks, 4, [&](int n) { return n > 1 && n < wide; }), 4, g, slots, 4);
+  build(b->wide, units(qs, ks, 8, [&](int n) { return n >= wide; }), 8, g, two, 4);
+  build(b->few, units(qs, ks, 1, [](int n) { return n == 1; }), 1, g, slots, 8);
+  const int bslots = at->DP * es <= 384 ? two : one;
+  build(b->dq, units(qs, ks, 4, [](int) { return true; }), 4, g, bslots, 4);
+  build(b->dkv, units(ks, qs, 4, [](int) { return true; }), 4, g, bslots, 4);
   return b.release();
 }
 
@@ -325,8 +366,8 @@ void attn_pack_launch(const cgtp_attn_batch_s* b, RowsIn k, RowsIn v, const uint
   const Context c = carve_context(b, context);
   PackArgs p = context_pack(b, k, v, mask);
   p.t[0].row_frags = c.kf;
-  p.t[0].bias = c.bias;
-  p.t[0].flags = c.flags;
+  p.bias = c.bias;
+  p.flags = c.flags;
   p.t[1].col_frags = c.vf;
   b->attn->k.pack(p, s);
   CGTP_CHECK_HIP(hipGetLastError());
@@ -382,7 +423,7 @@ void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn
     PackArgs p = context_pack(b, k, v, mask);
     p.t[0].row_frags = w.kr;
     p.t[0].col_frags = dq ? w.kc : nullptr;
-    p.t[0].bias = w.bias;
+    p.bias = w.bias;
     p.t[1].row_frags = w.vr;
     a->k.pack(p, s);
     CGTP_CHECK_HIP(hipGetLastError());
@@ -400,7 +441,7 @@ void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn
     p.t[1].vec = vec_rows(a, g.p, g.ld);
     p.t[1].row_frags = w.gr;
     p.t[1].col_frags = keys ? w.gc : nullptr;
-    p.t[1].rows_out = w.rows;
+    p.rows_out = w.rows;
     p.tiles = b->qtile_mem.as<Tile>();
     p.table = a->table.as<int4>();
     p.out = out;
@@ -441,25 +482,30 @@ void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn
   x.groups = a->kv_heads;
   if (dq && b->dq.items) {
     x.items = b->dq.item_mem.as<Item>();
-    x.joins = b->dq.join_mem.as<Join>();
     x.part = w.part_q;
     a->k.dq(x, b->dq.items, s);
     CGTP_CHECK_HIP(hipGetLastError());
     if (b->dq.joins) {
-      a->k.grad_join(x, b->dq.joins, true, w.part_q, dq, x.ldq, x.q_quad, s);
+      const GradJoinArgs j{b->dq.join_mem.as<Join>(), x.qtiles, x.table, w.part_q, nullptr, dq, nullptr, x.ldq, a->G,
+                           true, x.q_quad};
+      a->k.grad_join(j, b->dq.joins, 1, s);
       CGTP_CHECK_HIP(hipGetLastError());
     }
   }
   if ((dk || dv) && b->dkv.items) {
     x.items = b->dkv.item_mem.as<Item>();
-    x.joins = b->dkv.join_mem.as<Join>();
     x.part = w.part_k;
     x.part_v = w.part_v;
     a->k.dkv(x, b->dkv.items, s);
     CGTP_CHECK_HIP(hipGetLastError());
     if (b->dkv.joins) {
-      if (dk) a->k.grad_join(x, b->dkv.joins, false, w.part_k, dk, x.ldk, x.k_quad, s);
-      if (dv) a->k.grad_join(x, b->dkv.joins, false, w.part_v, dv, x.ldk, x.k_quad, s);
+      GradJoinArgs j{b->dkv.join_mem.as<Join>(), x.ktiles, x.table, w.part_k, w.part_v, dk, dv, x.ldk, 1, false,
+                     x.k_quad};
+      if (!dk) {
+        j.part0 = j.part1;
+        j.dst0 = j.dst1;
+      }
+      a->k.grad_join(j, b->dkv.joins, dk && dv ? 2 : 1, s);
       CGTP_CHECK_HIP(hipGetLastError());
     }
   }
