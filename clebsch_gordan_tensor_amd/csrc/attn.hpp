@@ -44,6 +44,7 @@ struct PackArgs {
   const float* lse;
   float* rows_out;      // queries and grad_out: lse and delta of every row (else NULL)
   float* bias;          // context: 0 or -inf for every key (else NULL)
+  float* norms;         // context: largest |k|^2 of every tile and head (or NULL)
   int32_t* flags;       // context: whether a tile has a masked or missing key (or NULL)
   int G, heads, groups;  // G = 0: context rows
   int ntiles;
@@ -68,7 +69,7 @@ struct FwdArgs {
   const Tile* qtiles;
   const int4* table;
   const void *q, *kf, *vf;
-  const float* bias;
+  const float *bias, *norms;
   const int32_t* flags;
   void* out;
   float *lse, *part, *part_ml;
@@ -108,7 +109,7 @@ KernelTable kernels_bf16(int dp);
 
 // Whether the forward has a form of 64 query rows a wave (8 tiles an item): its
 // operands and accumulators fit the registers.
-constexpr bool wide_forward(int dp, size_t size) { return size == 2 && dp <= 96; }
+constexpr bool wide_forward(int dp, size_t size) { return size == 2 && dp <= 128; }
 
 // A list of work items on the device with the joins of its splits.
 struct WorkList {

@@ -110,6 +110,13 @@ __device__ __forceinline__ float half_sum(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// max over the lanes of a wave
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int off = 1; off < 64; off *= 2) v = fmaxf(v, lane_fetch(v, (int(threadIdx.x & 63) ^ off) << 2));
+  return v;
+}
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // Unit u of a packed tile, this lane's 16 bytes.
@@ -132,6 +139,19 @@ __device__ __forceinline__ void copy_unit(const T* tile, int u, int lane, u32x4*
       (__attribute__((address_space(3))) void*)(dst), 16, 0, 0);
 }
 __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// The end of a turn: all but the last N copies of this wave have arrived, its
+// reads of shared memory are done, and the other waves have come as far. (Not
+// __syncthreads(), which waits for every copy.)
+template <int N>
+__device__ __forceinline__ void turn_end() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+// The lane, computed where it is needed (so that it holds no register meanwhile).
+__device__ __forceinline__ int lane_id() {
+  return int(__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u)));
+}
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(int(threadIdx.x) / 64); }
 
 // Element address of head-vector element d of query row (token, head) or of
@@ -248,6 +268,18 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
     if (a.t[0].col_frags) *reinterpret_cast<u32x4*>(&sh[0][r * LD + d0]) = v0[c];
     if (a.t[1].col_frags) *reinterpret_cast<u32x4*>(&sh[1][r * LD + d0]) = v1[c];
   }
+  if (a.norms) {
+    // |k|^2 of every row, the largest of the tile below
+    float n2 = 0.0f;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) {
+      T tv[VE];
+      __builtin_memcpy(tv, &v0[c], 16);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) n2 += to_acc<float>(tv[j]) * to_acc<float>(tv[j]);
+    }
+    red[r][tid % 8] = n2;
+  }
   if (grads) {
     float partial = 0.0f;
 #pragma unroll
@@ -267,6 +299,13 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
     for (int k = 0; k < 8; ++k) d += red[r][k];
     a.rows_out[at * 64 + r] = in && lse > -INFINITY ? lse * 1.44269504088896341f : INFINITY;
     a.rows_out[at * 64 + 32 + r] = d;
+  }
+  if (a.norms && wave == 0) {
+    float n2 = 0.0f;
+    for (int k = 0; k < 8; ++k) n2 += red[lane % 32][k];
+    const bool nan = __any(n2 != n2);
+    n2 = wave_max(n2);
+    if (lane == 0) a.norms[at] = nan ? INFINITY : n2;
   }
   if (a.bias && hk == 0 && tid < 32) {
     const bool seen = tid < tl.n && (a.mask == nullptr || a.mask[tl.row0 + tid] != 0);
@@ -304,29 +343,39 @@ struct Running {
   f32x16 o[DT];
 };
 
-// Turns a tile's products q.k into weights exp2(scale2 q.k - m). The reference
-// follows the maximum only when that grows by more than 2^8: the weights stay
-// below 2^8 (their sum is fp32), and most tiles need no rescaling of O. scale2 is
-// positive, so the maximum is taken before scaling.
-template <int DT>
-__device__ __forceinline__ void fold_scores(Running<DT>& st, f32x16& s, float scale2) {
+// The largest score of a lane's query in a tile (log2 domain; scale2 is positive,
+// so the maximum is taken before scaling).
+__device__ __forceinline__ float top_score(const f32x16& s, float scale2) {
   float mx = s[0];
 #pragma unroll
   for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
-  mx = half_max(mx) * scale2;
-  if (__any(mx > st.m + 8.0f)) {
-    const float mn = fmaxf(st.m, mx);
+  return half_max(mx) * scale2;
+}
+
+// Moves the reference up to a tile's top score. It follows only when that grows
+// by more than 2^8: the weights stay below 2^8 (their sum is fp32), and most
+// tiles need no rescaling of O.
+template <int DT>
+__device__ __forceinline__ void raise_reference(Running<DT>& st, float top) {
+  if (__any(top > st.m + 8.0f)) {
+    const float mn = fmaxf(st.m, top);
     const float alpha = mn == -INFINITY ? 1.0f : exp2_fast(st.m - mn);
     st.m = mn;
     st.l *= alpha;
 #pragma unroll
     for (int d = 0; d < DT; ++d) st.o[d] *= alpha;
   }
-  const float ref = st.m == -INFINITY ? 0.0f : st.m;
+}
+
+// Turns a tile's products q.k into weights exp2(scale2 q.k - m); m is 0 unless
+// MOVING.
+template <bool MOVING, int DT>
+__device__ __forceinline__ void weigh(Running<DT>& st, f32x16& s, float scale2) {
+  const float ref = !MOVING || st.m == -INFINITY ? 0.0f : st.m;
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    s[i] = exp2_fast(fmaf(s[i], scale2, -ref));
+    s[i] = exp2_fast(MOVING ? fmaf(s[i], scale2, -ref) : s[i] * scale2);
     sum += s[i];
   }
   st.l += sum;
@@ -376,9 +425,9 @@ constexpr int dkv_forms(int part) { return part == 0 ? 4 : part == 1 ? 2 : 3; }
 
 // Writes a wave's result: final rows, or an unnormalised part of a split.
 template <typename T, int DP>
-__device__ __forceinline__ void finish(const FwdArgs& a, const Item& it, const Tile& tl, int tile_in_item, int lane,
+__device__ __forceinline__ void finish(const FwdArgs& a, const Item& it, const Tile& tl, int tile_in_item,
                                        const Running<DP / 32>& st) {
-  const int n = lane % 32, h = lane / 32;
+  const int lane = lane_id(), n = lane % 32, h = lane / 32;
   const float l = half_sum(st.l);
   if (it.slot >= 0) {
     const int64_t r = (int64_t(it.slot) * it.stride + tile_in_item) * 32 + n;
@@ -415,100 +464,160 @@ __device__ __forceinline__ void finish(const FwdArgs& a, const Item& it, const T
     a.lse[int64_t(token) * a.heads + head] = l > 0.0f || l != l ? (st.m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// Four waves of RT x 32 query rows share the keys through shared memory. A wave's
-// turn t computes the scores of tile t + 1 (matrix cores) next to the softmax of
-// tile t (vector units), then adds tile t's values; the tiles after that are on
-// their way to shared memory meanwhile. Bound: matrix cores and vector units
-// together (16 exponentials a lane and tile); RT = 2 halves the operand reads
-// from shared memory per product, which else take as long as the products.
+// Tiles of the keys and of the values in shared memory: R - 1 turns for a copy to
+// arrive. Three where that leaves room for two workgroups a compute unit.
+template <typename T, int DP>
+constexpr int fwd_ring() {
+  return 6 * Dims<T, DP>::UNITS < 80 ? 3 : 2;
+}
+
+// The square of a bound of all scores (log2 domain) of a wave's queries against
+// the tiles of an item: |q.k| <= |q| |k|. NaN where a row holds one.
 template <typename T, int DP, int RT>
-__global__ __launch_bounds__(kThreads, lds_waves(4 * Dims<T, DP>::UNITS)) void fwd_kernel(FwdArgs a) {
+__device__ __forceinline__ float score_bound2(const FwdArgs& a, const Item& it, int lane,
+                                              const typename Op<T>::Frag (&q)[RT][Dims<T, DP>::KSTEPS]) {
+  using D = Dims<T, DP>;
+  float qn = 0.0f, kn = 0.0f;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    float n2 = 0.0f;
+#pragma unroll
+    for (int u = 0; u < D::KSTEPS; ++u)
+#pragma unroll
+      for (int j = 0; j < D::VE; ++j) {
+        const float e = static_cast<float>(q[r][u][j]);
+        n2 += e * e;
+      }
+    n2 = half_sum(n2);
+    qn = n2 > qn || n2 != n2 ? n2 : qn;
+  }
+  for (int t = it.b0 + lane; t < it.b1; t += 64) {
+    const float n2 = a.norms[int64_t(t) * a.groups + it.hk];
+    kn = n2 > kn || n2 != n2 ? n2 : kn;
+  }
+  const bool nan = __any(qn != qn || kn != kn);
+  return nan ? INFINITY : wave_max(qn) * wave_max(kn) * a.scale2 * a.scale2;
+}
+
+// Scores whose size is bounded by 2^kBound need no running maximum: with the
+// reference 0 their exponentials lie within 2^-60 .. 2^60, sums of 2^31 of them
+// stay far inside fp32, and bf16 has fp32's exponent range, so nothing is lost.
+constexpr float kBound = 60.0f;
+
+// Four waves of RT x 32 query rows share the keys through shared memory; the tiles
+// of the next turns are on their way there while one is worked on. Bound: matrix
+// cores, vector units (16 exponentials a lane and tile) and shared memory
+// together; RT = 2 halves the operand reads from shared memory per product,
+// which with the copies into it take 1.5 times as long as the products else. Two
+// paths: scores bounded beforehand by the rows' norms (what normalised features
+// give) go without maximum, branch and rescaling; others keep a running maximum
+// (for RT = 2 one 32-row half after the other).
+template <typename T, int DP, int RT>
+__global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T, DP>::UNITS)) void fwd_kernel(
+    FwdArgs a) {
   using D = Dims<T, DP>;
   using Frag = typename Op<T>::Frag;
-  __shared__ u32x4 kb[2][D::UNITS * 64], vb[2][D::UNITS * 64];
-  const Item it = a.items[blockIdx.x];
+  constexpr int R = fwd_ring<T, DP>();
+  __shared__ u32x4 kb[R][D::UNITS * 64], vb[R][D::UNITS * 64];
+  __shared__ float bounds[4];
+  const Item it = ldc(a.items + blockIdx.x);
   if (it.tiles == 0) return;
   const int lane = int(threadIdx.x) % 64, wave = wave_id(), h = lane / 32;
   const int mine = min(max(it.tiles - wave * RT, 0), RT);  // query tiles of this wave
+  const int n = it.b1 - it.b0;
+  // tile t of the keys and of the values, a quarter by each wave
+  const auto copy = [&](int t, int slot) {
+    const int64_t at = (int64_t(min(it.b0 + t, it.b1 - 1)) * a.groups + it.hk) * D::TILE;
+#pragma unroll
+    for (int k = 0; k < D::UNITS / 2; ++k) {
+      const int u = k * 4 + wave;
+      if (u < D::UNITS) copy_unit(static_cast<const T*>(a.kf) + at, u, lane, &kb[slot][u * 64]);
+      else copy_unit(static_cast<const T*>(a.vf) + at, u - D::UNITS, lane, &vb[slot][(u - D::UNITS) * 64]);
+    }
+  };
+  if (n > 0)
+#pragma unroll
+    for (int t = 0; t + 1 < R; ++t) copy(t, t);
   Frag q[RT][D::KSTEPS];
   Running<D::DT> st[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    load_queries<T, DP>(a, a.qtiles[it.a0 + (r < mine ? wave * RT + r : 0)], it.hk, lane, q[r]);
+    load_queries<T, DP>(a, ldc(a.qtiles + it.a0 + (r < mine ? wave * RT + r : 0)), it.hk, lane, q[r]);
 #pragma unroll
     for (int d = 0; d < D::DT; ++d) st[r].o[d] = zero16();
   }
-  // tile kt of the keys and tile vt of the values, a quarter by each wave
-  const auto copy = [&](int kt, u32x4* kdst, int vt, u32x4* vdst) {
-    const T* kf = static_cast<const T*>(a.kf) + (int64_t(kt) * a.groups + it.hk) * D::TILE;
-    const T* vf = static_cast<const T*>(a.vf) + (int64_t(vt) * a.groups + it.hk) * D::TILE;
+  const float b2 = score_bound2<T, DP, RT>(a, it, lane, q);
+  if (lane == 0) bounds[wave] = b2;
+  turn_end<0>();
+  bool bounded = true;
 #pragma unroll
-    for (int k = 0; k < D::UNITS / 2; ++k) {
-      const int u = k * 4 + wave;
-      if (u < D::UNITS) copy_unit(kf, u, lane, kdst + u * 64);
-      else copy_unit(vf, u - D::UNITS, lane, vdst + (u - D::UNITS) * 64);
-    }
-  };
-  f32x16 s[RT];
-  const auto scores = [&](const u32x4* kt, f32x16 (&o)[RT]) {
+  for (int w = 0; w < 4; ++w) bounded = bounded && bounds[w] <= kBound * kBound;
+
+  // query tiles R0 .. R0 + N - 1 of every wave over all keys; tiles 0 .. R - 2 are there
+  const auto run = [&](auto first, auto count, auto moving) {
+    constexpr int R0 = decltype(first)::value, N = decltype(count)::value;
+    constexpr bool kMoving = decltype(moving)::value;
+    if (!kMoving)
 #pragma unroll
-    for (int r = 0; r < RT; ++r) o[r] = zero16();
+      for (int r = R0; r < R0 + N; ++r) st[r].m = 0.0f;
+    int slot = 0;
+    for (int t = 0; t < n; ++t) {
+      const int tile = it.b0 + t;
+      copy(t + R - 1, slot == 0 ? R - 1 : slot - 1);
+      if (mine > R0) {
+        f32x16 s[N];
 #pragma unroll
-    for (int u = 0; u < D::KSTEPS; ++u) {
-      const Frag kf = as_frag<Frag>(kt[u * 64 + lane]);
+        for (int r = 0; r < N; ++r) s[r] = zero16();
 #pragma unroll
-      for (int r = 0; r < RT; ++r) o[r] = Op<T>::mma(kf, q[r][u], o[r]);
-    }
-  };
-  const auto turn = [&](int t, auto last) {
-    constexpr bool kLast = decltype(last)::value;
-    const int tile = it.b0 + t;
-    if (!kLast) copy(min(tile + 2, it.b1 - 1), kb[t & 1], tile + 1, vb[(t + 1) & 1]);
-    if (mine > 0) {
-      if (ldc(a.flags + tile))
+        for (int u = 0; u < D::KSTEPS; ++u) {
+          const Frag kf = as_frag<Frag>(kb[slot][u * 64 + lane]);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) mask_scores(s[r], a.bias + int64_t(tile) * 32, h);
-      f32x16 next[RT];
-      if (!kLast) scores(kb[(t + 1) & 1], next);
-      Frag p[RT][D::FR];
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        fold_scores(st[r], s[r], a.scale2);
-#pragma unroll
-        for (int f = 0; f < D::FR; ++f) p[r][f] = Op<T>::from_acc(s[r], f);
-      }
-#pragma unroll
-      for (int d = 0; d < D::DT; ++d)
-#pragma unroll
-        for (int f = 0; f < D::FR; ++f) {
-          const Frag vf = as_frag<Frag>(vb[t & 1][(d * D::FR + f) * 64 + lane]);
-#pragma unroll
-          for (int r = 0; r < RT; ++r) st[r].o[d] = Op<T>::mma(vf, p[r][f], st[r].o[d]);
+          for (int r = 0; r < N; ++r) s[r] = Op<T>::mma(kf, q[R0 + r][u], s[r]);
         }
-      if (!kLast)
+        if (ldc(a.flags + tile))
 #pragma unroll
-        for (int r = 0; r < RT; ++r) s[r] = next[r];
+          for (int r = 0; r < N; ++r) mask_scores(s[r], a.bias + int64_t(tile) * 32, h);
+        Frag p[N][D::FR];
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+          if (kMoving) raise_reference(st[R0 + r], top_score(s[r], a.scale2));
+          weigh<kMoving>(st[R0 + r], s[r], a.scale2);
+#pragma unroll
+          for (int f = 0; f < D::FR; ++f) p[r][f] = Op<T>::from_acc(s[r], f);
+        }
+#pragma unroll
+        for (int d = 0; d < D::DT; ++d)
+#pragma unroll
+          for (int f = 0; f < D::FR; ++f) {
+            const Frag vf = as_frag<Frag>(vb[slot][(d * D::FR + f) * 64 + lane]);
+#pragma unroll
+            for (int r = 0; r < N; ++r) st[R0 + r].o[d] = Op<T>::mma(vf, p[r][f], st[R0 + r].o[d]);
+          }
+      }
+      slot = slot + 1 == R ? 0 : slot + 1;
+      turn_end<(R - 2) * D::UNITS / 2>();
     }
-    if (!kLast) {
-      wait_copies();
-      __syncthreads();
-    }
+    wait_copies();  // none may land after the workgroup's end
   };
-  const int n = it.b1 - it.b0;
+  using zero = std::integral_constant<int, 0>;
+  using one = std::integral_constant<int, 1>;
   if (n > 0) {
-    // (the second copy's values are tile 1's, which turn 0 copies again)
-    copy(it.b0, kb[0], it.b0, vb[0]);
-    copy(min(it.b0 + 1, it.b1 - 1), kb[1], min(it.b0 + 1, it.b1 - 1), vb[1]);
-    wait_copies();
-    __syncthreads();
-    if (mine > 0) scores(kb[0], s);
-    __syncthreads();
-    for (int t = 0; t + 1 < n; ++t) turn(t, std::false_type{});
-    turn(n - 1, std::true_type{});
+    if (bounded) {
+      run(zero{}, std::integral_constant<int, RT>{}, std::false_type{});
+    } else {
+      run(zero{}, one{}, std::true_type{});
+      if constexpr (RT == 2) {
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t + 1 < R; ++t) copy(t, t);
+        turn_end<0>();
+        run(one{}, one{}, std::true_type{});
+      }
+    }
   }
 #pragma unroll
   for (int r = 0; r < RT; ++r)
-    if (r < mine) finish<T, DP>(a, it, a.qtiles[it.a0 + wave * RT + r], wave * RT + r, lane, st[r]);
+    if (r < mine) finish<T, DP>(a, it, ldc(a.qtiles + it.a0 + wave * RT + r), wave * RT + r, st[r]);
 }
 
 // At most 32 query rows against a long context (single tokens): the four waves
@@ -549,7 +658,8 @@ __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void fwd_few_ke
       for (int u = 0; u < D::KSTEPS; ++u) sc = Op<T>::mma(as_frag<Frag>(k[u]), q[u], sc);
     }
     if (ldc(a.flags + t)) mask_scores(sc, a.bias + int64_t(t) * 32, h);
-    fold_scores(st, sc, a.scale2);
+    raise_reference(st, top_score(sc, a.scale2));
+    weigh<true>(st, sc, a.scale2);
     Frag p[D::FR];
 #pragma unroll
     for (int f = 0; f < D::FR; ++f) p[f] = Op<T>::from_acc(sc, f);
@@ -602,7 +712,7 @@ __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void fwd_few_ke
   }
   if (wave == 0) {
     st.l = ml[0][1][lane] + ml[2][1][lane] + (ml[1][1][lane] + ml[3][1][lane]);
-    finish<T, DP>(a, it, tl, 0, lane, st);
+    finish<T, DP>(a, it, tl, 0, st);
   }
 }
 

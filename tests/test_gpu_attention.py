@@ -109,19 +109,43 @@ def test_masks_with_nan_and_inf_in_masked_places(dtype, nq):
         assert torch.all(dk[~mask] == 0) and torch.all(dv[~mask] == 0)
 
 
-def test_large_scores_do_not_overflow():
-    irreps, nq, nk = "32x0e", [50], [200]
-    attn = layers.CrossAttention(irreps, 2, dtype="f32")
-    q, k, v, g = inputs(irreps, 2, 2, nq, nk, "f32")
+@pytest.mark.parametrize("dtype,rows,heads,irreps", [("f32", 50, 2, "32x0e"), ("bf16", 300, 2, "32x0e"),
+                                                     ("bf16", 300, 1, "32x0e+32x1o"), ("bf16", 90, 1, "160x0e"),
+                                                     ("bf16", 1, 2, "32x0e")])
+def test_large_scores_do_not_overflow(dtype, rows, heads, irreps):
+    nq, nk = [rows, 20], [200, 70]
+    attn = layers.CrossAttention(irreps, heads, dtype=dtype)
+    q, k, v, g = inputs(irreps, heads, heads, nq, nk, dtype)
     b = attn.batch(layers.Samples(ptr_of(nq)), layers.Samples(ptr_of(nk)))
     # scores of some hundreds, rising along the context: every tile moves the running maximum
-    k = k + 8 * torch.arange(200, device="cuda")[:, None] / 200
+    k = k + (8 * torch.arange(270, device="cuda")[:, None] / 200).to(k.dtype)
     q = q + 20
+    q[:3] = -q[:3]                                    # and falling for some rows
     out, lse = attn.forward(b, q, k, v, need_lse=True)
     torch.cuda.synchronize()
-    ro, rl = ol.attn_forward(irreps, 2, 2, ptr_of(nq), ptr_of(nk), host(q), host(k), host(v), None, attn.scale)
-    # a score of size s carries s * 2^-23 of rounding from each of its sums' steps: some 1e-4 of a weight at s = 700
-    assert rel_err(host(out), ro) <= 2e-3 and np.abs(host(lse) - rl).max() <= 2e-3
+    ro, rl = ol.attn_forward(irreps, heads, heads, ptr_of(nq), ptr_of(nk), host(q), host(k), host(v), None, attn.scale)
+    # a score of size s carries s * 2^-23 of rounding from each of its sums' steps: some 1e-4 of a weight at s = 1000
+    tol = 2e-3 if dtype == "f32" else TOL[dtype]
+    assert rel_err(host(out), ro) <= tol and np.abs(host(lse) - rl).max() <= 4e-3
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_negative_and_zero_scale(dtype):
+    irreps, nq, nk = "32x0e+8x1o", [40, 300, 1], [70, 33, 100]
+    attn = layers.CrossAttention(irreps, 4, dtype=dtype)
+    q, k, v, g = inputs(irreps, 4, 4, nq, nk, dtype)
+    b = attn.batch(layers.Samples(ptr_of(nq)), layers.Samples(ptr_of(nk)))
+    for scale in (-0.4, 0.0, 30.0):
+        out, lse = attn.forward(b, q, k, v, scale=scale, need_lse=True)
+        grads = attn.backward(b, q, k, v, out, lse, g, scale=scale)
+        torch.cuda.synchronize()
+        args = (irreps, 4, 4, ptr_of(nq), ptr_of(nk), host(q), host(k), host(v), None, scale)
+        ro, rl = ol.attn_forward(*args)
+        assert rel_err(host(out), ro) <= (TOL[dtype] if scale < 1 else max(TOL[dtype], 2e-3))
+        if scale > 1:
+            continue                                  # (scores of hundreds: as above)
+        for x, y in zip(grads, ol.attn_backward(*args, host(g))):
+            assert np.abs(host(x) - y).max() <= TOL[dtype] * max(np.abs(y).max(), 0.1)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
