@@ -13,6 +13,8 @@
 // are in flight. A workgroup handles one block, so that every lane of a wave
 // has the same component count and neighbouring lanes read neighbouring 16-byte
 // pieces of a component's channels.
+#include <algorithm>
+
 #include "device_util.hpp"
 #include "layers.hpp"
 

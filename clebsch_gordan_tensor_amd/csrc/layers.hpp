@@ -61,11 +61,12 @@ struct alignas(16) NormStrip {
 }  // namespace cgtp
 
 struct cgtp_samples_s {
-  int64_t S = 0, rows = 0, nchunk = 0;
+  int64_t S = 0, rows = 0, nchunk = 0, longest = 0;
   std::vector<int64_t> ptr;
   std::vector<int32_t> sample_chunk;  // host copy: first chunk of each sample, [S + 1]
   int device = 0;
   cgtp::DevMem chunks, first;         // RowChunk [nchunk]; int32 [S + 1] as sample_chunk
+  cgtp::DevMem first_row;             // int32 [S + 1] as ptr
 };
 
 struct cgtp_norm_s {
@@ -76,10 +77,12 @@ struct cgtp_norm_s {
   cgtp_dtype dtype = CGTP_F32;
   int device = 0;
   // channels per lane: the widest access up to 16 bytes that no group straddles;
-  // strips for that width and for single channels (misaligned tensors)
+  // strips for that width and for single channels (misaligned tensors), then the
+  // same as narrow strips (about 128 bytes of channels)
   int vec = 1;
-  int nstrip[2] = {0, 0};
-  cgtp::DevMem strips[2];
+  int64_t narrow_row = 0;  // most elements of a narrow strip in one row
+  int nstrip[4] = {0, 0, 0, 0};
+  cgtp::DevMem strips[4];
 };
 
 struct cgtp_dropout_s {
@@ -91,7 +94,7 @@ struct cgtp_dropout_s {
 
 namespace cgtp {
 
-size_t norm_ws_bytes(const cgtp_norm_s* n, const cgtp_samples_s* sm);
+size_t norm_ws_bytes(const cgtp_norm_s* n, const cgtp_samples_s* sm, bool backward);
 void norm_forward_launch(const cgtp_norm_s* n, const cgtp_samples_s* sm, const void* x, const void* w, const void* b,
                          void* y, void* stats, void* ws, hipStream_t s);
 void norm_backward_launch(const cgtp_norm_s* n, const cgtp_samples_s* sm, const void* x, const void* w, const void* b,

@@ -85,11 +85,11 @@ void need_batch(const cgtp_attn_batch_s* b, double scale) {
 }
 
 // Rows in a run of the norm: long enough that a workgroup's work outweighs its
-// reduction, short enough that the runs of all samples fill the device.
-int64_t chunk_rows(int64_t rows) {
-  int64_t r = 32;
-  while (r < 256 && rows / r > 512) r *= 2;
-  return r;
+// reduction, short enough that the runs fill the device; at most 512 runs a
+// sample, since every run joins all of its sample's partial moments.
+int64_t chunk_rows(int64_t rows, int64_t sample_rows) {
+  const int64_t r = rows <= 16384 ? 32 : 64;
+  return std::max(r, (sample_rows + 511) / 512);
 }
 
 cgtp_samples_s* build_samples(int64_t S, const int64_t* ptr) {
@@ -101,10 +101,10 @@ cgtp_samples_s* build_samples(int64_t S, const int64_t* ptr) {
   sm->S = S;
   sm->rows = ptr[S];
   sm->ptr.assign(ptr, ptr + S + 1);
-  const int64_t R = chunk_rows(sm->rows);
   std::vector<RowChunk> ch;
   for (int64_t s = 0; s < S; ++s) {
-    const int64_t a = ptr[s], n = ptr[s + 1] - a, k = (n + R - 1) / R;
+    const int64_t a = ptr[s], n = ptr[s + 1] - a, R = chunk_rows(sm->rows, n), k = (n + R - 1) / R;
+    sm->longest = std::max(sm->longest, n);
     const int32_t c0 = int32_t(ch.size());
     sm->sample_chunk.push_back(c0);
     // even cuts, so that no run is much shorter than the others
@@ -116,26 +116,38 @@ cgtp_samples_s* build_samples(int64_t S, const int64_t* ptr) {
   sm->nchunk = int64_t(ch.size());
   sm->device = current_device();
   sm->chunks.upload(ch.data(), ch.size() * sizeof(RowChunk));
+  const std::vector<int32_t> rows(ptr, ptr + S + 1);
+  sm->first_row.upload(rows.data(), rows.size() * sizeof(int32_t));
   sm->first.upload(sm->sample_chunk.data(), sm->sample_chunk.size() * sizeof(int32_t));
   return sm.release();
 }
 
 // Lane width and strips of a norm: lanes never straddle a group, a strip is as
-// many whole groups as 256 lanes hold (at least one).
+// many whole groups as 256 lanes hold (at least one), a narrow one as many as 128
+// bytes hold.
 void norm_strips(cgtp_norm_s* n) {
   n->vec = 16 / int(dtype_size(n->dtype));
   for (const RowBlock& b : n->row.blocks)
     while ((b.mul / n->groups) % n->vec != 0) n->vec /= 2;
-  for (int k = 0; k < 2; ++k) {
-    const int vec = k == 0 ? n->vec : 1;
+  const int64_t es = int64_t(dtype_size(n->dtype));
+  for (int k = 0; k < 4; ++k) {
+    const int vec = k % 2 == 0 ? n->vec : 1;
     std::vector<NormStrip> st;
     for (size_t i = 0; i < n->row.blocks.size(); ++i) {
       const RowBlock& b = n->row.blocks[i];
       const int G = int(n->groups), cg = b.mul / G;
-      const int per = std::min(G, std::max(1, 256 * vec / cg));
+      int per = std::min(G, std::max(1, 256 * vec / cg));
+      if (k >= 2) {
+        per = std::min(per, std::max(1, int(128 / (cg * es))));
+        n->narrow_row = std::max<int64_t>(n->narrow_row, int64_t(per) * cg * b.nc);
+      }
       for (int g = 0; g < G; g += per)
         st.push_back({b.off, b.nc, b.mul, b.chan, b.bias, cg, g, std::min(per, G - g), int32_t(i) * G + g, 0, 0, 0});
     }
+    // the workgroups with the most work first
+    std::stable_sort(st.begin(), st.end(), [](const NormStrip& a, const NormStrip& b) {
+      return int64_t(a.nc) * a.ng * a.cg > int64_t(b.nc) * b.ng * b.cg;
+    });
     if (st.size() > 65535) throw Error{CGTP_ERR_UNSUPPORTED, "too many groups"};
     n->nstrip[k] = int(st.size());
     n->strips[k].upload(st.data(), st.size() * sizeof(NormStrip));
@@ -203,10 +215,10 @@ cgtp_status cgtp_norm_query(cgtp_norm norm, int64_t* dim, int64_t* channels, int
   });
 }
 
-cgtp_status cgtp_norm_workspace_size(cgtp_norm norm, cgtp_samples samples, size_t* bytes) {
+cgtp_status cgtp_norm_workspace_size(cgtp_norm norm, cgtp_samples samples, int backward, size_t* bytes) {
   return guarded([&] {
     need(norm != nullptr && samples != nullptr && bytes != nullptr, "NULL argument");
-    *bytes = norm_ws_bytes(norm, samples);
+    *bytes = norm_ws_bytes(norm, samples, backward != 0);
   });
 }
 
@@ -217,7 +229,7 @@ cgtp_status cgtp_norm_forward(cgtp_norm norm, cgtp_samples samples, const void* 
     need_device(norm->device, "the norm");
     need_device(samples->device, "the samples");
     need(samples->rows == 0 || (x && y), "NULL tensor");
-    need_ws(ws, ws_bytes, norm_ws_bytes(norm, samples), "norm forward");
+    need_ws(ws, ws_bytes, norm_ws_bytes(norm, samples, false), "norm forward");
     norm_forward_launch(norm, samples, x, weight, bias, y, stats, ws, as_stream(stream));
   });
 }
@@ -230,7 +242,7 @@ cgtp_status cgtp_norm_backward(cgtp_norm norm, cgtp_samples samples, const void*
     need_device(norm->device, "the norm");
     need_device(samples->device, "the samples");
     need(samples->rows == 0 || (x && grad_y && stats), "NULL tensor");
-    need_ws(ws, ws_bytes, norm_ws_bytes(norm, samples), "norm backward");
+    need_ws(ws, ws_bytes, norm_ws_bytes(norm, samples, true), "norm backward");
     if (!grad_x && !grad_weight && !grad_bias) return;
     norm_backward_launch(norm, samples, x, weight, bias, stats, grad_y, grad_x, grad_weight, grad_bias, ws,
                          as_stream(stream));

@@ -11,7 +11,7 @@ import ctypes
 
 import numpy as np
 
-from .cgtp import (_DT, _check, _lib, _need, _ptr, _stream, _torch, _torch_dtype, _vp, _ws_bytes, F64)
+from .cgtp import _DT, _check, _lib, _need, _torch, _torch_dtype, _vp, _ws_bytes, F64
 
 _i64, _size = ctypes.c_int64, ctypes.c_size_t
 _i64p, _sizep, _vpp = ctypes.POINTER(_i64), ctypes.POINTER(_size), ctypes.POINTER(_vp)
@@ -23,7 +23,7 @@ _SIGS = {
     "cgtp_norm_create": [ctypes.c_char_p, _i64, ctypes.c_int, _dbl, ctypes.c_int, _vpp],
     "cgtp_norm_destroy": [_vp],
     "cgtp_norm_query": [_vp, _i64p, _i64p, _i64p, _i64p],
-    "cgtp_norm_workspace_size": [_vp, _vp, _sizep],
+    "cgtp_norm_workspace_size": [_vp, _vp, ctypes.c_int, _sizep],
     "cgtp_norm_forward": [_vp] * 8 + [_size, _vp],
     "cgtp_norm_backward": [_vp] * 11 + [_size, _vp],
     "cgtp_dropout_create": [ctypes.c_char_p, ctypes.c_int, _vpp],
@@ -58,20 +58,51 @@ def _acc_dtype(code):
     return t.float64 if code == F64 else t.float32
 
 
-def _workspace(ws, nbytes, device):
-    """(tensor, bytes) of the caller's workspace or a new one."""
+_raw_stream = None
+
+
+def _stream_of(t):
+    """The current stream's handle on t's device (the plain number: building a
+    torch Stream object costs as much as a small kernel)."""
+    global _raw_stream
+    if _raw_stream is None:
+        torch = _torch()
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream(t.get_device())
+
+
+def _tensor(t, shape, dtype, name):
+    """t's device pointer, after _need's checks (its own path only where one fails)."""
+    if t is not None and t.is_cuda and t.shape == shape and t.dtype is dtype and t.is_contiguous():
+        return t.data_ptr()
+    return _need(t, shape, dtype, name).data_ptr()
+
+
+def _ws(ws, nbytes, device):
+    """(workspace kept alive, pointer, bytes): the caller's or a new one."""
     if ws is None:
-        ws = _torch().empty(max(nbytes, 1), dtype=_torch().uint8, device=device)
-    return ws, _ws_bytes(ws)
+        if nbytes == 0:
+            return None, 0, 0
+        ws = _torch().empty(nbytes, dtype=_torch().uint8, device=device)
+        return ws, ws.data_ptr(), nbytes
+    return ws, ws.data_ptr(), _ws_bytes(ws)
 
 
 class _Handle:
     """An opaque handle of the library, destroyed with this object."""
 
     _h = None
+    _dtype = None
 
     def _own(self, handle, destroy):
         self._h, self._destroy = handle, getattr(_lib, destroy)
+
+    @property
+    def torch_dtype(self):
+        if self._dtype is None:
+            self._dtype = _torch_dtype(self.dtype_code)
+        return self._dtype
 
     def __del__(self):
         if self._h and _lib is not None:
@@ -112,62 +143,60 @@ class GroupNorm(_Handle):
         v = [_i64() for _ in range(4)]
         _check(_lib.cgtp_norm_query(h, *[ctypes.byref(a) for a in v]), "cgtp_norm_query")
         self.dim, self.channels, self.biases, self.num_groups = (a.value for a in v)
+        self._acc = _acc_dtype(self.dtype_code)
+        self._sized, self._sizes = None, None
 
-    @property
-    def torch_dtype(self):
-        return _torch_dtype(self.dtype_code)
-
-    def workspace_size(self, samples):
-        n = _size()
-        _check(_lib.cgtp_norm_workspace_size(self._h, samples._h, ctypes.byref(n)), "cgtp_norm_workspace_size")
-        return n.value
+    def workspace_size(self, samples, backward=False):
+        # sizes of the layout last used: layouts repeat from call to call
+        if self._sized is not samples:
+            n, sizes = _size(), []
+            for k in range(2):
+                _check(_lib.cgtp_norm_workspace_size(self._h, samples._h, k, ctypes.byref(n)),
+                       "cgtp_norm_workspace_size")
+                sizes.append(n.value)
+            self._sized, self._sizes = samples, sizes
+        return self._sizes[1 if backward else 0]
 
     def _affine(self, weight, bias):
-        if weight is not None:
-            _need(weight, (self.channels,), self.torch_dtype, "weight")
-        if bias is not None:
-            _need(bias, (self.biases,), self.torch_dtype, "bias")
+        dt = self.torch_dtype
+        return (None if weight is None else _tensor(weight, (self.channels,), dt, "weight"),
+                None if bias is None else _tensor(bias, (self.biases,), dt, "bias"))
 
     def forward(self, samples, x, weight=None, bias=None, out=None, stats=None, ws=None):
         """(y, stats): the normalised rows and the [S, num_groups, 2] means and
         reciprocal deviations that the backward takes."""
         torch = _torch()
-        dt = self.torch_dtype
-        _need(x, (samples.rows, self.dim), dt, "x")
-        self._affine(weight, bias)
+        dt, shape = self.torch_dtype, (samples.rows, self.dim)
+        px = _tensor(x, shape, dt, "x")
+        pw, pb = self._affine(weight, bias)
         if out is None:
             out = torch.empty_like(x)
-        _need(out, (samples.rows, self.dim), dt, "out")
-        shape = (samples.S, self.num_groups, 2)
+        po = _tensor(out, shape, dt, "out")
+        sshape, adt = (samples.S, self.num_groups, 2), self._acc
         if stats is None:
-            stats = torch.empty(shape, dtype=_acc_dtype(self.dtype_code), device=x.device)
-        _need(stats, shape, _acc_dtype(self.dtype_code), "stats")
-        ws, nws = _workspace(ws, self.workspace_size(samples), x.device)
-        _check(_lib.cgtp_norm_forward(self._h, samples._h, _ptr(x), _ptr(weight), _ptr(bias), _ptr(out), _ptr(stats),
-                                      _ptr(ws), nws, _stream(x)), "cgtp_norm_forward")
+            stats = torch.empty(sshape, dtype=adt, device=x.device)
+        ps = _tensor(stats, sshape, adt, "stats")
+        ws, pws, nws = _ws(ws, self.workspace_size(samples), x.device)
+        _check(_lib.cgtp_norm_forward(self._h, samples._h, px, pw, pb, po, ps, pws, nws, _stream_of(x)),
+               "cgtp_norm_forward")
         return out, stats
 
     def backward(self, samples, x, weight, bias, stats, grad_y, need=(True, True, True), out=(None, None, None),
                  ws=None):
         """(grad_x, grad_weight, grad_bias)."""
         torch = _torch()
-        dt = self.torch_dtype
-        _need(x, (samples.rows, self.dim), dt, "x")
-        _need(grad_y, (samples.rows, self.dim), dt, "grad_y")
-        _need(stats, (samples.S, self.num_groups, 2), _acc_dtype(self.dtype_code), "stats")
-        self._affine(weight, bias)
-        shapes = [(samples.rows, self.dim), (self.channels,), (self.biases,)]
-        res = []
-        for k in range(3):
-            if not need[k]:
-                res.append(None)
-                continue
-            t = out[k] if out[k] is not None else torch.empty(shapes[k], dtype=dt, device=x.device)
-            res.append(_need(t, shapes[k], dt, "grad"))
-        ws, nws = _workspace(ws, self.workspace_size(samples), x.device)
-        _check(_lib.cgtp_norm_backward(self._h, samples._h, _ptr(x), _ptr(weight), _ptr(bias), _ptr(stats),
-                                       _ptr(grad_y), _ptr(res[0]), _ptr(res[1]), _ptr(res[2]), _ptr(ws), nws,
-                                       _stream(x)), "cgtp_norm_backward")
+        dt, shape = self.torch_dtype, (samples.rows, self.dim)
+        px = _tensor(x, shape, dt, "x")
+        pg = _tensor(grad_y, shape, dt, "grad_y")
+        ps = _tensor(stats, (samples.S, self.num_groups, 2), self._acc, "stats")
+        pw, pb = self._affine(weight, bias)
+        shapes = (shape, (self.channels,), (self.biases,))
+        res = [None if not n else torch.empty(s, dtype=dt, device=x.device) if o is None else o
+               for n, s, o in zip(need, shapes, out)]
+        pr = [None if r is None else _tensor(r, s, dt, "grad") for r, s in zip(res, shapes)]
+        ws, pws, nws = _ws(ws, self.workspace_size(samples, backward=True), x.device)
+        _check(_lib.cgtp_norm_backward(self._h, samples._h, px, pw, pb, ps, pg, pr[0], pr[1], pr[2], pws, nws,
+                                       _stream_of(x)), "cgtp_norm_backward")
         return tuple(res)
 
 
@@ -185,10 +214,6 @@ class Dropout(_Handle):
         _check(_lib.cgtp_dropout_query(h, ctypes.byref(n)), "cgtp_dropout_query")
         self.dim = n.value
 
-    @property
-    def torch_dtype(self):
-        return _torch_dtype(self.dtype_code)
-
     @staticmethod
     def _key(seed, offset):
         if not 0 <= seed < 1 << 64 or not 0 <= offset < 1 << 32:
@@ -199,26 +224,23 @@ class Dropout(_Handle):
         """residual + dropout(x); ``offset`` differs from call to call and layer to layer."""
         shape, dt = (x.shape[0], self.dim), self.torch_dtype
         seed, offset = self._key(seed, offset)
-        _need(x, shape, dt, "x")
-        if residual is not None:
-            _need(residual, shape, dt, "residual")
+        px = _tensor(x, shape, dt, "x")
+        pr = None if residual is None else _tensor(residual, shape, dt, "residual")
         if out is None:
             out = _torch().empty_like(x)
-        _need(out, shape, dt, "out")
-        _check(_lib.cgtp_dropout_forward(self._h, x.shape[0], _ptr(x), float(p), seed, offset, _ptr(residual),
-                                         _ptr(out), _stream(x)), "cgtp_dropout_forward")
+        _check(_lib.cgtp_dropout_forward(self._h, shape[0], px, float(p), seed, offset, pr,
+                                         _tensor(out, shape, dt, "out"), _stream_of(x)), "cgtp_dropout_forward")
         return out
 
     def backward(self, grad_y, p, seed, offset, out=None):
         """grad_x for the forward's p, seed and offset (the residual's gradient is grad_y)."""
         shape, dt = (grad_y.shape[0], self.dim), self.torch_dtype
         seed, offset = self._key(seed, offset)
-        _need(grad_y, shape, dt, "grad_y")
+        pg = _tensor(grad_y, shape, dt, "grad_y")
         if out is None:
             out = _torch().empty_like(grad_y)
-        _need(out, shape, dt, "out")
-        _check(_lib.cgtp_dropout_backward(self._h, grad_y.shape[0], _ptr(grad_y), float(p), seed, offset, _ptr(out),
-                                          _stream(grad_y)), "cgtp_dropout_backward")
+        _check(_lib.cgtp_dropout_backward(self._h, shape[0], pg, float(p), seed, offset,
+                                          _tensor(out, shape, dt, "out"), _stream_of(grad_y)), "cgtp_dropout_backward")
         return out
 
 
@@ -264,10 +286,6 @@ class CrossAttention(_Handle):
         self.dim_q, self.dim_kv, self.head_dim = (a.value for a in v)
         self.scale = self.head_dim ** -0.5
 
-    @property
-    def torch_dtype(self):
-        return _torch_dtype(self.dtype_code)
-
     def batch(self, queries, context):
         return AttentionBatch(self, queries, context)
 
@@ -277,37 +295,37 @@ class CrossAttention(_Handle):
             raise ValueError("%s is required" % name)
         if not t.is_cuda:
             raise ValueError("%s must be a device tensor" % name)
-        if tuple(t.shape) != (rows, dim):
+        if t.shape != (rows, dim):
             raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (rows, dim)))
         if t.dtype != self.torch_dtype:
             raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, self.torch_dtype))
-        ld = t.stride(0) if rows > 1 else dim
-        if (dim > 1 and t.stride(1) != 1) or ld < dim:
+        step, unit = t.stride()
+        ld = step if rows > 1 else dim
+        if (dim > 1 and unit != 1) or ld < dim:
             raise ValueError("%s must have unit stride within its rows, which may not overlap" % name)
-        return _ptr(t), ld
+        return t.data_ptr(), ld
 
     def _mask(self, m, rows):
         if m is None:
-            return _vp(0)
+            return None
         torch = _torch()
         if m.dtype not in (torch.bool, torch.uint8):
             raise ValueError("key_mask must be bool or uint8")
-        return _ptr(_need(m, (rows,), m.dtype, "key_mask"))
+        return _tensor(m, (rows,), m.dtype, "key_mask")
 
     def _batch(self, batch):
         if batch.attn is not self:
             raise ValueError("the batch belongs to another CrossAttention")
 
     def _outputs(self, batch, q, out, lse, need_lse):
+        """(out, lse or None, their pointers)"""
         torch = _torch()
         if out is None:
             out = torch.empty((batch.nq, self.dim_q), dtype=self.torch_dtype, device=q.device)
-        _need(out, (batch.nq, self.dim_q), self.torch_dtype, "out")
         if need_lse and lse is None:
             lse = torch.empty((batch.nq, self.heads), dtype=torch.float32, device=q.device)
-        if lse is not None:
-            _need(lse, (batch.nq, self.heads), torch.float32, "lse")
-        return out, lse
+        return (out, lse, _tensor(out, (batch.nq, self.dim_q), self.torch_dtype, "out"),
+                None if lse is None else _tensor(lse, (batch.nq, self.heads), torch.float32, "lse"))
 
     def forward(self, batch, q, k, v, scale=None, key_mask=None, need_lse=False, out=None, lse=None, ws=None):
         """out, or (out, lse) with ``need_lse``; scale defaults to head_dim ** -0.5."""
@@ -316,11 +334,11 @@ class CrossAttention(_Handle):
         pk, ldk = self._rows(k, batch.nk, self.dim_kv, "k")
         pv, ldv = self._rows(v, batch.nk, self.dim_kv, "v")
         mask = self._mask(key_mask, batch.nk)
-        out, lse = self._outputs(batch, q, out, lse, need_lse)
-        ws, nws = _workspace(ws, batch.workspace_size(ATTN_FORWARD), q.device)
+        out, lse, po, pl = self._outputs(batch, q, out, lse, need_lse)
+        ws, pws, nws = _ws(ws, batch.workspace_size(ATTN_FORWARD), q.device)
         _check(_lib.cgtp_attn_forward(batch._h, pq, ldq, pk, ldk, pv, ldv, mask,
-                                      self.scale if scale is None else float(scale), _ptr(out), _ptr(lse), _ptr(ws),
-                                      nws, _stream(q)), "cgtp_attn_forward")
+                                      self.scale if scale is None else float(scale), po, pl, pws, nws, _stream_of(q)),
+               "cgtp_attn_forward")
         return (out, lse) if need_lse else out
 
     def pack(self, batch, k, v, key_mask=None, out=None):
@@ -329,19 +347,21 @@ class CrossAttention(_Handle):
         pk, ldk = self._rows(k, batch.nk, self.dim_kv, "k")
         pv, ldv = self._rows(v, batch.nk, self.dim_kv, "v")
         mask = self._mask(key_mask, batch.nk)
-        out, n = _workspace(out, batch.workspace_size(ATTN_CONTEXT), k.device)
-        _check(_lib.cgtp_attn_pack(batch._h, pk, ldk, pv, ldv, mask, _ptr(out), n, _stream(k)), "cgtp_attn_pack")
+        if out is None:
+            out = _torch().empty(max(batch.workspace_size(ATTN_CONTEXT), 16), dtype=_torch().uint8, device=k.device)
+        _check(_lib.cgtp_attn_pack(batch._h, pk, ldk, pv, ldv, mask, out.data_ptr(), _ws_bytes(out), _stream_of(k)),
+               "cgtp_attn_pack")
         return out
 
     def forward_packed(self, batch, q, context, scale=None, need_lse=False, out=None, lse=None, ws=None):
         """forward on a packed context (of this batch or one with the same context samples)."""
         self._batch(batch)
         pq, ldq = self._rows(q, batch.nq, self.dim_q, "q")
-        out, lse = self._outputs(batch, q, out, lse, need_lse)
-        ws, nws = _workspace(ws, batch.workspace_size(ATTN_FORWARD_PACKED), q.device)
-        _check(_lib.cgtp_attn_forward_packed(batch._h, pq, ldq, _ptr(context), _ws_bytes(context),
-                                             self.scale if scale is None else float(scale), _ptr(out), _ptr(lse),
-                                             _ptr(ws), nws, _stream(q)), "cgtp_attn_forward_packed")
+        out, lse, po, pl = self._outputs(batch, q, out, lse, need_lse)
+        ws, pws, nws = _ws(ws, batch.workspace_size(ATTN_FORWARD_PACKED), q.device)
+        _check(_lib.cgtp_attn_forward_packed(batch._h, pq, ldq, context.data_ptr(), _ws_bytes(context),
+                                             self.scale if scale is None else float(scale), po, pl, pws, nws,
+                                             _stream_of(q)), "cgtp_attn_forward_packed")
         return (out, lse) if need_lse else out
 
     def backward(self, batch, q, k, v, out, lse, grad_out, scale=None, key_mask=None, need=(True, True, True),
@@ -355,18 +375,14 @@ class CrossAttention(_Handle):
         pv, ldv = self._rows(v, batch.nk, self.dim_kv, "v")
         pg, ldg = self._rows(grad_out, batch.nq, self.dim_q, "grad_out")
         mask = self._mask(key_mask, batch.nk)
-        _need(out, (batch.nq, self.dim_q), dt, "out")
-        _need(lse, (batch.nq, self.heads), torch.float32, "lse")
-        shapes = [(batch.nq, self.dim_q), (batch.nk, self.dim_kv), (batch.nk, self.dim_kv)]
-        res = []
-        for i in range(3):
-            if not need[i]:
-                res.append(None)
-                continue
-            t = grads[i] if grads[i] is not None else torch.empty(shapes[i], dtype=dt, device=q.device)
-            res.append(_need(t, shapes[i], dt, "grad"))
-        ws, nws = _workspace(ws, batch.workspace_size(ATTN_BACKWARD), q.device)
+        po = _tensor(out, (batch.nq, self.dim_q), dt, "out")
+        pl = _tensor(lse, (batch.nq, self.heads), torch.float32, "lse")
+        shapes = ((batch.nq, self.dim_q), (batch.nk, self.dim_kv), (batch.nk, self.dim_kv))
+        res = [None if not n else torch.empty(s, dtype=dt, device=q.device) if g is None else g
+               for n, s, g in zip(need, shapes, grads)]
+        pr = [None if r is None else _tensor(r, s, dt, "grad") for r, s in zip(res, shapes)]
+        ws, pws, nws = _ws(ws, batch.workspace_size(ATTN_BACKWARD), q.device)
         _check(_lib.cgtp_attn_backward(batch._h, pq, ldq, pk, ldk, pv, ldv, mask,
-                                       self.scale if scale is None else float(scale), _ptr(out), _ptr(lse), pg, ldg,
-                                       *[_ptr(t) for t in res], _ptr(ws), nws, _stream(q)), "cgtp_attn_backward")
+                                       self.scale if scale is None else float(scale), po, pl, pg, ldg, pr[0], pr[1],
+                                       pr[2], pws, nws, _stream_of(q)), "cgtp_attn_backward")
         return tuple(res)

@@ -61,8 +61,8 @@ cgtp_status cgtp_norm_create(const char* irreps, int64_t groups, cgtp_act act, d
 cgtp_status cgtp_norm_destroy(cgtp_norm norm);
 /* Row size, channel count, bias count and number of groups over all blocks. */
 cgtp_status cgtp_norm_query(cgtp_norm norm, int64_t* dim, int64_t* channels, int64_t* biases, int64_t* num_groups);
-/* Workspace bytes of the two calls below (the larger of both). */
-cgtp_status cgtp_norm_workspace_size(cgtp_norm norm, cgtp_samples samples, size_t* bytes);
+/* Workspace bytes of cgtp_norm_forward (backward = 0) or cgtp_norm_backward. */
+cgtp_status cgtp_norm_workspace_size(cgtp_norm norm, cgtp_samples samples, int backward, size_t* bytes);
 /* y [rows][dim] from x [rows][dim]. stats [S][num_groups][2] receives mu and
  * 1 / sqrt(var + eps) in the accumulation type (fp32; fp64 for fp64 norms) for
  * the backward (entries of empty samples are not written); NULL if not wanted.

@@ -194,6 +194,7 @@ def test_norm_refusals():
     norm = layers.GroupNorm("8x0e+8x1o", 2)
     sm = layers.Samples([0, 4])
     x = torch.zeros((4, norm.dim), device="cuda")
+    y, stats = norm.forward(sm, x)
     with pytest.raises(ValueError):
         norm.forward(sm, x[:3])
     with pytest.raises(ValueError):
@@ -201,9 +202,9 @@ def test_norm_refusals():
     with pytest.raises(ValueError):
         norm.forward(sm, x, weight=torch.ones(3, device="cuda"))
     with pytest.raises(cgtp.CgtpError) as e:
-        norm.forward(sm, x, ws=torch.empty(4, dtype=torch.uint8, device="cuda"))
+        norm.backward(sm, x, None, None, stats, x, ws=torch.empty(4, dtype=torch.uint8, device="cuda"))
     assert e.value.status == 5
-    ws = torch.empty(norm.workspace_size(sm) + 16, dtype=torch.uint8, device="cuda")[1:]
+    ws = torch.empty(norm.workspace_size(sm, backward=True) + 16, dtype=torch.uint8, device="cuda")[1:]
     with pytest.raises(cgtp.CgtpError) as e:
-        norm.forward(sm, x, ws=ws)
+        norm.backward(sm, x, None, None, stats, x, ws=ws)
     assert e.value.status == 1

@@ -61,7 +61,7 @@ def test_null_arguments():
     assert lib.cgtp_norm_create(n, 1, 0, 1e-5, 0, n) == INVALID
     assert lib.cgtp_norm_forward(n, n, n, n, n, n, n, n, 0, n) == INVALID
     assert lib.cgtp_norm_backward(*([n] * 11), 0, n) == INVALID
-    assert lib.cgtp_norm_workspace_size(n, n, ctypes.byref(sz)) == INVALID
+    assert lib.cgtp_norm_workspace_size(n, n, 0, ctypes.byref(sz)) == INVALID
     assert lib.cgtp_dropout_forward(n, 1, n, 0.1, 0, 0, n, n, n) == INVALID
     assert lib.cgtp_attn_create(n, 1, 1, 0, n) == INVALID
     assert lib.cgtp_attn_batch_create(n, n, n, n) == INVALID
