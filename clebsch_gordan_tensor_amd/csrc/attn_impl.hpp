@@ -41,7 +41,7 @@ constexpr int kThreads = 256;  // 4 waves
 // compiler keeps them in the accumulation file and moves them to and fro for
 // every vector operation (the forward of a head of 128 took 1.3 times as long).
 // The heads whose whole tiles do not fit 256 registers take one wave.
-constexpr int few_waves(int dp, size_t size) { return dp * int(size) <= (size == 2 ? 384 : 512) ? 2 : 1; }
+constexpr int few_waves(int dp, size_t size) { return dp * int(size) <= (size == 2 ? 320 : 384) ? 2 : 1; }
 // two workgroups a compute unit, where its 160 KB of shared memory hold `units` KB twice
 constexpr int lds_waves(int units) { return units < 80 ? 2 : 1; }
 
@@ -628,35 +628,44 @@ __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void fwd_few_ke
   using Frag = typename Op<T>::Frag;
   __shared__ f32x4 sh[2][D::DT * 4 * 64];
   __shared__ float ml[4][2][64];
-  const Item it = a.items[blockIdx.x];
+  const Item it = ldc(a.items + blockIdx.x);
   if (it.tiles == 0) return;
   const int lane = int(threadIdx.x) % 64, wave = wave_id(), h = lane / 32;
-  const Tile tl = a.qtiles[it.a0];
+  const Tile tl = ldc(a.qtiles + it.a0);
+  // the widest heads leave no registers for whole tiles: read as they are used
+  constexpr bool kStream = DP * int(sizeof(T)) > 640;
+  // a tile's units, in registers a turn ahead: the keys' are read again as soon as
+  // the scores are done, the values' as soon as they are added
+  u32x4 k[kStream ? 1 : D::UNITS], v[kStream ? 1 : D::UNITS];
+  const auto tile = [&](const void* src, int t) {
+    return static_cast<const T*>(src) + (int64_t(min(t, it.b1 - 1)) * a.groups + it.hk) * D::TILE;
+  };
+  const auto fetch = [&](const T* src, auto& dst) {
+    if constexpr (!kStream)
+#pragma unroll
+      for (int u = 0; u < D::UNITS; ++u) dst[u] = unit16(src, u, lane);
+  };
+  if (it.b0 + wave < it.b1) {
+    fetch(tile(a.kf, it.b0 + wave), k);
+    fetch(tile(a.vf, it.b0 + wave), v);
+  }
   Frag q[D::KSTEPS];
   load_queries<T, DP>(a, tl, it.hk, lane, q);
   Running<D::DT> st;
 #pragma unroll
   for (int d = 0; d < D::DT; ++d) st.o[d] = zero16();
   for (int t = it.b0 + wave; t < it.b1; t += 4) {
-    const T* kf = static_cast<const T*>(a.kf) + (int64_t(t) * a.groups + it.hk) * D::TILE;
-    const T* vf = static_cast<const T*>(a.vf) + (int64_t(t) * a.groups + it.hk) * D::TILE;
     f32x16 sc = zero16();
-    u32x4 v[D::UNITS];
-    if constexpr (D::kShort) {
 #pragma unroll
-      for (int u = 0; u < D::KSTEPS; ++u) {
-        sc = Op<T>::mma(as_frag<Frag>(unit16(kf, u, lane)), q[u], sc);
-        pace<T, DP>(u);
+    for (int u = 0; u < D::KSTEPS; ++u) {
+      if constexpr (kStream) {
+        sc = Op<T>::mma(as_frag<Frag>(unit16(tile(a.kf, t), u, lane)), q[u], sc);
+        if (u % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+      } else {
+        sc = Op<T>::mma(as_frag<Frag>(k[u]), q[u], sc);
       }
-    } else {
-      u32x4 k[D::UNITS];
-#pragma unroll
-      for (int u = 0; u < D::UNITS; ++u) k[u] = unit16(kf, u, lane);
-#pragma unroll
-      for (int u = 0; u < D::UNITS; ++u) v[u] = unit16(vf, u, lane);
-#pragma unroll
-      for (int u = 0; u < D::KSTEPS; ++u) sc = Op<T>::mma(as_frag<Frag>(k[u]), q[u], sc);
     }
+    fetch(tile(a.kf, t + 4), k);
     if (ldc(a.flags + t)) mask_scores(sc, a.bias + int64_t(t) * 32, h);
     raise_reference(st, top_score(sc, a.scale2));
     weigh<true>(st, sc, a.scale2);
@@ -668,10 +677,14 @@ __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void fwd_few_ke
 #pragma unroll
       for (int f = 0; f < D::FR; ++f) {
         const int u = d * D::FR + f;
-        if constexpr (D::kShort) v[u] = unit16(vf, u, lane);
-        st.o[d] = Op<T>::mma(as_frag<Frag>(v[u]), p[f], st.o[d]);
-        pace<T, DP>(u);
+        if constexpr (kStream) {
+          st.o[d] = Op<T>::mma(as_frag<Frag>(unit16(tile(a.vf, t), u, lane)), p[f], st.o[d]);
+          if (u % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+        } else {
+          st.o[d] = Op<T>::mma(as_frag<Frag>(v[u]), p[f], st.o[d]);
+        }
       }
+    fetch(tile(a.vf, t + 4), v);
   }
   // join: common reference, then waves 2, 3 into 0, 1 and 1 into 0
   ml[wave][0][lane] = st.m;
