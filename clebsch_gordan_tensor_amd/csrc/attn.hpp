@@ -17,8 +17,9 @@ struct Tile {
 // tiles = 0: nothing (padding of the list).
 struct alignas(16) Item {
   int32_t a0, tiles, b0, b1;
-  int32_t hk, slot, stride, pad;
+  int32_t hk, slot, stride, kind;  // kind: of gradient items
 };
+enum : int32_t { kItemQ = 0, kItemV = 1, kItemK = 2 };  // grad_q; grad_v (or both); grad_k
 
 // One tile whose result is the sum of parts slot .. slot + parts - 1, number
 // `within` of the `stride` tiles of each.
@@ -80,14 +81,29 @@ struct FwdArgs {
   bool q_vec, out_quad;
 };
 
+// Packed forms of the gradients: row or column fragments of K, V, Q and grad_out, in
+// the order in which they lie in the workspace.
+enum : int { kKRows = 0, kVRows = 1, kKCols = 2, kKForms = 3 };
+enum : int { kQRows = 0, kGCols = 1, kGRows = 2, kQCols = 3, kQForms = 4 };
+
 struct BwdArgs {
   const Item* items;
   const Tile *qtiles, *ktiles;
   const int4* table;
-  const void *kr, *kc, *vr, *qr, *qc, *gr, *gc;  // r: row fragments, c: column fragments; g: grad_out
+  // packed forms, one after another at equal strides (in elements)
+  const void *kforms_, *qforms_;
+  int64_t kstride, qstride;
+  template <typename T>
+  __host__ __device__ const T* kforms(int form) const {
+    return static_cast<const T*>(kforms_) + form * kstride;
+  }
+  template <typename T>
+  __host__ __device__ const T* qforms(int form) const {
+    return static_cast<const T*>(qforms_) + form * qstride;
+  }
   const float *bias, *rows;
   void *dq, *dk, *dv;
-  float *part, *part_v;
+  float *part_q, *part_k, *part_v;
   int64_t ldq, ldk;
   float scale, scale2;
   int G, heads, groups;
@@ -98,8 +114,7 @@ struct KernelTable {
   void (*pack)(const PackArgs&, hipStream_t);
   void (*fwd)(const FwdArgs&, int items, int tiles, hipStream_t);  // items of up to 1, 4 or 8 tiles
   void (*fwd_join)(const FwdArgs&, int joins, hipStream_t);
-  void (*dq)(const BwdArgs&, int items, hipStream_t);
-  void (*dkv)(const BwdArgs&, int items, hipStream_t);  // grad_k and grad_v, each unless NULL
+  void (*bwd)(const BwdArgs&, int items, hipStream_t);  // each gradient unless NULL
   void (*grad_join)(const GradJoinArgs&, int joins, int tensors, hipStream_t);
 };
 
@@ -111,11 +126,16 @@ KernelTable kernels_bf16(int dp);
 // operands and accumulators fit the registers.
 constexpr bool wide_forward(int dp, size_t size) { return size == 2 && dp <= 128; }
 
-// A list of work items on the device with the joins of its splits.
+// Whether both gradients of the keys are formed in one pass: their accumulators
+// and operands fit the registers (else four products' worth of work becomes five).
+constexpr bool one_pass(int dp, size_t size) { return dp <= (size == 2 ? 128 : 160); }
+
+// A list of work items on the device with the joins of its splits: those of the
+// query side, then those of the context side.
 struct WorkList {
-  int items = 0, joins = 0;
-  int64_t part_tiles = 0;  // tiles of partial results
-  DevMem item_mem, join_mem;
+  int items = 0, joins[2] = {0, 0};
+  int64_t part_tiles[2] = {0, 0};  // tiles of partial results
+  DevMem item_mem, join_mem[2];
 };
 
 }  // namespace attn
@@ -138,7 +158,7 @@ struct cgtp_attn_batch_s {
   int device = 0;
   cgtp::DevMem qtile_mem, ktile_mem;
   cgtp::attn::WorkList few, fwd, wide;  // forward, items of up to 1, 4 and 8 query tiles
-  cgtp::attn::WorkList dq, dkv;
+  cgtp::attn::WorkList bwd;
 };
 
 namespace cgtp {

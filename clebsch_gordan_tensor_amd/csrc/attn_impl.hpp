@@ -802,26 +802,24 @@ __device__ __forceinline__ void finish_grad(const BwdArgs& a, const Item& it, co
 // dQ^T += K^T dS^T. Three packed forms of a tile pass through shared memory: K
 // rows, V rows, K columns.
 template <typename T, int DP>
-__global__ __launch_bounds__(kThreads, lds_waves(stage_units(3 * Dims<T, DP>::UNITS))) void dq_kernel(BwdArgs a) {
+__device__ __forceinline__ void dq_item(const BwdArgs& a, const Item& it, u32x4* pool, float* bias_pool) {
   using D = Dims<T, DP>;
   using Frag = typename Op<T>::Frag;
   constexpr int STAGE = 3 * D::UNITS, PER = (STAGE + 3) / 4;
   constexpr int BUFS = stage_buffers(STAGE);
-  __shared__ u32x4 sh[BUFS][STAGE * 64];
-  __shared__ __attribute__((aligned(16))) float bias[BUFS][32];
-  const Item it = a.items[blockIdx.x];
-  if (it.tiles == 0) return;
+  const auto sh = reinterpret_cast<u32x4(*)[STAGE * 64]>(pool);
+  const auto bias = reinterpret_cast<float(*)[64]>(bias_pool);
   const int lane = int(threadIdx.x) % 64, wave = wave_id(), n = lane % 32, h = lane / 32;
   const bool active = wave < it.tiles;
   const int qt = it.a0 + (active ? wave : 0);
-  const Tile tl = a.qtiles[qt];
+  const Tile tl = ldc(a.qtiles + qt);
   const int64_t qat = int64_t(qt) * a.groups + it.hk;
-  const T* const qrows = static_cast<const T*>(a.qr) + qat * D::TILE;
+  const T* const qrows = a.qforms<T>(kQRows) + qat * D::TILE;
   Frag q[D::kShort ? 1 : D::KSTEPS], g[D::KSTEPS];
 #pragma unroll
   for (int t = 0; t < D::KSTEPS; ++t) {
     if constexpr (!D::kShort) q[t] = as_frag<Frag>(unit16(qrows, t, lane));
-    g[t] = as_frag<Frag>(unit16(static_cast<const T*>(a.gr) + qat * D::TILE, t, lane));
+    g[t] = as_frag<Frag>(unit16(a.qforms<T>(kGRows) + qat * D::TILE, t, lane));
   }
   const float lse2 = a.rows[qat * 64 + n], delta = a.rows[qat * 64 + 32 + n];
   f32x16 dq[D::DT];
@@ -829,13 +827,12 @@ __global__ __launch_bounds__(kThreads, lds_waves(stage_units(3 * Dims<T, DP>::UN
   for (int d = 0; d < D::DT; ++d) dq[d] = zero16();
 
   const auto fetch = [&](int tile, int buf) {
-    const int64_t at = (int64_t(tile) * a.groups + it.hk) * D::TILE;
+    const T* base = a.kforms<T>(0) + (int64_t(tile) * a.groups + it.hk) * D::TILE;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      const int u = k * 4 + wave, which = u / D::UNITS;
+      const int u = k * 4 + wave, form = u / D::UNITS;
       if (u >= STAGE) break;
-      const T* base = static_cast<const T*>(which == 0 ? a.kr : which == 1 ? a.vr : a.kc);
-      copy_unit(base + at, u % D::UNITS, lane, &sh[buf][u * 64]);
+      copy_unit(base + form * a.kstride, u % D::UNITS, lane, &sh[buf][u * 64]);
     }
     if (threadIdx.x < 32) bias[buf][threadIdx.x] = a.bias[int64_t(tile) * 32 + threadIdx.x];
   };
@@ -882,38 +879,36 @@ __global__ __launch_bounds__(kThreads, lds_waves(stage_units(3 * Dims<T, DP>::UN
     __syncthreads();
   }
   if (active)
-    finish_grad<T, DP>(a, it, tl, wave, lane, true, a.dq, a.ldq, a.part, a.q_quad, dq, a.scale);
+    finish_grad<T, DP>(a, it, tl, wave, lane, true, a.dq, a.ldq, a.part_q, a.q_quad, dq, a.scale);
 }
 
 // grad_k and grad_v: a wave keeps 32 keys and walks the query tiles (all heads
 // of the group): S = Q K^T, P = exp2(S - lse), dV^T += dO^T P, dP = dO V^T,
-// dS = P (dP - delta), dK^T += Q^T dS. PART 0: both; heads whose operands and
-// accumulators do not fit the registers run it as PART 1 (grad_v) and 2 (grad_k).
+// dS = P (dP - delta), dK^T += Q^T dS. PART 0: both (one_pass); else as PART 1
+// (grad_v) and 2 (grad_k).
 template <typename T, int DP, int PART>
-__global__ __launch_bounds__(kThreads, lds_waves(stage_units(dkv_forms(PART) * Dims<T, DP>::UNITS))) void dkv_kernel(BwdArgs a) {
+__device__ __forceinline__ void dkv_item(const BwdArgs& a, const Item& it, u32x4* pool, float* row_pool) {
   using D = Dims<T, DP>;
   using Frag = typename Op<T>::Frag;
   constexpr bool WANT_V = PART != 2, WANT_K = PART != 1;
   constexpr int FORMS = dkv_forms(PART);
-  constexpr int GC = 1, GR = WANT_V ? 2 : 1, QC = GR + 1;
+  constexpr int GC = 1, GR = WANT_V ? 2 : 1, QC = GR + 1;  // place of a form in the stage (Q rows: 0)
   constexpr int STAGE = FORMS * D::UNITS, PER = (STAGE + 3) / 4;
   constexpr int BUFS = stage_buffers(STAGE);
-  __shared__ u32x4 sh[BUFS][STAGE * 64];
-  __shared__ __attribute__((aligned(16))) float rows[BUFS][64];
-  const Item it = a.items[blockIdx.x];
-  if (it.tiles == 0) return;
+  const auto sh = reinterpret_cast<u32x4(*)[STAGE * 64]>(pool);
+  const auto rows = reinterpret_cast<float(*)[64]>(row_pool);
   const int lane = int(threadIdx.x) % 64, wave = wave_id(), n = lane % 32, h = lane / 32;
   const bool active = wave < it.tiles;
   const int kt = it.a0 + (active ? wave : 0);
-  const Tile tl = a.ktiles[kt];
+  const Tile tl = ldc(a.ktiles + kt);
   const int64_t kat = (int64_t(kt) * a.groups + it.hk) * D::TILE;
   constexpr bool kReread = D::kShort && WANT_K;
-  const T* const krows = static_cast<const T*>(a.kr) + kat;
+  const T* const krows = a.kforms<T>(kKRows) + kat;
   Frag k[kReread ? 1 : D::KSTEPS], v[WANT_K ? D::KSTEPS : 1];
 #pragma unroll
   for (int t = 0; t < D::KSTEPS; ++t) {
     if constexpr (!kReread) k[t] = as_frag<Frag>(unit16(krows, t, lane));
-    if (WANT_K) v[t] = as_frag<Frag>(unit16(static_cast<const T*>(a.vr) + kat, t, lane));
+    if (WANT_K) v[t] = as_frag<Frag>(unit16(a.kforms<T>(kVRows) + kat, t, lane));
   }
   const float bias = a.bias[int64_t(kt) * 32 + n];
   f32x16 dk[WANT_K ? D::DT : 1], dv[WANT_V ? D::DT : 1];
@@ -924,12 +919,14 @@ __global__ __launch_bounds__(kThreads, lds_waves(stage_units(dkv_forms(PART) * D
   }
   const auto fetch = [&](int tile, int buf) {
     const int64_t at = int64_t(tile) * a.groups + it.hk;
+    const T* base = a.qforms<T>(0) + at * D::TILE;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int u = i * 4 + wave, which = u / D::UNITS;
+      const int u = i * 4 + wave;
       if (u >= STAGE) break;
-      const void* base = which == 0 ? a.qr : (WANT_V && which == GC) ? a.gc : which == GR ? a.gr : a.qc;
-      copy_unit(static_cast<const T*>(base) + at * D::TILE, u % D::UNITS, lane, &sh[buf][u * 64]);
+      // the forms in use, in their order in memory
+      const int form = u / D::UNITS + (WANT_V || u < D::UNITS ? 0 : 1);
+      copy_unit(base + form * a.qstride, u % D::UNITS, lane, &sh[buf][u * 64]);
     }
     if (threadIdx.x < 64) rows[buf][threadIdx.x] = a.rows[at * 64 + threadIdx.x];
   };
@@ -986,7 +983,34 @@ __global__ __launch_bounds__(kThreads, lds_waves(stage_units(dkv_forms(PART) * D
   if constexpr (WANT_V)
     if (a.dv) finish_grad<T, DP>(a, it, tl, wave, lane, false, a.dv, a.ldk, a.part_v, a.k_quad, dv, 1.0f);
   if constexpr (WANT_K)
-    if (a.dk) finish_grad<T, DP>(a, it, tl, wave, lane, false, a.dk, a.ldk, a.part, a.k_quad, dk, a.scale);
+    if (a.dk) finish_grad<T, DP>(a, it, tl, wave, lane, false, a.dk, a.ldk, a.part_k, a.k_quad, dk, a.scale);
+}
+
+// All gradients in one launch: the items of the three kinds fill the device
+// together and end together (a ragged batch's three launches each left a quarter
+// of it idle at their end).
+template <typename T, int DP>
+constexpr int bwd_units() {
+  constexpr int U = Dims<T, DP>::UNITS;
+  // grad_q and grad_k: 3 forms; grad_v: 2, which may be kept twice where 3 are not
+  constexpr int a = stage_units(3 * U), b = stage_units(dkv_forms(one_pass(DP, sizeof(T)) ? 0 : 1) * U);
+  return a > b ? a : b;
+}
+template <typename T, int DP>
+__global__ __launch_bounds__(kThreads, lds_waves(bwd_units<T, DP>())) void bwd_kernel(BwdArgs a) {
+  __shared__ u32x4 pool[bwd_units<T, DP>() * 64];
+  __shared__ __attribute__((aligned(16))) float rows[2 * 64];
+  const Item it = ldc(a.items + blockIdx.x);
+  if (it.tiles == 0) return;
+  if (it.kind == kItemQ) {
+    if (a.dq) dq_item<T, DP>(a, it, pool, rows);
+  } else if constexpr (one_pass(DP, sizeof(T))) {
+    if (a.dk || a.dv) dkv_item<T, DP, 0>(a, it, pool, rows);
+  } else if (it.kind == kItemV) {
+    if (a.dv) dkv_item<T, DP, 1>(a, it, pool, rows);
+  } else {
+    if (a.dk) dkv_item<T, DP, 2>(a, it, pool, rows);
+  }
 }
 
 // Adds the parts of split gradient rows in order, as fwd_join_kernel.
@@ -1012,10 +1036,6 @@ __global__ __launch_bounds__(kThreads) void grad_join_kernel(GradJoinArgs a) {
 
 template <typename T, int DP>
 struct Kernels {
-  // whether both gradients of the keys fit the registers of a lane in one
-  // pass: two accumulators and two operands
-  static constexpr bool kOnePass = DP <= (sizeof(T) == 2 ? 128 : 160);
-
   static void pack(const PackArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((pack_kernel<T, DP>), dim3(unsigned((a.ntiles + 7) / 8 * 8 * a.groups)), dim3(kThreads), 0, s, a);
   }
@@ -1028,22 +1048,14 @@ struct Kernels {
   static void fwd_join(const FwdArgs& a, int joins, hipStream_t s) {
     hipLaunchKernelGGL((fwd_join_kernel<T, DP>), dim3(unsigned(joins), DP / 32), dim3(kThreads), 0, s, a);
   }
-  static void dq(const BwdArgs& a, int items, hipStream_t s) {
-    hipLaunchKernelGGL((dq_kernel<T, DP>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
-  }
-  static void dkv(const BwdArgs& a, int items, hipStream_t s) {
-    if constexpr (kOnePass) {
-      hipLaunchKernelGGL((dkv_kernel<T, DP, 0>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
-    } else {
-      if (a.dv) hipLaunchKernelGGL((dkv_kernel<T, DP, 1>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
-      if (a.dk) hipLaunchKernelGGL((dkv_kernel<T, DP, 2>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
-    }
+  static void bwd(const BwdArgs& a, int items, hipStream_t s) {
+    hipLaunchKernelGGL((bwd_kernel<T, DP>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
   }
   static void grad_join(const GradJoinArgs& a, int joins, int tensors, hipStream_t s) {
     hipLaunchKernelGGL((grad_join_kernel<T, DP>), dim3(unsigned(joins), DP / 32, unsigned(tensors)), dim3(kThreads), 0,
                        s, a);
   }
-  static KernelTable table() { return {pack, fwd, fwd_join, dq, dkv, grad_join}; }
+  static KernelTable table() { return {pack, fwd, fwd_join, bwd, grad_join}; }
 };
 
 }  // namespace attn

@@ -44,48 +44,60 @@ Side cut(const std::vector<int64_t>& ptr, int64_t G) {
   return s;
 }
 
-// A unit of work before splitting: tiles a0 .. a0 + tiles - 1 of one side of
-// sample s, for every context head, against b0 .. b1 - 1 of the other.
+// A unit of work before splitting: tiles a0 .. a0 + tiles - 1 of one side (0:
+// queries, 1: context) of a sample, for every context head, against b0 .. b1 - 1
+// of the other; every tile of those costs `weight` products. kinds: the items made
+// of it (each with the same split).
 struct Unit {
-  int32_t sample, a0, tiles, b0, b1;
+  int32_t sample, side, a0, tiles, b0, b1, weight;
+  std::vector<int32_t> kinds;
 };
 
 template <typename F>
-std::vector<Unit> units(const Side& a, const Side& b, int per, F&& take) {
-  std::vector<Unit> u;
+void add_units(std::vector<Unit>& u, const Side& a, const Side& b, int side, int per, int weight,
+               std::vector<int32_t> kinds, F&& take) {
   for (size_t s = 0; s + 1 < a.first.size(); ++s) {
     const int n = a.first[s + 1] - a.first[s];
     if (!take(n)) continue;
     for (int t = 0; t < n; t += per)
-      u.push_back({int32_t(s), a.first[s] + t, std::min(per, n - t), b.first[s], b.first[s + 1]});
+      u.push_back({int32_t(s), side, a.first[s] + t, std::min(per, n - t), b.first[s], b.first[s + 1], weight, kinds});
   }
-  return u;
 }
 
-// Longest part of a unit, in tiles: of some candidates the one whose parts, the
-// longest first onto `slots` places, end earliest. An item costs its tiles plus
-// about two for its start and end, a part of a split one about three more for
+int64_t parts_of(const Unit& x, int64_t cost) {
+  const int64_t n = x.b1 - x.b0;
+  return std::max<int64_t>(1, std::min<int64_t>(n, (n * x.weight + cost - 1) / cost));
+}
+
+// Largest cost of a part: of some candidates the one whose parts, the longest
+// first onto `slots` places, end earliest. An item costs its products plus about
+// two tiles' for its start and end, a part of a split one about three more for
 // its partial result and the join (measured: parts of a ragged batch cut to
 // twice the number cost as much as the better balance gained). Parts have at least
 // min_len tiles, and batches with many more items than places are not split.
-int64_t part_length(const std::vector<Unit>& u, int groups, int slots, int min_len) {
-  int64_t longest = 1;
-  for (const Unit& x : u) longest = std::max<int64_t>(longest, x.b1 - x.b0);
-  if (int64_t(u.size()) * groups > 16 * int64_t(slots)) return longest;
+int64_t part_cost(const std::vector<Unit>& u, int groups, int slots, int min_len) {
+  int64_t longest = 1, count = 0;
+  int weight = 1;
+  for (const Unit& x : u) {
+    longest = std::max<int64_t>(longest, int64_t(x.b1 - x.b0) * x.weight);
+    count += int64_t(x.kinds.size()) * groups;
+    weight = std::max<int>(weight, x.weight);
+  }
+  if (count > 16 * int64_t(slots)) return longest;
   int64_t best = longest, best_end = INT64_MAX;
   for (int64_t parts = 1; parts <= 64; parts += 1 + parts / 8) {
-    const int64_t len = (longest + parts - 1) / parts;
-    if (parts > 1 && len < min_len) break;
-    std::vector<int64_t> cost;
+    const int64_t cost = (longest + parts - 1) / parts;
+    if (parts > 1 && cost < int64_t(min_len) * weight) break;
+    std::vector<int64_t> costs;
     for (const Unit& x : u) {
-      const int64_t n = x.b1 - x.b0, k = std::max<int64_t>(1, (n + len - 1) / len);
-      for (int64_t i = 0; i < k * groups; ++i) cost.push_back((n + k - 1) / k + (k > 1 ? 5 : 2));
+      const int64_t k = parts_of(x, cost), n = (x.b1 - x.b0 + k - 1) / k;
+      costs.insert(costs.end(), size_t(k) * size_t(groups) * x.kinds.size(), (n + (k > 1 ? 5 : 2)) * x.weight);
     }
-    if (parts > 1 && int64_t(cost.size()) > 16 * int64_t(slots)) break;
-    std::sort(cost.begin(), cost.end(), std::greater<int64_t>());
+    if (parts > 1 && int64_t(costs.size()) > 16 * int64_t(slots)) break;
+    std::sort(costs.begin(), costs.end(), std::greater<int64_t>());
     std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> ends;
     int64_t end = 0;
-    for (int64_t c : cost) {
+    for (int64_t c : costs) {
       int64_t t = c;
       if (int64_t(ends.size()) >= slots) {
         t += ends.top();
@@ -96,56 +108,57 @@ int64_t part_length(const std::vector<Unit>& u, int groups, int slots, int min_l
     }
     if (end < best_end) {
       best_end = end;
-      best = len;
+      best = cost;
     }
   }
   return best;
 }
 
 // Splits long units (of at most `stride` tiles) and lays the items out for the
-// device.
-//
-// `slots` is the number of workgroups that the device works on at once.
+// device. `slots` is the number of workgroups that the device works on at once.
 // Order: workgroups go to the 8 dies in turn, and each die has its own L2, so
-// all items that read the same packed tiles (one sample and context head) are
-// given to one die and follow each other there, those with the longest items
+// all items that read the same packed tiles (one sample, side and context head)
+// are given to one die and follow each other there, those with the longest items
 // first, so that the short ones fill the end; a group bigger than a die's share
 // goes round several.
 void build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, int slots, int min_len) {
-  const int64_t len = part_length(u, groups, slots, min_len);
+  const int64_t cost = part_cost(u, groups, slots, min_len);
   struct Group {
     int64_t work = 0, longest = 0;
     std::vector<Item> items;
+    std::vector<int64_t> costs;
   };
   std::vector<Group> gs;
-  std::vector<Join> joins;
-  int64_t nslot = 0;
+  std::vector<Join> joins[2];
+  int64_t nslot[2] = {0, 0};
   for (size_t i = 0; i < u.size();) {
     size_t j = i;
-    while (j < u.size() && u[j].sample == u[i].sample) ++j;
+    while (j < u.size() && u[j].sample == u[i].sample && u[j].side == u[i].side) ++j;
     for (int hk = 0; hk < groups; ++hk) {
-      Group g;
+      std::vector<Group> g(u[i].kinds.size());
       for (size_t k = i; k < j; ++k) {
         const Unit& x = u[k];
-        const int64_t n = x.b1 - x.b0, parts = std::max<int64_t>(1, (n + len - 1) / len);
-        for (int64_t p = 0; p < parts; ++p) {
-          const int32_t b0 = int32_t(x.b0 + n * p / parts), b1 = int32_t(x.b0 + n * (p + 1) / parts);
-          g.items.push_back({x.a0, x.tiles, b0, b1, hk, parts > 1 ? int32_t(nslot + p) : -1, stride, 0});
-          g.work += b1 - b0 + 1;
-          g.longest = std::max<int64_t>(g.longest, b1 - b0);
-        }
+        const int64_t n = x.b1 - x.b0, parts = parts_of(x, cost);
+        int64_t& slot = nslot[x.side];
+        for (size_t q = 0; q < g.size(); ++q)
+          for (int64_t p = 0; p < parts; ++p) {
+            const int32_t b0 = int32_t(x.b0 + n * p / parts), b1 = int32_t(x.b0 + n * (p + 1) / parts);
+            g[q].items.push_back(
+                {x.a0, x.tiles, b0, b1, hk, parts > 1 ? int32_t(slot + p) : -1, stride, x.kinds[q]});
+            g[q].costs.push_back(int64_t(b1 - b0 + 1) * x.weight);
+            g[q].work += g[q].costs.back();
+            g[q].longest = std::max(g[q].longest, g[q].costs.back());
+          }
         if (parts > 1) {
           for (int t = 0; t < x.tiles; ++t)
-            joins.push_back({x.a0 + t, hk, int32_t(nslot), int32_t(parts), stride, t, 0, 0});
-          nslot += parts;
+            joins[x.side].push_back({x.a0 + t, hk, int32_t(slot), int32_t(parts), stride, t, 0, 0});
+          slot += parts;
         }
       }
-      gs.push_back(std::move(g));
+      for (Group& q : g) gs.push_back(std::move(q));
     }
     i = j;
   }
-  w.part_tiles = nslot * stride;
-  if (w.part_tiles > INT32_MAX / 32) throw Error{CGTP_ERR_UNSUPPORTED, "attention: too many partial tiles"};
 
   int64_t total = 0;
   for (const Group& g : gs) total += g.work;
@@ -162,7 +175,7 @@ void build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, int 
       const int x = int(std::min_element(load.begin(), load.end()) - load.begin());
       int64_t room = std::max<int64_t>(1, share - load[x]);
       while (at < g.items.size() && room > 0) {
-        const int64_t c = g.items[at].b1 - g.items[at].b0 + 1;
+        const int64_t c = g.costs[at];
         queue[size_t(x)].push_back(g.items[at++]);
         load[size_t(x)] += c;
         room -= c;
@@ -179,9 +192,13 @@ void build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, int 
   while (!items.empty() && items.back().tiles == 0) items.pop_back();
   if (items.size() > size_t(INT32_MAX)) throw Error{CGTP_ERR_UNSUPPORTED, "attention: too many work items"};
   w.items = int(items.size());
-  w.joins = int(joins.size());
   w.item_mem.upload(items.data(), items.size() * sizeof(Item));
-  w.join_mem.upload(joins.data(), joins.size() * sizeof(Join));
+  for (int k = 0; k < 2; ++k) {
+    w.part_tiles[k] = nslot[k] * stride;
+    if (w.part_tiles[k] > INT32_MAX / 32) throw Error{CGTP_ERR_UNSUPPORTED, "attention: too many partial tiles"};
+    w.joins[k] = int(joins[k].size());
+    w.join_mem[k].upload(joins[k].data(), joins[k].size() * sizeof(Join));
+  }
 }
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
@@ -221,7 +238,8 @@ Context carve_context(const cgtp_attn_batch_s* b, void* p) {
 }
 
 struct Backward {
-  void *kr, *kc, *vr, *qr, *qc, *gr, *gc;
+  char *kforms, *qforms;  // at strides of kbytes and qbytes
+  size_t kbytes, qbytes;
   float *bias, *rows, *part_q, *part_k, *part_v;
   size_t bytes;
 };
@@ -231,24 +249,21 @@ Backward carve_backward(const cgtp_attn_batch_s* b, void* p) {
   const size_t g = size_t(a->kv_heads), nk = size_t(b->ktiles) * g * tile_bytes(a);
   const size_t nq = size_t(b->qtiles) * g * tile_bytes(a);
   Backward x{};
-  x.kr = c.take(nk);
-  x.kc = c.take(nk);
-  x.vr = c.take(nk);
-  x.qr = c.take(nq);
-  x.qc = c.take(nq);
-  x.gr = c.take(nq);
-  x.gc = c.take(nq);
+  x.kbytes = nk;  // tiles are multiples of 1 KB
+  x.qbytes = nq;
+  x.kforms = static_cast<char*>(c.take(kKForms * nk));
+  x.qforms = static_cast<char*>(c.take(kQForms * nq));
   x.bias = static_cast<float*>(c.take(size_t(b->ktiles) * 32 * 4));
   x.rows = static_cast<float*>(c.take(size_t(b->qtiles) * g * 64 * 4));
-  x.part_q = static_cast<float*>(c.take(size_t(b->dq.part_tiles) * 32 * size_t(a->DP) * 4));
-  x.part_k = static_cast<float*>(c.take(size_t(b->dkv.part_tiles) * 32 * size_t(a->DP) * 4));
-  x.part_v = static_cast<float*>(c.take(size_t(b->dkv.part_tiles) * 32 * size_t(a->DP) * 4));
+  x.part_q = static_cast<float*>(c.take(size_t(b->bwd.part_tiles[0]) * 32 * size_t(a->DP) * 4));
+  x.part_k = static_cast<float*>(c.take(size_t(b->bwd.part_tiles[1]) * 32 * size_t(a->DP) * 4));
+  x.part_v = static_cast<float*>(c.take(size_t(b->bwd.part_tiles[1]) * 32 * size_t(a->DP) * 4));
   x.bytes = c.used;
   return x;
 }
 
 int64_t fwd_part_tiles(const cgtp_attn_batch_s* b) {
-  return std::max(std::max(b->fwd.part_tiles, b->few.part_tiles), b->wide.part_tiles);
+  return std::max(std::max(b->fwd.part_tiles[0], b->few.part_tiles[0]), b->wide.part_tiles[0]);
 }
 
 }  // namespace
@@ -315,12 +330,22 @@ cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, co
   // workgroups at once: two a compute unit where registers and shared memory allow
   const int es = int(dtype_size(at->dtype)), two = 2 * kCus, one = kCus;
   const int slots = at->DP * es <= 512 ? two : one;
-  build(b->fwd, units(qs, ks, 4, [&](int n) { return n > 1 && n < wide; }), 4, g, slots, 4);
-  build(b->wide, units(qs, ks, 8, [&](int n) { return n >= wide; }), 8, g, two, 4);
-  build(b->few, units(qs, ks, 1, [](int n) { return n == 1; }), 1, g, slots, 8);
-  const int bslots = at->DP * es <= 384 ? two : one;
-  build(b->dq, units(qs, ks, 4, [](int) { return true; }), 4, g, bslots, 4);
-  build(b->dkv, units(ks, qs, 4, [](int) { return true; }), 4, g, bslots, 4);
+  const auto forward = [&](WorkList& w, int per, int slots, int min_len, auto&& take) {
+    std::vector<Unit> u;
+    add_units(u, qs, ks, 0, per, 1, {0}, take);
+    build(w, u, per, g, slots, min_len);
+  };
+  forward(b->fwd, 4, slots, 4, [&](int n) { return n > 1 && n < wide; });
+  forward(b->wide, 8, two, 4, [&](int n) { return n >= wide; });
+  forward(b->few, 1, slots, 8, [](int n) { return n == 1; });
+  std::vector<Unit> u;
+  const auto all = [](int) { return true; };
+  add_units(u, qs, ks, 0, 4, 3, {kItemQ}, all);
+  if (one_pass(at->DP, dtype_size(at->dtype)))
+    add_units(u, ks, qs, 1, 4, 4, {kItemV}, all);
+  else
+    add_units(u, ks, qs, 1, 4, 3, {kItemV, kItemK}, all);
+  build(b->bwd, u, 4, g, at->DP * es <= 384 ? two : one, 4);
   return b.release();
 }
 
@@ -409,11 +434,11 @@ void attn_forward_launch(const cgtp_attn_batch_s* b, RowsIn q, const void* conte
     const WorkList& w = tiles == 8 ? b->wide : tiles == 4 ? b->fwd : b->few;
     if (w.items == 0) continue;
     f.items = w.item_mem.as<Item>();
-    f.joins = w.join_mem.as<Join>();
+    f.joins = w.join_mem[0].as<Join>();
     a->k.fwd(f, w.items, tiles, s);
     CGTP_CHECK_HIP(hipGetLastError());
-    if (w.joins) {
-      a->k.fwd_join(f, w.joins, s);
+    if (w.joins[0]) {
+      a->k.fwd_join(f, w.joins[0], s);
       CGTP_CHECK_HIP(hipGetLastError());
     }
   }
@@ -426,10 +451,10 @@ void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn
   const Backward w = carve_backward(b, ws);
   if (b->ktiles) {
     PackArgs p = context_pack(b, k, v, mask);
-    p.t[0].row_frags = w.kr;
-    p.t[0].col_frags = dq ? w.kc : nullptr;
+    p.t[0].row_frags = w.kforms + kKRows * w.kbytes;
+    p.t[0].col_frags = dq ? w.kforms + kKCols * w.kbytes : nullptr;
     p.bias = w.bias;
-    p.t[1].row_frags = w.vr;
+    p.t[1].row_frags = w.kforms + kVRows * w.kbytes;
     a->k.pack(p, s);
     CGTP_CHECK_HIP(hipGetLastError());
   }
@@ -439,13 +464,13 @@ void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn
     p.t[0].src = q.p;
     p.t[0].ld = q.ld;
     p.t[0].vec = vec_rows(a, q.p, q.ld);
-    p.t[0].row_frags = w.qr;
-    p.t[0].col_frags = keys ? w.qc : nullptr;
+    p.t[0].row_frags = w.qforms + kQRows * w.qbytes;
+    p.t[0].col_frags = keys ? w.qforms + kQCols * w.qbytes : nullptr;
     p.t[1].src = g.p;
     p.t[1].ld = g.ld;
     p.t[1].vec = vec_rows(a, g.p, g.ld);
-    p.t[1].row_frags = w.gr;
-    p.t[1].col_frags = keys ? w.gc : nullptr;
+    p.t[1].row_frags = w.qforms + kGRows * w.qbytes;
+    p.t[1].col_frags = keys ? w.qforms + kGCols * w.qbytes : nullptr;
     p.rows_out = w.rows;
     p.tiles = b->qtile_mem.as<Tile>();
     p.table = a->table.as<int4>();
@@ -464,13 +489,10 @@ void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn
   x.qtiles = b->qtile_mem.as<Tile>();
   x.ktiles = b->ktile_mem.as<Tile>();
   x.table = a->table.as<int4>();
-  x.kr = w.kr;
-  x.kc = w.kc;
-  x.vr = w.vr;
-  x.qr = w.qr;
-  x.qc = w.qc;
-  x.gr = w.gr;
-  x.gc = w.gc;
+  x.kforms_ = w.kforms;
+  x.qforms_ = w.qforms;
+  x.kstride = int64_t(w.kbytes / dtype_size(a->dtype));
+  x.qstride = int64_t(w.qbytes / dtype_size(a->dtype));
   x.bias = w.bias;
   x.rows = w.rows;
   x.dq = dq;
@@ -485,34 +507,29 @@ void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn
   x.G = a->G;
   x.heads = a->heads;
   x.groups = a->kv_heads;
-  if (dq && b->dq.items) {
-    x.items = b->dq.item_mem.as<Item>();
-    x.part = w.part_q;
-    a->k.dq(x, b->dq.items, s);
+  x.part_q = w.part_q;
+  x.part_k = w.part_k;
+  x.part_v = w.part_v;
+  const WorkList& l = b->bwd;
+  if (l.items == 0) return;
+  x.items = l.item_mem.as<Item>();
+  a->k.bwd(x, l.items, s);
+  CGTP_CHECK_HIP(hipGetLastError());
+  if (dq && l.joins[0]) {
+    const GradJoinArgs j{l.join_mem[0].as<Join>(), x.qtiles, x.table, w.part_q, nullptr, dq, nullptr, x.ldq, a->G,
+                         true, x.q_quad};
+    a->k.grad_join(j, l.joins[0], 1, s);
     CGTP_CHECK_HIP(hipGetLastError());
-    if (b->dq.joins) {
-      const GradJoinArgs j{b->dq.join_mem.as<Join>(), x.qtiles, x.table, w.part_q, nullptr, dq, nullptr, x.ldq, a->G,
-                           true, x.q_quad};
-      a->k.grad_join(j, b->dq.joins, 1, s);
-      CGTP_CHECK_HIP(hipGetLastError());
-    }
   }
-  if ((dk || dv) && b->dkv.items) {
-    x.items = b->dkv.item_mem.as<Item>();
-    x.part = w.part_k;
-    x.part_v = w.part_v;
-    a->k.dkv(x, b->dkv.items, s);
-    CGTP_CHECK_HIP(hipGetLastError());
-    if (b->dkv.joins) {
-      GradJoinArgs j{b->dkv.join_mem.as<Join>(), x.ktiles, x.table, w.part_k, w.part_v, dk, dv, x.ldk, 1, false,
-                     x.k_quad};
-      if (!dk) {
-        j.part0 = j.part1;
-        j.dst0 = j.dst1;
-      }
-      a->k.grad_join(j, b->dkv.joins, dk && dv ? 2 : 1, s);
-      CGTP_CHECK_HIP(hipGetLastError());
+  if ((dk || dv) && l.joins[1]) {
+    GradJoinArgs j{l.join_mem[1].as<Join>(), x.ktiles, x.table, w.part_k, w.part_v, dk, dv, x.ldk, 1, false,
+                   x.k_quad};
+    if (!dk) {
+      j.part0 = j.part1;
+      j.dst0 = j.dst1;
     }
+    a->k.grad_join(j, l.joins[1], dk && dv ? 2 : 1, s);
+    CGTP_CHECK_HIP(hipGetLastError());
   }
 }
 
