@@ -73,7 +73,8 @@ struct FwdArgs {
   const float *bias, *norms;
   const int32_t* flags;
   void* out;
-  float *lse, *part, *part_ml;
+  float *lse, *part;
+  float4* part_ml;  // of every row of a part: reference, sum of the rounded weights, of the exact ones
   int64_t ldq, ldo;
   float scale2;     // |scale| log2 e
   uint32_t q_sign;  // flips the queries' signs where the scale is negative

@@ -31,6 +31,7 @@ namespace attn {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -61,6 +62,17 @@ struct Op<bf16> {
 #pragma unroll
     for (int j = 0; j < VE; ++j) r[j] = static_cast<__bf16>(s[VE * f + j]);
     return r;
+  }
+  // c + the sum of an operand's values (products with 1, summed in fp32)
+  static __device__ __forceinline__ float add(Frag a, float c) {
+    const bf16x2 one = {static_cast<__bf16>(1.0f), static_cast<__bf16>(1.0f)};
+    const u32x4 v = __builtin_bit_cast(u32x4, a);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t pair = v[j];
+      c = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), one, c, false);
+    }
+    return c;
   }
 };
 template <>
@@ -336,7 +348,12 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
 // ------------------------------------------------------------------- forward
 
 // Running softmax of 32 queries: a lane holds its query's reference m (log2
-// domain), its own keys' sum l and O^T.
+// domain), its own keys' sum l of the weights as the matrix cores take them, and
+// O^T. bf16 rounds the weights, and O / l is then still a mean of the values with
+// weights that add up to one: a row that sees one key gives exactly its value,
+// and its score gradients P (dP - delta) cancel. Where bf16 results come with the
+// lse, the sum before rounding is formed beside l (from l the lse would be off by
+// up to 2^-9).
 template <int DT>
 struct Running {
   float m = -INFINITY, l = 0.0f;
@@ -356,29 +373,41 @@ __device__ __forceinline__ float top_score(const f32x16& s, float scale2) {
 // by more than 2^8: the weights stay below 2^8 (their sum is fp32), and most
 // tiles need no rescaling of O.
 template <int DT>
-__device__ __forceinline__ void raise_reference(Running<DT>& st, float top) {
+__device__ __forceinline__ void raise_reference(Running<DT>& st, float top, float& e, bool exact) {
   if (__any(top > st.m + 8.0f)) {
     const float mn = fmaxf(st.m, top);
     const float alpha = mn == -INFINITY ? 1.0f : exp2_fast(st.m - mn);
     st.m = mn;
     st.l *= alpha;
+    if (exact) e *= alpha;
 #pragma unroll
     for (int d = 0; d < DT; ++d) st.o[d] *= alpha;
   }
 }
 
-// Turns a tile's products q.k into weights exp2(scale2 q.k - m); m is 0 unless
-// MOVING.
-template <bool MOVING, int DT>
-__device__ __forceinline__ void weigh(Running<DT>& st, f32x16& s, float scale2) {
+// Turns a tile's products q.k into weights exp2(scale2 q.k - m), the operands p;
+// m is 0 unless MOVING.
+template <typename T, bool MOVING, int DT>
+__device__ __forceinline__ void weigh(Running<DT>& st, f32x16& s, float scale2, float& e, bool exact,
+                                      typename Op<T>::Frag (&p)[16 / Op<T>::VE]) {
   const float ref = !MOVING || st.m == -INFINITY ? 0.0f : st.m;
-  float sum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    s[i] = exp2_fast(MOVING ? fmaf(s[i], scale2, -ref) : s[i] * scale2);
-    sum += s[i];
+  for (int i = 0; i < 16; ++i) s[i] = exp2_fast(MOVING ? fmaf(s[i], scale2, -ref) : s[i] * scale2);
+#pragma unroll
+  for (int f = 0; f < 16 / Op<T>::VE; ++f) p[f] = Op<T>::from_acc(s, f);
+  const auto add = [&](float& to) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum += s[i];
+    to += sum;
+  };
+  if constexpr (sizeof(T) == 2) {
+    if (exact) add(e);
+#pragma unroll
+    for (int f = 0; f < 16 / Op<T>::VE; ++f) st.l = Op<T>::add(p[f], st.l);
+  } else {
+    add(st.l);
   }
-  st.l += sum;
 }
 
 // Adds 0 or -inf for every key of a tile with masked or missing keys.
@@ -426,9 +455,9 @@ constexpr int dkv_forms(int part) { return part == 0 ? 4 : part == 1 ? 2 : 3; }
 // Writes a wave's result: final rows, or an unnormalised part of a split.
 template <typename T, int DP>
 __device__ __forceinline__ void finish(const FwdArgs& a, const Item& it, const Tile& tl, int tile_in_item,
-                                       const Running<DP / 32>& st) {
+                                       const Running<DP / 32>& st, float exact_sum) {
   const int lane = lane_id(), n = lane % 32, h = lane / 32;
-  const float l = half_sum(st.l);
+  const float l = half_sum(st.l), e = sizeof(T) == 2 ? half_sum(exact_sum) : l;
   if (it.slot >= 0) {
     const int64_t r = (int64_t(it.slot) * it.stride + tile_in_item) * 32 + n;
     float* o = a.part + r * DP;
@@ -441,10 +470,7 @@ __device__ __forceinline__ void finish(const FwdArgs& a, const Item& it, const T
         for (int i = 0; i < 4; ++i) v[i] = st.o[d][4 * b + i];
         *reinterpret_cast<f32x4*>(o + 32 * d + 8 * b + 4 * h) = v;
       }
-    if (h == 0) {
-      a.part_ml[2 * r] = st.m;
-      a.part_ml[2 * r + 1] = l;
-    }
+    if (h == 0) a.part_ml[r] = make_float4(st.m, l, e, 0.0f);
     return;
   }
   if (n >= tl.n) return;
@@ -461,7 +487,7 @@ __device__ __forceinline__ void finish(const FwdArgs& a, const Item& it, const T
       scatter4(out, a.table, 32 * d + 8 * b + 4 * h, true, head, a.out_quad, v);
     }
   if (a.lse && h == 0)
-    a.lse[int64_t(token) * a.heads + head] = l > 0.0f || l != l ? (st.m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+    a.lse[int64_t(token) * a.heads + head] = l > 0.0f || l != l ? (st.m + __log2f(e)) * 0.69314718055994531f : -INFINITY;
 }
 
 // Tiles of the keys and of the values in shared memory: R - 1 turns for a copy to
@@ -519,7 +545,7 @@ __global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T,
   using Frag = typename Op<T>::Frag;
   constexpr int R = fwd_ring<T, DP>();
   __shared__ u32x4 kb[R][D::UNITS * 64], vb[R][D::UNITS * 64];
-  __shared__ float bounds[4];
+  __shared__ float bounds[4], sums[sizeof(T) == 2 ? RT : 1][kThreads];
   const Item it = ldc(a.items + blockIdx.x);
   if (it.tiles == 0) return;
   const int lane = int(threadIdx.x) % 64, wave = wave_id(), h = lane / 32;
@@ -538,10 +564,14 @@ __global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T,
   if (n > 0)
 #pragma unroll
     for (int t = 0; t + 1 < R; ++t) copy(t, t);
+  // a lane's own entry for each of its queries: no register to spare for it where RT = 2
+  const bool exact = sizeof(T) == 2 && a.lse != nullptr;
+  const auto sum = [&](int r) -> float& { return sums[sizeof(T) == 2 ? r : 0][threadIdx.x]; };
   Frag q[RT][D::KSTEPS];
   Running<D::DT> st[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
+    sum(r) = 0.0f;
     load_queries<T, DP>(a, ldc(a.qtiles + it.a0 + (r < mine ? wave * RT + r : 0)), it.hk, lane, q[r]);
 #pragma unroll
     for (int d = 0; d < D::DT; ++d) st[r].o[d] = zero16();
@@ -580,10 +610,8 @@ __global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T,
         Frag p[N][D::FR];
 #pragma unroll
         for (int r = 0; r < N; ++r) {
-          if (kMoving) raise_reference(st[R0 + r], top_score(s[r], a.scale2));
-          weigh<kMoving>(st[R0 + r], s[r], a.scale2);
-#pragma unroll
-          for (int f = 0; f < D::FR; ++f) p[r][f] = Op<T>::from_acc(s[r], f);
+          if (kMoving) raise_reference(st[R0 + r], top_score(s[r], a.scale2), sum(R0 + r), exact);
+          weigh<T, kMoving>(st[R0 + r], s[r], a.scale2, sum(R0 + r), exact, p[r]);
         }
 #pragma unroll
         for (int d = 0; d < D::DT; ++d)
@@ -617,7 +645,7 @@ __global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T,
   }
 #pragma unroll
   for (int r = 0; r < RT; ++r)
-    if (r < mine) finish<T, DP>(a, it, ldc(a.qtiles + it.a0 + wave * RT + r), wave * RT + r, st[r]);
+    if (r < mine) finish<T, DP>(a, it, ldc(a.qtiles + it.a0 + wave * RT + r), wave * RT + r, st[r], sum(r));
 }
 
 // At most 32 query rows against a long context (single tokens): the four waves
@@ -627,7 +655,7 @@ __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void fwd_few_ke
   using D = Dims<T, DP>;
   using Frag = typename Op<T>::Frag;
   __shared__ f32x4 sh[2][D::DT * 4 * 64];
-  __shared__ float ml[4][2][64];
+  __shared__ float ml[4][3][64];
   const Item it = ldc(a.items + blockIdx.x);
   if (it.tiles == 0) return;
   const int lane = int(threadIdx.x) % 64, wave = wave_id(), h = lane / 32;
@@ -652,6 +680,8 @@ __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void fwd_few_ke
   Frag q[D::KSTEPS];
   load_queries<T, DP>(a, tl, it.hk, lane, q);
   Running<D::DT> st;
+  float e = 0.0f;
+  const bool exact = sizeof(T) == 2 && a.lse != nullptr;
 #pragma unroll
   for (int d = 0; d < D::DT; ++d) st.o[d] = zero16();
   for (int t = it.b0 + wave; t < it.b1; t += 4) {
@@ -667,11 +697,9 @@ __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void fwd_few_ke
     }
     fetch(tile(a.kf, t + 4), k);
     if (ldc(a.flags + t)) mask_scores(sc, a.bias + int64_t(t) * 32, h);
-    raise_reference(st, top_score(sc, a.scale2));
-    weigh<true>(st, sc, a.scale2);
+    raise_reference(st, top_score(sc, a.scale2), e, exact);
     Frag p[D::FR];
-#pragma unroll
-    for (int f = 0; f < D::FR; ++f) p[f] = Op<T>::from_acc(sc, f);
+    weigh<T, true>(st, sc, a.scale2, e, exact, p);
 #pragma unroll
     for (int d = 0; d < D::DT; ++d)
 #pragma unroll
@@ -695,9 +723,11 @@ __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void fwd_few_ke
   const float f = m == -INFINITY ? 1.0f : exp2_fast(st.m - m);
   st.m = m;
   st.l *= f;
+  e *= f;
 #pragma unroll
   for (int d = 0; d < D::DT; ++d) st.o[d] *= f;
   ml[wave][1][lane] = st.l;
+  ml[wave][2][lane] = e;
 #pragma unroll
   for (int round = 2; round >= 1; --round) {
     // the upper `round` waves write, the lower ones add
@@ -725,7 +755,8 @@ __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void fwd_few_ke
   }
   if (wave == 0) {
     st.l = ml[0][1][lane] + ml[2][1][lane] + (ml[1][1][lane] + ml[3][1][lane]);
-    finish<T, DP>(a, it, tl, 0, st);
+    e = ml[0][2][lane] + ml[2][2][lane] + (ml[1][2][lane] + ml[3][2][lane]);
+    finish<T, DP>(a, it, tl, 0, st, e);
   }
 }
 
@@ -739,16 +770,18 @@ __global__ __launch_bounds__(kThreads) void fwd_join_kernel(FwdArgs a) {
   const int n = int(threadIdx.x) / 8, d = int(blockIdx.y) * 32 + int(threadIdx.x) % 8 * 4;
   if (n >= tl.n) return;
   const int64_t first = (int64_t(j.slot) * j.stride + j.within) * 32 + n, step = int64_t(j.stride) * 32;
-  float m = -INFINITY, l = 0.0f;
+  float m = -INFINITY, l = 0.0f, e = 0.0f;
 #pragma unroll 4
-  for (int k = 0; k < j.parts; ++k) m = fmaxf(m, a.part_ml[2 * (first + k * step)]);
+  for (int k = 0; k < j.parts; ++k) m = fmaxf(m, a.part_ml[first + k * step].x);
   const float ref = m == -INFINITY ? 0.0f : m;
   float v[4] = {0, 0, 0, 0};
 #pragma unroll 4
   for (int k = 0; k < j.parts; ++k) {
     const int64_t r = first + k * step;
-    const float w = exp2_fast(a.part_ml[2 * r] - ref);
-    l += a.part_ml[2 * r + 1] * w;
+    const float4 ml = a.part_ml[r];
+    const float w = exp2_fast(ml.x - ref);
+    l += ml.y * w;
+    e += ml.z * w;
     const f32x4 o = *reinterpret_cast<const f32x4*>(a.part + r * DP + d);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] += w * o[i];
@@ -759,7 +792,7 @@ __global__ __launch_bounds__(kThreads) void fwd_join_kernel(FwdArgs a) {
   for (int i = 0; i < 4; ++i) v[i] *= inv;
   scatter4(static_cast<T*>(a.out) + int64_t(token) * a.ldo, a.table, d, true, head, a.out_quad, v);
   if (a.lse && d == 0)
-    a.lse[int64_t(token) * a.heads + head] = l > 0.0f || l != l ? (ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+    a.lse[int64_t(token) * a.heads + head] = l > 0.0f || l != l ? (ref + __log2f(e)) * 0.69314718055994531f : -INFINITY;
 }
 
 // ------------------------------------------------------------------ backward

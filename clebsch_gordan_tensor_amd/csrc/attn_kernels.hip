@@ -352,7 +352,7 @@ cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, co
 size_t attn_context_bytes(const cgtp_attn_batch_s* b) { return carve_context(b, nullptr).bytes; }
 
 size_t attn_forward_ws_bytes(const cgtp_attn_batch_s* b, bool packed) {
-  const size_t part = size_t(fwd_part_tiles(b)) * 32 * (size_t(b->attn->DP) + 2) * 4;
+  const size_t part = size_t(fwd_part_tiles(b)) * 32 * (size_t(b->attn->DP) + 4) * 4;
   return up16(part) + (packed ? 0 : attn_context_bytes(b));
 }
 
@@ -421,8 +421,8 @@ void attn_forward_launch(const cgtp_attn_batch_s* b, RowsIn q, const void* conte
   f.ldo = a->qrow.dim;
   f.out_quad = quad_rows(a, out);
   f.lse = lse;
-  f.part_ml = static_cast<float*>(ws);
-  f.part = f.part_ml + size_t(fwd_part_tiles(b)) * 64;
+  f.part_ml = static_cast<float4*>(ws);
+  f.part = reinterpret_cast<float*>(f.part_ml + size_t(fwd_part_tiles(b)) * 32);
   // a zero scale stays a small positive one: every score is then 0 all the same
   f.scale2 = std::max(float(std::fabs(scale) * 1.4426950408889634), 1e-37f);
   f.q_sign = scale < 0.0 ? (a->dtype == CGTP_BF16 ? 0x80008000u : 0x80000000u) : 0u;

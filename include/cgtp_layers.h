@@ -118,7 +118,8 @@ cgtp_status cgtp_dropout_backward(cgtp_dropout drop, int64_t B, const void* grad
  * masked keys' rows are never used (they may hold infinities or NaN; their
  * gradients are 0). fp32 (fp32 matrix cores) and bf16 (products of bf16 values
  * summed in fp32; softmax weights and the score gradients are rounded to bf16
- * as matrix operands). D <= 256.
+ * as matrix operands, and the weights are normalised by the sum of what they
+ * were rounded to, so a row that sees one key gets exactly its value). D <= 256.
  * Errors: PARSE; UNSUPPORTED (fp64, heads does not divide a multiplicity, D >
  * 256, a degree above CGTP_LMAX); INVALID_ARG (heads or kv_heads < 1, kv_heads
  * does not divide heads). */

@@ -284,3 +284,44 @@ def test_refusals():
         with pytest.raises(cgtp.CgtpError) as e:
             bad()
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("irreps,heads,kv_heads,nq", [
+    ("35x0e+21x1o+7x2e", 7, 1, [1, 70, 5]),                         # few rows; ordinary
+    ("128x0e+128x1o", 4, 2, [3, 300, 40]),                          # 64-row waves
+    ("128x0e+128x1o+128x2e", 8, 4, [50, 140, 1]),
+])
+def test_rows_that_see_one_key(irreps, heads, kv_heads, nq):
+    """bf16: such a row is its value exactly, and its score gradients cancel.
+
+    out = (w v) / w with the same rounded weight w, v to fp32's last bits, rounded to v.
+    grad_q = scale P (dP - delta) k, dP and delta the same D products g v summed in
+    fp32 in two orders, each sum off by at most D 2^-24 sum |g v| from the exact one.
+    grad_k adds such terms over queries and heads. P is 1 to 2e-5, and rounding to
+    bf16 (twice) adds 2^-8 of the result: a factor of 1.1 covers both."""
+    nk, rng = [40, 65, 3], np.random.default_rng(23)
+    q, k, v, g = inputs(irreps, heads, kv_heads, nq, nk, "bf16", seed=21)
+    qp, kp = ptr_of(nq), ptr_of(nk)
+    seen = [rng.integers(a, b) for a, b in zip(kp[:-1], kp[1:])]
+    mask = torch.zeros(kp[-1], dtype=torch.bool)
+    mask[seen] = True
+    attn = layers.CrossAttention(irreps, heads, kv_heads, dtype="bf16")
+    batch = attn.batch(layers.Samples(qp), layers.Samples(kp))
+    out, lse = attn.forward(batch, q, k, v, key_mask=mask.cuda(), need_lse=True)
+    dq, dk, _ = (host(t) for t in attn.backward(batch, q, k, v, out, lse, g, key_mask=mask.cuda()))
+    hq, hk, hv, hg, ho = host(q), host(k), host(v), host(g), host(out)
+    kvi = ol.kv_irreps(irreps, heads, kv_heads)
+    for s, j in enumerate(seen):
+        for h in range(heads):
+            rows = np.ix_(np.arange(qp[s], qp[s + 1]), ol.head_columns(irreps, heads, h))
+            cols = ol.head_columns(kvi, kv_heads, h * kv_heads // heads)
+            assert np.array_equal(ho[rows], np.broadcast_to(hv[j, cols], ho[rows].shape))
+            sums = 2 * len(cols) * 2.0 ** -24 * np.abs(hg[rows] * hv[j, cols]).sum(1, keepdims=True)
+            assert (np.abs(dq[rows]) <= 1.1 * attn.scale * sums * np.abs(hk[j, cols])).all()
+        for h in range(kv_heads):
+            cols, bound = ol.head_columns(kvi, kv_heads, h), 0.0
+            for hh in range(h * heads // kv_heads, (h + 1) * heads // kv_heads):
+                rows = np.ix_(np.arange(qp[s], qp[s + 1]), ol.head_columns(irreps, heads, hh))
+                sums = 2 * len(cols) * 2.0 ** -24 * np.abs(hg[rows] * hv[j, cols]).sum(1, keepdims=True)
+                bound = bound + (sums * np.abs(hq[rows])).sum(0)
+            assert (np.abs(dk[j, cols]) <= 1.1 * attn.scale * bound).all()
