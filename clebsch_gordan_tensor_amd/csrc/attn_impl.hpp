@@ -173,25 +173,50 @@ __device__ __forceinline__ int64_t elem(const int4& e, bool query, int head) {
   return (query ? e.x : e.y) + int64_t(head) * e.z;
 }
 
-// 16 bytes (VE elements from d0 on) of a row; zeros outside the head.
-template <typename T>
-__device__ __forceinline__ u32x4 gather16(const T* row, const int4* table, int d0, bool query, int head, bool vec) {
+// Rows are read without conditions: places outside the head have the table entry
+// 0, i.e. the row's start, and are cleared when all loads are on their way (a
+// condition around each would make every load wait for the one before).
+
+// Pieces d0 = VE (first + 8 c) of a row, c = 0 .. PER - 1 (the last valid piece
+// where there are fewer).
+template <typename T, int PIECES, int PER>
+__device__ __forceinline__ void load_pieces(const T* row, const int4* table, int first, bool query, int head, bool vec,
+                                            u32x4 (&v)[PER]) {
   constexpr int VE = Op<T>::VE;
-  u32x4 v = {0, 0, 0, 0};
-  const int4 e = table[d0];
   if (vec) {
-    if (e.w) v = *reinterpret_cast<const u32x4*>(row + elem(e, query, head));
-  } else if (e.w) {
-    T t[VE];
 #pragma unroll
-    for (int j = 0; j < VE; ++j) {
-      const int4 ej = table[d0 + j];
-      t[j] = T{};
-      if (ej.w) t[j] = row[elem(ej, query, head)];
-    }
-    __builtin_memcpy(&v, t, 16);
+    for (int c = 0; c < PER; ++c)
+      v[c] = *reinterpret_cast<const u32x4*>(row + elem(table[VE * min(first + 8 * c, PIECES - 1)], query, head));
+  } else {
+    T t[PER][VE];
+#pragma unroll
+    for (int c = 0; c < PER; ++c)
+#pragma unroll
+      for (int j = 0; j < VE; ++j) t[c][j] = row[elem(table[VE * min(first + 8 * c, PIECES - 1) + j], query, head)];
+#pragma unroll
+    for (int c = 0; c < PER; ++c) __builtin_memcpy(&v[c], t[c], 16);
   }
+}
+
+// The elements of piece d0 that lie inside the head.
+template <typename T>
+__device__ __forceinline__ u32x4 inside_head(u32x4 v, const int4* table, int d0, bool vec) {
+  constexpr int VE = Op<T>::VE;
+  if (vec) return table[d0].w ? v : u32x4{0, 0, 0, 0};
+  T t[VE];
+  __builtin_memcpy(t, &v, 16);
+#pragma unroll
+  for (int j = 0; j < VE; ++j)
+    if (!table[d0 + j].w) t[j] = T{};
+  __builtin_memcpy(&v, t, 16);
   return v;
+}
+
+// Table entry d0 of the lower half of a wave, d0 + step of the upper one, by the
+// scalar unit.
+__device__ __forceinline__ int4 half_entry(const int4* table, int d0, int step, int h) {
+  const int4 a = ldc(table + d0), b = ldc(table + d0 + step);
+  return h ? b : a;
 }
 
 // Four consecutive head elements d0 .. d0 + 3 of one row, from fp32.
@@ -209,6 +234,31 @@ __device__ __forceinline__ void scatter4(T* row, const int4* table, int d0, bool
       if (ej.w) from_acc(row[elem(ej, query, head)], v[j]);
     }
   }
+}
+
+// A lane's part of a row (transposed accumulators g times scale): elements
+// 8 b + 4 h .. + 3 of every column group.
+template <typename T, int DT>
+__device__ __forceinline__ void scatter_acc(T* row, const int4* table, bool query, int head, bool quad, int h,
+                                            const f32x16 (&g)[DT], float scale) {
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = g[d][4 * b + i] * scale;
+      if (quad) {
+        const int4 e = half_entry(table, 32 * d + 8 * b, 4, h);
+        if (e.w) VecIO<T, 4>::store(row + elem(e, query, head), v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int4 e = half_entry(table, 32 * d + 8 * b + i, 4, h);
+          if (e.w) from_acc(row[elem(e, query, head)], v[i]);
+        }
+      }
+    }
 }
 
 // ------------------------------------------------------------------ packing
@@ -244,20 +294,22 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
   const bool live = in && (a.mask == nullptr || a.mask[token] != 0);
   const float lse = grads && in ? a.lse[int64_t(token) * a.heads + head] : 0.0f;
   const bool live1 = live && (!grads || lse > -INFINITY);
+  // the others' places are read from the tile's first row
+  const auto row = [&](const void* src, int64_t ld, bool live) {
+    return static_cast<const T*>(src) + int64_t(live ? token : tl.row0 / G) * ld;
+  };
   u32x4 v0[PER], v1[PER], vo[PER];
+  load_pieces<T, PIECES>(row(a.t[0].src, a.t[0].ld, live), a.table, tid % 8, query, head, a.t[0].vec, v0);
+  load_pieces<T, PIECES>(row(a.t[1].src, a.t[1].ld, live1), a.table, tid % 8, query, head, a.t[1].vec, v1);
+  if (grads) load_pieces<T, PIECES>(row(a.out, a.ldo, live1), a.table, tid % 8, query, head, a.out_vec, vo);
 #pragma unroll
   for (int c = 0; c < PER; ++c) {
-    const int p = tid % 8 + 8 * c;
-    v0[c] = v1[c] = vo[c] = u32x4{0, 0, 0, 0};
-    if (PIECES % 8 != 0 && p >= PIECES) break;
-    const auto piece = [&](const void* src, int64_t ld, bool vec) {
-      return gather16(static_cast<const T*>(src) + int64_t(token) * ld, a.table, p * VE, query, head, vec);
-    };
-    if (live) v0[c] = piece(a.t[0].src, a.t[0].ld, a.t[0].vec);
-    if (live1) {
-      v1[c] = piece(a.t[1].src, a.t[1].ld, a.t[1].vec);
-      if (grads) vo[c] = piece(a.out, a.ldo, a.out_vec);
-    }
+    const u32x4 none = {0, 0, 0, 0};
+    const int p = tid % 8 + 8 * c, d0 = VE * min(p, PIECES - 1);
+    const bool piece = PIECES % 8 == 0 || p < PIECES;
+    v0[c] = piece && live ? inside_head<T>(v0[c], a.table, d0, a.t[0].vec) : none;
+    v1[c] = piece && live1 ? inside_head<T>(v1[c], a.table, d0, a.t[1].vec) : none;
+    vo[c] = grads && piece && live1 ? inside_head<T>(vo[c], a.table, d0, a.out_vec) : none;
   }
   const int64_t at = int64_t(tile) * a.groups + hk;
   // piece p of row r is lane r + 32 (p % 2) of row fragment p / 2
@@ -429,12 +481,31 @@ __device__ __forceinline__ void load_queries(const FwdArgs& a, const Tile& tl, i
   const int row = tl.row0 + (n < tl.n ? n : tl.n - 1);
   const int token = row / a.G, head = hk * a.G + row % a.G;
   const T* src = static_cast<const T*>(a.q) + int64_t(token) * a.ldq;
+  // a negative scale: the sign goes to the queries
+  if (a.q_vec) {
+    u32x4 v[D::KSTEPS];
 #pragma unroll
-  for (int t = 0; t < D::KSTEPS; ++t)
-  {
-    u32x4 v = gather16(src, a.table, 2 * D::VE * t + D::VE * h, true, head, a.q_vec);
-    v ^= a.q_sign;  // a negative scale: the sign goes to the queries
-    q[t] = as_frag<typename Op<T>::Frag>(v);
+    for (int t = 0; t < D::KSTEPS; ++t)
+      v[t] = *reinterpret_cast<const u32x4*>(src + elem(half_entry(a.table, 2 * D::VE * t, D::VE, h), true, head));
+#pragma unroll
+    for (int t = 0; t < D::KSTEPS; ++t) {
+      const u32x4 inside = half_entry(a.table, 2 * D::VE * t, D::VE, h).w ? v[t] : u32x4{0, 0, 0, 0};
+      q[t] = as_frag<typename Op<T>::Frag>(inside ^ a.q_sign);
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < D::KSTEPS; ++t) {
+      T e[D::VE];
+#pragma unroll
+      for (int j = 0; j < D::VE; ++j) {
+        const int4 at = half_entry(a.table, 2 * D::VE * t + j, D::VE, h);
+        const T x = src[elem(at, true, head)];
+        e[j] = at.w ? x : T{};
+      }
+      u32x4 v;
+      __builtin_memcpy(&v, e, 16);
+      q[t] = as_frag<typename Op<T>::Frag>(v ^ a.q_sign);
+    }
   }
 }
 
@@ -476,16 +547,7 @@ __device__ __forceinline__ void finish(const FwdArgs& a, const Item& it, const T
   if (n >= tl.n) return;
   const int row = tl.row0 + n, token = row / a.G, head = it.hk * a.G + row % a.G;
   const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-  T* out = static_cast<T*>(a.out) + int64_t(token) * a.ldo;
-#pragma unroll
-  for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      float v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = st.o[d][4 * b + i] * inv;
-      scatter4(out, a.table, 32 * d + 8 * b + 4 * h, true, head, a.out_quad, v);
-    }
+  scatter_acc(static_cast<T*>(a.out) + int64_t(token) * a.ldo, a.table, true, head, a.out_quad, h, st.o, inv);
   if (a.lse && h == 0)
     a.lse[int64_t(token) * a.heads + head] = l > 0.0f || l != l ? (st.m + __log2f(e)) * 0.69314718055994531f : -INFINITY;
 }
@@ -818,16 +880,7 @@ __device__ __forceinline__ void finish_grad(const BwdArgs& a, const Item& it, co
   }
   if (n >= tl.n) return;
   const int row = tl.row0 + n, G = query ? a.G : 1, token = row / G, head = it.hk * G + row % G;
-  T* out = static_cast<T*>(dst) + int64_t(token) * ld;
-#pragma unroll
-  for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      float v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = g[d][4 * b + i] * scale;
-      scatter4(out, a.table, 32 * d + 8 * b + 4 * h, query, head, quad, v);
-    }
+  scatter_acc(static_cast<T*>(dst) + int64_t(token) * ld, a.table, query, head, quad, h, g, scale);
 }
 
 // grad_q: as the forward, a wave keeps 32 query rows and walks the key tiles:
