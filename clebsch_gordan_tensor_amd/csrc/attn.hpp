@@ -48,7 +48,7 @@ struct PackArgs {
   float* norms;         // context: largest |k|^2 of every tile and head (or NULL)
   int32_t* flags;       // context: whether a tile has a masked or missing key (or NULL)
   int G, heads, groups;  // G = 0: context rows
-  int ntiles;
+  int ntiles, size;  // size: elements of a head
   bool out_vec;
 };
 

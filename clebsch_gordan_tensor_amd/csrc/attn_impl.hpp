@@ -198,17 +198,18 @@ __device__ __forceinline__ void load_pieces(const T* row, const int4* table, int
   }
 }
 
-// The elements of piece d0 that lie inside the head.
+// The elements of piece d0 that lie inside a head of `size` elements.
 template <typename T>
-__device__ __forceinline__ u32x4 inside_head(u32x4 v, const int4* table, int d0, bool vec) {
+__device__ __forceinline__ u32x4 inside_head(u32x4 v, int d0, int size) {
   constexpr int VE = Op<T>::VE;
-  if (vec) return table[d0].w ? v : u32x4{0, 0, 0, 0};
-  T t[VE];
-  __builtin_memcpy(t, &v, 16);
+  if (d0 + VE > size) {
+    T t[VE];
+    __builtin_memcpy(t, &v, 16);
 #pragma unroll
-  for (int j = 0; j < VE; ++j)
-    if (!table[d0 + j].w) t[j] = T{};
-  __builtin_memcpy(&v, t, 16);
+    for (int j = 0; j < VE; ++j)
+      if (d0 + j >= size) t[j] = T{};
+    __builtin_memcpy(&v, t, 16);
+  }
   return v;
 }
 
@@ -291,25 +292,22 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
   const int token = grow / G, head = hk * G + grow % G;
   const bool grads = a.rows_out != nullptr;  // tensor 1 is grad_out
   // masked rows, and gradients of rows that saw nothing, count as zero
-  const bool live = in && (a.mask == nullptr || a.mask[token] != 0);
-  const float lse = grads && in ? a.lse[int64_t(token) * a.heads + head] : 0.0f;
-  const bool live1 = live && (!grads || lse > -INFINITY);
-  // the others' places are read from the tile's first row
-  const auto row = [&](const void* src, int64_t ld, bool live) {
-    return static_cast<const T*>(src) + int64_t(live ? token : tl.row0 / G) * ld;
-  };
+  const uint8_t seen = a.mask ? a.mask[token] : 1;
+  const float lse = grads ? a.lse[int64_t(token) * a.heads + head] : 0.0f;
+  // (rows that do not count are read as well: the mask need not be waited for)
+  const auto row = [&](const void* src, int64_t ld) { return static_cast<const T*>(src) + int64_t(token) * ld; };
   u32x4 v0[PER], v1[PER], vo[PER];
-  load_pieces<T, PIECES>(row(a.t[0].src, a.t[0].ld, live), a.table, tid % 8, query, head, a.t[0].vec, v0);
-  load_pieces<T, PIECES>(row(a.t[1].src, a.t[1].ld, live1), a.table, tid % 8, query, head, a.t[1].vec, v1);
-  if (grads) load_pieces<T, PIECES>(row(a.out, a.ldo, live1), a.table, tid % 8, query, head, a.out_vec, vo);
+  load_pieces<T, PIECES>(row(a.t[0].src, a.t[0].ld), a.table, tid % 8, query, head, a.t[0].vec, v0);
+  load_pieces<T, PIECES>(row(a.t[1].src, a.t[1].ld), a.table, tid % 8, query, head, a.t[1].vec, v1);
+  if (grads) load_pieces<T, PIECES>(row(a.out, a.ldo), a.table, tid % 8, query, head, a.out_vec, vo);
+  const bool live = in && seen != 0, live1 = live && (!grads || lse > -INFINITY);
 #pragma unroll
   for (int c = 0; c < PER; ++c) {
     const u32x4 none = {0, 0, 0, 0};
-    const int p = tid % 8 + 8 * c, d0 = VE * min(p, PIECES - 1);
-    const bool piece = PIECES % 8 == 0 || p < PIECES;
-    v0[c] = piece && live ? inside_head<T>(v0[c], a.table, d0, a.t[0].vec) : none;
-    v1[c] = piece && live1 ? inside_head<T>(v1[c], a.table, d0, a.t[1].vec) : none;
-    vo[c] = grads && piece && live1 ? inside_head<T>(vo[c], a.table, d0, a.out_vec) : none;
+    const int d0 = VE * (tid % 8 + 8 * c);  // beyond the head where there is no such piece
+    v0[c] = live ? inside_head<T>(v0[c], d0, a.size) : none;
+    v1[c] = live1 ? inside_head<T>(v1[c], d0, a.size) : none;
+    vo[c] = grads && live1 ? inside_head<T>(vo[c], d0, a.size) : none;
   }
   const int64_t at = int64_t(tile) * a.groups + hk;
   // piece p of row r is lane r + 32 (p % 2) of row fragment p / 2

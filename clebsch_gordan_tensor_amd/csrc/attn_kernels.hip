@@ -380,6 +380,7 @@ PackArgs context_pack(const cgtp_attn_batch_s* b, RowsIn k, RowsIn v, const uint
   p.tiles = b->ktile_mem.as<Tile>();
   p.ntiles = int(b->ktiles);
   p.table = a->table.as<int4>();
+  p.size = a->D;
   p.mask = mask;
   p.heads = a->heads;
   p.groups = a->kv_heads;
@@ -474,6 +475,7 @@ void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn
     p.rows_out = w.rows;
     p.tiles = b->qtile_mem.as<Tile>();
     p.table = a->table.as<int4>();
+    p.size = a->D;
     p.out = out;
     p.ldo = a->qrow.dim;
     p.out_vec = vec_rows(a, out, a->qrow.dim);
