@@ -179,11 +179,11 @@ __device__ __forceinline__ int64_t elem(const int4& e, bool query, int head) {
 
 // Pieces d0 = VE (first + 8 c) of a row, c = 0 .. PER - 1 (the last valid piece
 // where there are fewer).
-template <typename T, int PIECES, int PER>
-__device__ __forceinline__ void load_pieces(const T* row, const int4* table, int first, bool query, int head, bool vec,
+template <typename T, bool VEC, int PIECES, int PER>
+__device__ __forceinline__ void load_pieces(const T* row, const int4* table, int first, bool query, int head,
                                             u32x4 (&v)[PER]) {
   constexpr int VE = Op<T>::VE;
-  if (vec) {
+  if constexpr (VEC) {
 #pragma unroll
     for (int c = 0; c < PER; ++c)
       v[c] = *reinterpret_cast<const u32x4*>(row + elem(table[VE * min(first + 8 * c, PIECES - 1)], query, head));
@@ -199,9 +199,10 @@ __device__ __forceinline__ void load_pieces(const T* row, const int4* table, int
 }
 
 // The elements of piece d0 that lie inside a head of `size` elements.
-template <typename T>
+template <typename T, bool VEC>
 __device__ __forceinline__ u32x4 inside_head(u32x4 v, int d0, int size) {
   constexpr int VE = Op<T>::VE;
+  if constexpr (VEC) return d0 < size ? v : u32x4{0, 0, 0, 0};
   if (d0 + VE > size) {
     T t[VE];
     __builtin_memcpy(t, &v, 16);
@@ -270,12 +271,22 @@ __device__ __forceinline__ void scatter_acc(T* row, const int4* table, bool quer
 // fragments by way of shared memory. Bound: memory, each element read once and
 // written once per form; both tensors' loads are issued together, since what
 // holds a small workgroup up is the latency of its chain of loads.
-template <typename T, int DP>
+//
+// VEC: every tensor's runs are whole aligned 16-byte pieces (else read element by
+// element); GRADS: the tensors are q and grad_out, with out for delta. As run-time
+// arguments they cost registers, i.e. waves (ragged batch 615 us against 609 us; with
+// unaligned rows 257 us against 232 us). A context of 32,764 rows of 4 KB packs at
+// 3.8 TB/s read and written, one of 72,000 rows at 4.9 TB/s. Reading whole cache lines
+// across neighbouring heads instead of one head's runs was no faster (155 us against
+// 143 us): the lines are shared in the die's L2 already.
+template <typename T, int DP, bool VEC, bool GRADS>
 __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
   using D = Dims<T, DP>;
   constexpr int VE = D::VE, LD = DP + VE;  // an odd count of 16-byte pieces a row: no bank conflicts
   constexpr int PIECES = DP / VE, PER = (PIECES + 7) / 8;
-  __shared__ __attribute__((aligned(16))) T sh[2][32 * LD];
+  // without GRADS one tensor at most has column fragments
+  constexpr int B = GRADS ? 1 : 0;  // place of tensor 1
+  __shared__ __attribute__((aligned(16))) T sh[B + 1][32 * LD];
   __shared__ float red[32][9];
   // A head's channels are short runs of a row: the heads of one tile share its
   // cache lines, so they go to one die (workgroup index modulo 8), one after another
@@ -290,24 +301,23 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
   const bool in = r < tl.n;
   const int grow = tl.row0 + (in ? r : 0);
   const int token = grow / G, head = hk * G + grow % G;
-  const bool grads = a.rows_out != nullptr;  // tensor 1 is grad_out
   // masked rows, and gradients of rows that saw nothing, count as zero
   const uint8_t seen = a.mask ? a.mask[token] : 1;
-  const float lse = grads ? a.lse[int64_t(token) * a.heads + head] : 0.0f;
+  const float lse = GRADS ? a.lse[int64_t(token) * a.heads + head] : 0.0f;
   // (rows that do not count are read as well: the mask need not be waited for)
   const auto row = [&](const void* src, int64_t ld) { return static_cast<const T*>(src) + int64_t(token) * ld; };
   u32x4 v0[PER], v1[PER], vo[PER];
-  load_pieces<T, PIECES>(row(a.t[0].src, a.t[0].ld), a.table, tid % 8, query, head, a.t[0].vec, v0);
-  load_pieces<T, PIECES>(row(a.t[1].src, a.t[1].ld), a.table, tid % 8, query, head, a.t[1].vec, v1);
-  if (grads) load_pieces<T, PIECES>(row(a.out, a.ldo), a.table, tid % 8, query, head, a.out_vec, vo);
-  const bool live = in && seen != 0, live1 = live && (!grads || lse > -INFINITY);
+  load_pieces<T, VEC, PIECES>(row(a.t[0].src, a.t[0].ld), a.table, tid % 8, query, head, v0);
+  load_pieces<T, VEC, PIECES>(row(a.t[1].src, a.t[1].ld), a.table, tid % 8, query, head, v1);
+  if constexpr (GRADS) load_pieces<T, VEC, PIECES>(row(a.out, a.ldo), a.table, tid % 8, query, head, vo);
+  const bool live = in && seen != 0, live1 = live && (!GRADS || lse > -INFINITY);
 #pragma unroll
   for (int c = 0; c < PER; ++c) {
     const u32x4 none = {0, 0, 0, 0};
     const int d0 = VE * (tid % 8 + 8 * c);  // beyond the head where there is no such piece
-    v0[c] = live ? inside_head<T>(v0[c], d0, a.size) : none;
-    v1[c] = live1 ? inside_head<T>(v1[c], d0, a.size) : none;
-    vo[c] = grads && live1 ? inside_head<T>(vo[c], d0, a.size) : none;
+    v0[c] = live ? inside_head<T, VEC>(v0[c], d0, a.size) : none;
+    v1[c] = live1 ? inside_head<T, VEC>(v1[c], d0, a.size) : none;
+    if constexpr (GRADS) vo[c] = live1 ? inside_head<T, VEC>(vo[c], d0, a.size) : none;
   }
   const int64_t at = int64_t(tile) * a.groups + hk;
   // piece p of row r is lane r + 32 (p % 2) of row fragment p / 2
@@ -328,9 +338,9 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
     const int d0 = (tid % 8 + 8 * c) * VE;
     if (PIECES % 8 != 0 && d0 >= DP) break;
     if (a.t[0].col_frags) *reinterpret_cast<u32x4*>(&sh[0][r * LD + d0]) = v0[c];
-    if (a.t[1].col_frags) *reinterpret_cast<u32x4*>(&sh[1][r * LD + d0]) = v1[c];
+    if (a.t[1].col_frags) *reinterpret_cast<u32x4*>(&sh[B][r * LD + d0]) = v1[c];
   }
-  if (a.norms) {
+  if (!GRADS && a.norms) {
     // |k|^2 of every row, the largest of the tile below
     float n2 = 0.0f;
 #pragma unroll
@@ -342,7 +352,7 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
     }
     red[r][tid % 8] = n2;
   }
-  if (grads) {
+  if constexpr (GRADS) {
     float partial = 0.0f;
 #pragma unroll
     for (int c = 0; c < PER; ++c) {
@@ -355,21 +365,21 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
     red[r][tid % 8] = partial;
   }
   __syncthreads();
-  if (grads && tid % 8 == 0) {
+  if (GRADS && tid % 8 == 0) {
     // log2-domain lse (+inf: the row contributes nothing) and rowsum(grad_out out)
     float d = 0.0f;
     for (int k = 0; k < 8; ++k) d += red[r][k];
     a.rows_out[at * 64 + r] = in && lse > -INFINITY ? lse * 1.44269504088896341f : INFINITY;
     a.rows_out[at * 64 + 32 + r] = d;
   }
-  if (a.norms && wave == 0) {
+  if (!GRADS && a.norms && wave == 0) {
     float n2 = 0.0f;
     for (int k = 0; k < 8; ++k) n2 += red[lane % 32][k];
     const bool nan = __any(n2 != n2);
     n2 = wave_max(n2);
     if (lane == 0) a.norms[at] = nan ? INFINITY : n2;
   }
-  if (a.bias && hk == 0 && tid < 32) {
+  if (!GRADS && a.bias && hk == 0 && tid < 32) {
     const bool seen = tid < tl.n && (a.mask == nullptr || a.mask[tl.row0 + tid] != 0);
     a.bias[int64_t(tile) * 32 + tid] = seen ? 0.0f : -INFINITY;
     const bool some = __any(!seen);
@@ -386,7 +396,7 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
 #pragma unroll
       for (int j = 0; j < VE; ++j) {
         const int rr = VE * f + j;
-        t[j] = sh[k][(8 * (rr / 4) + 4 * h + rr % 4) * LD + 32 * dt + n];
+        t[j] = sh[k * B][(8 * (rr / 4) + 4 * h + rr % 4) * LD + 32 * dt + n];
       }
       u32x4 v;
       __builtin_memcpy(&v, t, 16);
@@ -1134,7 +1144,10 @@ __global__ __launch_bounds__(kThreads) void grad_join_kernel(GradJoinArgs a) {
 template <typename T, int DP>
 struct Kernels {
   static void pack(const PackArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL((pack_kernel<T, DP>), dim3(unsigned((a.ntiles + 7) / 8 * 8 * a.groups)), dim3(kThreads), 0, s, a);
+    const bool grads = a.rows_out != nullptr, vec = a.t[0].vec && a.t[1].vec && (!grads || a.out_vec);
+    const auto k = vec ? (grads ? pack_kernel<T, DP, true, true> : pack_kernel<T, DP, true, false>)
+                       : (grads ? pack_kernel<T, DP, false, true> : pack_kernel<T, DP, false, false>);
+    hipLaunchKernelGGL(k, dim3(unsigned((a.ntiles + 7) / 8 * 8 * a.groups)), dim3(kThreads), 0, s, a);
   }
   static void fwd(const FwdArgs& a, int items, int tiles, hipStream_t s) {
     if (tiles == 1) hipLaunchKernelGGL((fwd_few_kernel<T, DP>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
