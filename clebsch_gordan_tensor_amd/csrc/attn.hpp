@@ -128,7 +128,8 @@ KernelTable kernels_bf16(int dp);
 constexpr bool wide_forward(int dp, size_t size) { return size == 2 && dp <= 128; }
 
 // Whether both gradients of the keys are formed in one pass: their accumulators
-// and operands fit the registers (else four products' worth of work becomes five).
+// and operands fit the registers (else four products' worth of work becomes five:
+// fp32, heads of 128, 3000 queries and 611 keys 231 us in one, 244 us in two).
 constexpr bool one_pass(int dp, size_t size) { return dp <= (size == 2 ? 128 : 160); }
 
 // A list of work items on the device with the joins of its splits: those of the

@@ -561,7 +561,8 @@ __device__ __forceinline__ void finish(const FwdArgs& a, const Item& it, const T
 }
 
 // Tiles of the keys and of the values in shared memory: R - 1 turns for a copy to
-// arrive. Three where that leaves room for two workgroups a compute unit.
+// arrive. Three where that leaves room for two workgroups a compute unit (long
+// contexts, head of 128: 1153 us, with two 1159 us).
 template <typename T, int DP>
 constexpr int fwd_ring() {
   return 6 * Dims<T, DP>::UNITS < 80 ? 3 : 2;
@@ -607,7 +608,8 @@ constexpr float kBound = 60.0f;
 // which with the copies into it take 1.5 times as long as the products else. Two
 // paths: scores bounded beforehand by the rows' norms (what normalised features
 // give) go without maximum, branch and rescaling; others keep a running maximum
-// (for RT = 2 one 32-row half after the other).
+// (for RT = 2 one 32-row half after the other; long contexts, head of 128: 1083 us
+// bounded, 1277 us with it).
 // Measured: 4 x 4096 queries against 8191 keys, 16 heads of 128, bf16: 945 us =
 // 1160 TFLOP/s with matrix cores busy 55 % of the cycles; a ragged batch of heads of
 // 144 (RT = 1): 140 us, 32 %; fp32, heads of 128: 66 %.

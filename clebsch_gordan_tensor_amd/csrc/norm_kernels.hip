@@ -693,7 +693,8 @@ void with_vec(int vec, F&& f) {
 }
 
 // Short samples (at most this many bytes of a block in a sample): one workgroup
-// a sample and narrow strip, one launch forward and two backward.
+// a sample and narrow strip, one launch forward and two backward (96 samples of
+// 20 - 220 rows 53 us, as runs 70 us; 8 molecules forward 8.9 us and 12.7 us).
 constexpr int64_t kSampleBytes = 256 << 10;
 
 bool by_sample(const cgtp_norm_s* n, const cgtp_samples_s* sm) {
@@ -702,7 +703,8 @@ bool by_sample(const cgtp_norm_s* n, const cgtp_samples_s* sm) {
 
 // Longer samples take two passes over the rows. The second reads them from the
 // last-level cache if it follows soon enough, so the rows are worked off in
-// slices of whole samples of about this many bytes a tensor.
+// slices of whole samples of about this many bytes a tensor (104,217 rows of 4 KB
+// 270 us, all at once 315 us).
 constexpr int64_t kSliceBytes = int64_t(160) << 20;
 
 // f(first sample, end sample) for each slice.
