@@ -549,7 +549,9 @@ __device__ __forceinline__ void finish(const FwdArgs& a, const Item& it, const T
         for (int i = 0; i < 4; ++i) v[i] = st.o[d][4 * b + i];
         *reinterpret_cast<f32x4*>(o + 32 * d + 8 * b + 4 * h) = v;
       }
-    if (h == 0) a.part_ml[r] = make_float4(st.m, l, e, 0.0f);
+    // (a part without a visible key has no reference: the 0 of bounded scores would
+    // stand above those of the other parts when they are joined)
+    if (h == 0) a.part_ml[r] = make_float4(l == 0.0f ? -INFINITY : st.m, l, e, 0.0f);
     return;
   }
   if (n >= tl.n) return;

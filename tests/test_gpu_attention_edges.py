@@ -1,0 +1,51 @@
+"""GPU cross attention at the edges of its range: split contexts with parts that
+the mask empties, NaN in queries, values far from one, limits of its arguments."""
+
+import numpy as np
+import pytest
+
+from oracle import layers as ol
+from tests.gpu_util import TOL, dev, host, rel_err
+from tests.test_gpu_attention import inputs, ptr_of
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+cgtp = pytest.importorskip("clebsch_gordan_tensor_amd.cgtp")
+layers = pytest.importorskip("clebsch_gordan_tensor_amd.layers")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("nq", [3, 40, 300])                 # few rows; 32 rows a wave; 64 rows a wave (bf16)
+def test_split_context_whose_last_parts_are_masked(dtype, nq):
+    """Scores near -196 against the first 200 of 2500 keys, the rest masked: a part
+    without a key must not count as one of score 0.
+
+    A score is a sum of 32 products of size 6: rounding leaves at most 32 * 2^-24 * 196
+    = 3.7e-4 of it, twice that of a weight and of its share in the result, so 2e-3 of
+    the largest value covers fp32; bf16 adds its own rounding."""
+    irreps, nk, seen = "32x0e", 2500, 200
+    attn = layers.CrossAttention(irreps, 1, dtype=dtype)
+    rng = np.random.default_rng(31)
+    base = 14.0 / np.sqrt(32)
+    q = dev(-base + 0.1 * rng.standard_normal((nq + 2, 32)), dtype)
+    k = dev(base + 0.1 * rng.standard_normal((nk + 900, 32)), dtype)
+    v, g = dev(rng.standard_normal((nk + 900, 32)), dtype), dev(rng.standard_normal((nq + 2, 32)), dtype)
+    mask = torch.zeros(nk + 900, dtype=torch.bool, device="cuda")
+    mask[:seen] = True                                       # the second sample keeps none of its 900 keys
+    qp, kp = ptr_of([nq, 2]), ptr_of([nk, 900])
+    b = attn.batch(layers.Samples(qp), layers.Samples(kp))
+    assert b.workspace_size(layers.ATTN_FORWARD_PACKED) > 0  # the contexts are split
+    out, lse = attn.forward(b, q, k, v, scale=1.0, key_mask=mask, need_lse=True)
+    dv = attn.backward(b, q, k, v, out, lse, g, scale=1.0, key_mask=mask)[2]
+    torch.cuda.synchronize()
+    args = (irreps, 1, 1, qp, kp, host(q), host(k), host(v), mask.cpu().numpy(), 1.0)
+    ro, rl = ol.attn_forward(*args)
+    rdv = ol.attn_backward(*args, host(g))[2]
+    tol = 2e-3 if dtype == "f32" else TOL[dtype]
+    assert np.array_equal(np.isinf(host(lse)), np.isinf(rl))
+    assert np.abs(host(lse)[:nq] - rl[:nq]).max() <= 1e-3
+    assert rel_err(host(out), ro) <= tol and rel_err(host(dv), rdv) <= tol
+    assert torch.all(out[nq:] == 0)
