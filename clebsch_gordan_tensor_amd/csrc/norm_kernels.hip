@@ -441,7 +441,8 @@ __device__ __forceinline__ void strip_sums(const NormStrip& st, const Place& p, 
               }
         });
       });
-      if constexpr (NC > 1)
+      // (not of an empty sample, whose statistics are not written: 0 times them may be NaN)
+      if (NC > 1 && r0 < r1)
 #pragma unroll
         for (int i = 0; i < VEC; ++i) sum[i] *= rs;
     }
