@@ -1096,6 +1096,14 @@ __device__ __forceinline__ void dkv_item(const BwdArgs& a, const Item& it, u32x4
     __syncthreads();
   }
   if (!active) return;
+  // a masked key's gradients are 0 whatever the queries hold (its weights are, unless a
+  // score or an lse is NaN)
+  if (bias < 0.0f)
+#pragma unroll
+    for (int d = 0; d < D::DT; ++d) {
+      if (WANT_K) dk[d] = zero16();
+      if (WANT_V) dv[d] = zero16();
+    }
   if constexpr (WANT_V)
     if (a.dv) finish_grad<T, DP>(a, it, tl, wave, lane, false, a.dv, a.ldk, a.part_v, a.k_quad, dv, 1.0f);
   if constexpr (WANT_K)

@@ -49,3 +49,20 @@ def test_split_context_whose_last_parts_are_masked(dtype, nq):
     assert np.abs(host(lse)[:nq] - rl[:nq]).max() <= 1e-3
     assert rel_err(host(out), ro) <= tol and rel_err(host(dv), rdv) <= tol
     assert torch.all(out[nq:] == 0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("irreps,heads", [("32x0e+16x1o", 4), ("48x0e+48x1o", 1)])  # both gradients in one pass; in two
+@pytest.mark.parametrize("where", ["query", "key"])
+def test_masked_keys_have_no_gradient_beside_nan(where, irreps, heads, dtype):
+    nq, nk = [40, 300], [90, 700]
+    attn = layers.CrossAttention(irreps, heads, dtype=dtype)
+    q, k, v, g = inputs(irreps, heads, heads, nq, nk, dtype)
+    mask = torch.from_numpy(np.random.default_rng(6).random(sum(nk)) < 0.6).cuda()
+    mask[3] = True
+    (q if where == "query" else k)[3] = float("nan")
+    b = attn.batch(layers.Samples(ptr_of(nq)), layers.Samples(ptr_of(nk)))
+    out, lse = attn.forward(b, q, k, v, key_mask=mask, need_lse=True)
+    _, dk, dv = attn.backward(b, q, k, v, out, lse, g, key_mask=mask)
+    assert torch.isnan(out[3]).all() and torch.isnan(dk[3]).all()
+    assert torch.all(dk[~mask] == 0) and torch.all(dv[~mask] == 0)
