@@ -310,7 +310,7 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
   load_pieces<T, VEC, PIECES>(row(a.t[0].src, a.t[0].ld), a.table, tid % 8, query, head, v0);
   load_pieces<T, VEC, PIECES>(row(a.t[1].src, a.t[1].ld), a.table, tid % 8, query, head, v1);
   if constexpr (GRADS) load_pieces<T, VEC, PIECES>(row(a.out, a.ldo), a.table, tid % 8, query, head, vo);
-  const bool live = in && seen != 0, live1 = live && (!GRADS || lse > -INFINITY);
+  const bool live = in && seen != 0, live1 = live && (!GRADS || lse != -INFINITY);
 #pragma unroll
   for (int c = 0; c < PER; ++c) {
     const u32x4 none = {0, 0, 0, 0};
@@ -366,10 +366,11 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
   }
   __syncthreads();
   if (GRADS && tid % 8 == 0) {
-    // log2-domain lse (+inf: the row contributes nothing) and rowsum(grad_out out)
+    // log2-domain lse (+inf: the row contributes nothing; NaN stays: every weight of the
+    // row is NaN then) and rowsum(grad_out out)
     float d = 0.0f;
     for (int k = 0; k < 8; ++k) d += red[r][k];
-    a.rows_out[at * 64 + r] = in && lse > -INFINITY ? lse * 1.44269504088896341f : INFINITY;
+    a.rows_out[at * 64 + r] = in && lse != -INFINITY ? lse * 1.44269504088896341f : INFINITY;
     a.rows_out[at * 64 + 32 + r] = d;
   }
   if (!GRADS && a.norms && wave == 0) {

@@ -66,3 +66,34 @@ def test_masked_keys_have_no_gradient_beside_nan(where, irreps, heads, dtype):
     _, dk, dv = attn.backward(b, q, k, v, out, lse, g, key_mask=mask)
     assert torch.isnan(out[3]).all() and torch.isnan(dk[3]).all()
     assert torch.all(dk[~mask] == 0) and torch.all(dv[~mask] == 0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("nq", [[40, 3, 70], [1, 1, 1], [5, 300, 9]])
+@pytest.mark.parametrize("where", ["query", "key"])
+def test_nan_reaches_the_gradients(where, nq, dtype):
+    """A NaN in a query with keys is in its own gradient and in those of all keys that it
+    sees; one in a visible key is in every gradient of its sample; none is in another
+    sample's."""
+    irreps, heads, kv_heads, nk = "32x0e+16x1o", 4, 2, [90, 45, 64]
+    qp, kp = ptr_of(nq), ptr_of(nk)
+    attn = layers.CrossAttention(irreps, heads, kv_heads=kv_heads, dtype=dtype)
+    q, k, v, g = inputs(irreps, heads, kv_heads, nq, nk, dtype)
+    b = attn.batch(layers.Samples(qp), layers.Samples(kp))
+    ref = ol.attn_backward(irreps, heads, kv_heads, qp, kp, host(q), host(k), host(v), None, attn.scale, host(g))
+    keys = slice(kp[1], kp[2])
+    if where == "query":
+        q[qp[1]] = float("nan")
+        rows = slice(qp[1], qp[1] + 1)
+    else:
+        k[kp[1] + 7] = float("nan")
+        rows = slice(qp[1], qp[2])
+    out, lse = attn.forward(b, q, k, v, need_lse=True)
+    grads = [host(t) for t in attn.backward(b, q, k, v, out, lse, g)]
+    assert torch.isnan(out[rows]).all() and torch.isnan(lse[rows]).all()
+    # all else as without it, judged against the largest gradient of its kind
+    for got, want, bad in zip(grads, ref, (rows, keys, keys)):
+        assert np.isnan(got[bad]).all()
+        rest = np.delete(got, bad, 0)
+        scale = max(np.abs(want).max(), 0.1 * max(np.abs(r).max() for r in ref))
+        assert np.abs(rest - np.delete(want, bad, 0)).max() <= TOL[dtype] * scale
