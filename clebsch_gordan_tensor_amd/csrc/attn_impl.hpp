@@ -301,7 +301,7 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
   const bool in = r < tl.n;
   const int grow = tl.row0 + (in ? r : 0);
   const int token = grow / G, head = hk * G + grow % G;
-  // masked rows, and gradients of rows that saw nothing, count as zero
+  // masked rows, and queries and gradients of rows that saw nothing, count as zero
   const uint8_t seen = a.mask ? a.mask[token] : 1;
   const float lse = GRADS ? a.lse[int64_t(token) * a.heads + head] : 0.0f;
   // (rows that do not count are read as well: the mask need not be waited for)
@@ -310,14 +310,14 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
   load_pieces<T, VEC, PIECES>(row(a.t[0].src, a.t[0].ld), a.table, tid % 8, query, head, v0);
   load_pieces<T, VEC, PIECES>(row(a.t[1].src, a.t[1].ld), a.table, tid % 8, query, head, v1);
   if constexpr (GRADS) load_pieces<T, VEC, PIECES>(row(a.out, a.ldo), a.table, tid % 8, query, head, vo);
-  const bool live = in && seen != 0, live1 = live && (!GRADS || lse != -INFINITY);
+  const bool live = in && seen != 0 && (!GRADS || lse != -INFINITY);
 #pragma unroll
   for (int c = 0; c < PER; ++c) {
     const u32x4 none = {0, 0, 0, 0};
     const int d0 = VE * (tid % 8 + 8 * c);  // beyond the head where there is no such piece
     v0[c] = live ? inside_head<T, VEC>(v0[c], d0, a.size) : none;
-    v1[c] = live1 ? inside_head<T, VEC>(v1[c], d0, a.size) : none;
-    if constexpr (GRADS) vo[c] = live1 ? inside_head<T, VEC>(vo[c], d0, a.size) : none;
+    v1[c] = live ? inside_head<T, VEC>(v1[c], d0, a.size) : none;
+    if constexpr (GRADS) vo[c] = live ? inside_head<T, VEC>(vo[c], d0, a.size) : none;
   }
   const int64_t at = int64_t(tile) * a.groups + hk;
   // piece p of row r is lane r + 32 (p % 2) of row fragment p / 2
@@ -471,13 +471,14 @@ __device__ __forceinline__ void weigh(Running<DT>& st, f32x16& s, float scale2, 
   }
 }
 
-// Adds 0 or -inf for every key of a tile with masked or missing keys.
+// -inf for every masked or missing key of a tile (not by addition: the score of a
+// NaN query is NaN for such keys too, and a row without a key is 0 whatever it holds).
 __device__ __forceinline__ void mask_scores(f32x16& s, const float* bias, int h) {
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
     const f32x4 bv = *reinterpret_cast<const f32x4*>(bias + 8 * b + 4 * h);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[4 * b + i] += bv[i];
+    for (int i = 0; i < 4; ++i) s[4 * b + i] = bv[i] < 0.0f ? -INFINITY : s[4 * b + i];
   }
 }
 

@@ -97,3 +97,29 @@ def test_nan_reaches_the_gradients(where, nq, dtype):
         rest = np.delete(got, bad, 0)
         scale = max(np.abs(want).max(), 0.1 * max(np.abs(r).max() for r in ref))
         assert np.abs(rest - np.delete(want, bad, 0)).max() <= TOL[dtype] * scale
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("nq", [[40, 3, 70], [1, 1, 1], [5, 300, 9]])
+def test_nan_queries_without_a_key(dtype, nq):
+    """Rows that see no key are 0 with lse -inf whatever they hold, and reach no gradient."""
+    irreps, heads, kv_heads, nk = "32x0e+16x1o", 4, 2, [90, 45, 64]
+    attn = layers.CrossAttention(irreps, heads, kv_heads=kv_heads, dtype=dtype)
+    q, k, v, g = inputs(irreps, heads, kv_heads, nq, nk, dtype)
+    mask = torch.from_numpy(np.random.default_rng(5).random(sum(nk)) < 0.6).cuda()
+    mask[0] = mask[-1] = True
+    mask[90:135] = False                                     # the second sample has no key left
+    b = attn.batch(layers.Samples(ptr_of(nq)), layers.Samples(ptr_of(nk)))
+
+    def step(q):
+        out, lse = attn.forward(b, q, k, v, key_mask=mask, need_lse=True)
+        packed = attn.forward_packed(b, q, attn.pack(b, k, v, key_mask=mask))
+        return (out, packed, lse) + attn.backward(b, q, k, v, out, lse, g, key_mask=mask)
+
+    want = step(q)
+    rows = slice(nq[0], nq[0] + nq[1])
+    assert torch.all(want[0][rows] == 0) and torch.all(want[2][rows] == -float("inf"))
+    for bad in (float("nan"), float("inf")):
+        q2 = q.clone()
+        q2[rows] = bad
+        assert all(torch.equal(x, y) for x, y in zip(step(q2), want))
