@@ -164,6 +164,10 @@ __device__ __forceinline__ void turn_end() {
 __device__ __forceinline__ int lane_id() {
   return int(__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u)));
 }
+// A value that is the same in all lanes, as a scalar.
+__device__ __forceinline__ float uniform(float v) {
+  return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v)));
+}
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(int(threadIdx.x) / 64); }
 
 // Element address of head-vector element d of query row (token, head) or of
@@ -447,13 +451,13 @@ __device__ __forceinline__ void raise_reference(Running<DT>& st, float top, floa
 }
 
 // Turns a tile's products q.k into weights exp2(scale2 q.k - m), the operands p;
-// m is 0 unless MOVING.
+// m is `fixed` unless MOVING.
 template <typename T, bool MOVING, int DT>
-__device__ __forceinline__ void weigh(Running<DT>& st, f32x16& s, float scale2, float& e, bool exact,
+__device__ __forceinline__ void weigh(Running<DT>& st, f32x16& s, float scale2, float fixed, float& e, bool exact,
                                       typename Op<T>::Frag (&p)[16 / Op<T>::VE]) {
-  const float ref = !MOVING || st.m == -INFINITY ? 0.0f : st.m;
+  const float ref = !MOVING ? fixed : st.m == -INFINITY ? 0.0f : st.m;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) s[i] = exp2_fast(MOVING ? fmaf(s[i], scale2, -ref) : s[i] * scale2);
+  for (int i = 0; i < 16; ++i) s[i] = exp2_fast(fmaf(s[i], scale2, -ref));
 #pragma unroll
   for (int f = 0; f < 16 / Op<T>::VE; ++f) p[f] = Op<T>::from_acc(s, f);
   const auto add = [&](float& to) {
@@ -551,7 +555,7 @@ __device__ __forceinline__ void finish(const FwdArgs& a, const Item& it, const T
         for (int i = 0; i < 4; ++i) v[i] = st.o[d][4 * b + i];
         *reinterpret_cast<f32x4*>(o + 32 * d + 8 * b + 4 * h) = v;
       }
-    // (a part without a visible key has no reference: the 0 of bounded scores would
+    // (a part without a visible key has no reference: that of bounded scores would
     // stand above those of the other parts when they are joined)
     if (h == 0) a.part_ml[r] = make_float4(l == 0.0f ? -INFINITY : st.m, l, e, 0.0f);
     return;
@@ -600,10 +604,12 @@ __device__ __forceinline__ float score_bound2(const FwdArgs& a, const Item& it, 
   return nan ? INFINITY : wave_max(qn) * wave_max(kn) * a.scale2 * a.scale2;
 }
 
-// Scores whose size is bounded by 2^kBound need no running maximum: with the
-// reference 0 their exponentials lie within 2^-60 .. 2^60, sums of 2^31 of them
-// stay far inside fp32, and bf16 has fp32's exponent range, so nothing is lost.
-constexpr float kBound = 60.0f;
+// Scores bounded by B <= kBound (log2 domain) need no running maximum: with the
+// reference max(B - 8, 0) their weights are at most 2^8, as with a running maximum, so
+// that values as large as there can be summed, and the largest of a row is at least
+// 2^(8 - 2 kBound) = 2^-72: its products with values above 2^-54 are normal numbers of
+// fp32 (whose exponent range bf16 shares).
+constexpr float kBound = 40.0f;
 
 // Four waves of RT x 32 query rows share the keys through shared memory; the tiles
 // of the next turns are on their way there while one is worked on. Bound: matrix
@@ -661,6 +667,7 @@ __global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T,
   bool bounded = true;
 #pragma unroll
   for (int w = 0; w < 4; ++w) bounded = bounded && bounds[w] <= kBound * kBound;
+  const float fixed = uniform(fmaxf(__builtin_amdgcn_sqrtf(b2) - 8.0f, 0.0f));  // the wave's reference, if bounded
 
   // A wave at its products goes before one at its exponentials, which then fill the
   // gaps (long contexts, head of 128: 1074 us against 1093 us; with 32 rows a wave the
@@ -675,9 +682,6 @@ __global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T,
   const auto run = [&](auto first, auto count, auto moving) {
     constexpr int R0 = decltype(first)::value, N = decltype(count)::value;
     constexpr bool kMoving = decltype(moving)::value;
-    if (!kMoving)
-#pragma unroll
-      for (int r = R0; r < R0 + N; ++r) st[r].m = 0.0f;
     int slot = 0;
     for (int t = 0; t < n; ++t) {
       const int tile = it.b0 + t;
@@ -701,7 +705,7 @@ __global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T,
 #pragma unroll
         for (int r = 0; r < N; ++r) {
           if (kMoving) raise_reference(st[R0 + r], top_score(s[r], a.scale2), sum(R0 + r), exact);
-          weigh<T, kMoving>(st[R0 + r], s[r], a.scale2, sum(R0 + r), exact, p[r]);
+          weigh<T, kMoving>(st[R0 + r], s[r], a.scale2, fixed, sum(R0 + r), exact, p[r]);
         }
         products(true);
 #pragma unroll
@@ -718,6 +722,9 @@ __global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T,
       turn_end<(R - 2) * D::UNITS / 2>();
     }
     wait_copies();  // none may land after the workgroup's end
+    if (!kMoving)
+#pragma unroll
+      for (int r = R0; r < R0 + N; ++r) st[r].m = fixed;
   };
   using zero = std::integral_constant<int, 0>;
   using one = std::integral_constant<int, 1>;
@@ -793,7 +800,7 @@ __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void fwd_few_ke
     if (ldc(a.flags + t)) mask_scores(sc, a.bias + int64_t(t) * 32, h);
     raise_reference(st, top_score(sc, a.scale2), e, exact);
     Frag p[D::FR];
-    weigh<T, true>(st, sc, a.scale2, e, exact, p);
+    weigh<T, true>(st, sc, a.scale2, 0.0f, e, exact, p);
 #pragma unroll
     for (int d = 0; d < D::DT; ++d)
 #pragma unroll

@@ -123,3 +123,27 @@ def test_nan_queries_without_a_key(dtype, nq):
         q2 = q.clone()
         q2[rows] = bad
         assert all(torch.equal(x, y) for x, y in zip(step(q2), want))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("nq", [3, 40, 300])
+@pytest.mark.parametrize("sign,size", [(1, 2.0 ** 105), (-1, 2.0 ** 105), (1, 2.0 ** -60), (-1, 2.0 ** -60)])
+def test_values_far_from_one(dtype, nq, sign, size):
+    """Scores of +-16 (2^+-23 as weights without a reference) with values whose products
+    with such weights leave fp32: the result is a mean of the values all the same.
+
+    A score of 16 from 32 products carries at most 32 * 2^-24 * 16 = 3e-5; its weight
+    and the result twice that at most."""
+    irreps, nk = "32x0e", 200
+    attn = layers.CrossAttention(irreps, 1, dtype=dtype)
+    rng = np.random.default_rng(41)
+    base = 4.0 / np.sqrt(32)
+    q = dev(sign * base + 0.02 * rng.standard_normal((nq, 32)), dtype)
+    k = dev(base + 0.02 * rng.standard_normal((nk, 32)), dtype)
+    v = dev(size * (1 + rng.random((nk, 32))), dtype)
+    b = attn.batch(layers.Samples([0, nq]), layers.Samples([0, nk]))
+    out, lse = attn.forward(b, q, k, v, scale=1.0, need_lse=True)
+    torch.cuda.synchronize()
+    ro, rl = ol.attn_forward(irreps, 1, 1, [0, nq], [0, nk], host(q), host(k), host(v), None, 1.0)
+    assert rel_err(host(out), ro) <= (1e-4 if dtype == "f32" else TOL[dtype])
+    assert np.abs(host(lse) - rl).max() <= 1e-4
