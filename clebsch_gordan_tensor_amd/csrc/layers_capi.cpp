@@ -80,7 +80,8 @@ void need_rows(int64_t rows, const void* p, int64_t ld, int64_t dim, const char*
 
 void need_batch(const cgtp_attn_batch_s* b, double scale) {
   need(b != nullptr, "batch is NULL");
-  need(std::isfinite(scale), "scale must be finite");
+  // as the kernels hold it, times log2 e in 32 bits: 0 * inf would make NaN of scores of 0
+  need(std::isfinite(float(scale * 1.4426950408889634)), "scale must be finite in 32 bits");
   need_device(b->device, "the batch");
 }
 

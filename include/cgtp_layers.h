@@ -146,7 +146,7 @@ cgtp_status cgtp_attn_workspace_size(cgtp_attn_batch batch, int op, size_t* byte
 
 /* out [queries][dim_q] (contiguous rows) from q, k, v with row strides ldq, ldk,
  * ldv in elements (at least the row size; k and v may be slices of one row).
- * key_mask [context rows]: one byte a row, nonzero = may be attended; NULL =
+ * |scale| is at most 2e38 (else INVALID_ARG). key_mask [context rows]: one byte a row, nonzero = may be attended; NULL =
  * all. lse [queries][heads] fp32, or NULL. ws is 16-byte aligned. */
 cgtp_status cgtp_attn_forward(cgtp_attn_batch batch, const void* q, int64_t ldq, const void* k, int64_t ldk,
                               const void* v, int64_t ldv, const uint8_t* key_mask, double scale, void* out, float* lse,

@@ -147,3 +147,20 @@ def test_values_far_from_one(dtype, nq, sign, size):
     ro, rl = ol.attn_forward(irreps, 1, 1, [0, nq], [0, nk], host(q), host(k), host(v), None, 1.0)
     assert rel_err(host(out), ro) <= (1e-4 if dtype == "f32" else TOL[dtype])
     assert np.abs(host(lse) - rl).max() <= 1e-4
+
+
+def test_scale_beyond_fp32_is_refused():
+    # finite in 64 bits, infinite in the kernels' 32 (times log2 e): 0 * inf would be NaN
+    attn = layers.CrossAttention("16x0e", 2)
+    b = attn.batch(layers.Samples([0, 3]), layers.Samples([0, 5]))
+    q, k = torch.zeros((3, 16), device="cuda"), torch.ones((5, 16), device="cuda")
+    out, lse = attn.forward(b, q, k, k, scale=2e38, need_lse=True)
+    assert torch.all(out == 1)
+    ctx = attn.pack(b, k, k)
+    for scale in (1e39, -3e38, float("nan")):
+        for bad in (lambda: attn.forward(b, q, k, k, scale=scale),
+                    lambda: attn.forward_packed(b, q, ctx, scale=scale),
+                    lambda: attn.backward(b, q, k, k, out, lse, q, scale=scale)):
+            with pytest.raises(cgtp.CgtpError) as e:
+                bad()
+            assert e.value.status == 1
