@@ -184,7 +184,10 @@ cgtp_status cgtp_norm_create(const char* irreps, int64_t groups, cgtp_act act, d
     *out = nullptr;
     need_dtype(dtype);
     need(groups >= 1, "groups < 1");
-    need(eps > 0.0 && std::isfinite(eps), "eps must be positive");
+    need(eps > 0.0, "eps must be positive");
+    // in the arithmetic of the kernels: as 0 it would leave 0 * inf where a variance is 0
+    need(dtype == CGTP_F64 ? std::isnormal(eps) : std::isnormal(float(eps)),
+         "eps must be a normal number of the norm's arithmetic");
     need(act == CGTP_ACT_NONE || act == CGTP_ACT_SILU || act == CGTP_ACT_GELU, "bad activation");
     auto n = std::make_unique<cgtp_norm_s>();
     n->row = row_layout(irreps);

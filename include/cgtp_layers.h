@@ -55,7 +55,8 @@ typedef enum { CGTP_ACT_NONE = 0, CGTP_ACT_SILU = 1, CGTP_ACT_GELU = 2 } cgtp_ac
  * mul), bias [biases] one per channel of the 0e blocks. gelu is x Phi(x) with
  * the error function. fp32, bf16 (fp32 arithmetic) and fp64.
  * Errors: PARSE; UNSUPPORTED (groups does not divide a multiplicity, a degree
- * above CGTP_LMAX); INVALID_ARG (groups < 1, eps <= 0, bad enum). */
+ * above CGTP_LMAX); INVALID_ARG (groups < 1, eps not positive or no normal number
+ * of the arithmetic, bad enum). */
 cgtp_status cgtp_norm_create(const char* irreps, int64_t groups, cgtp_act act, double eps, cgtp_dtype dtype,
                              cgtp_norm* out);
 cgtp_status cgtp_norm_destroy(cgtp_norm norm);

@@ -36,3 +36,14 @@ def test_statistics_of_empty_samples_are_not_used(irreps, lens, dtype):
         assert_close(host(y), ol.norm_forward(*args), block_cols(irreps), dtype, "y")
         assert_close(host(gx), ref[0], block_cols(irreps), dtype, "grad_x")
         assert rel_err(host(gw), ref[1]) <= TOL[dtype] and rel_err(host(gb), ref[2]) <= TOL[dtype]
+
+
+@pytest.mark.parametrize("dtype,eps", [("f32", 1.2e-38), ("bf16", 1.2e-38), ("f64", 2.3e-308)])
+def test_smallest_eps_leaves_constant_groups_finite(dtype, eps):
+    norm, sm = layers.GroupNorm("8x0e+8x1o", 2, activation="silu", eps=eps, dtype=dtype), layers.Samples([0, 4])
+    x = torch.zeros((4, norm.dim), dtype=norm.torch_dtype, device="cuda")
+    x[:, :8] = 3
+    y, stats = norm.forward(sm, x)
+    gx = norm.backward(sm, x, None, None, stats, torch.zeros_like(x), need=(True, False, False))[0]
+    torch.cuda.synchronize()
+    assert torch.all(y == 0) and torch.all(gx == 0)
