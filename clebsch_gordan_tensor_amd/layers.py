@@ -8,6 +8,7 @@ in the HIP kernels of libcgtp.so.
 """
 
 import ctypes
+import weakref
 
 import numpy as np
 
@@ -144,18 +145,20 @@ class GroupNorm(_Handle):
         _check(_lib.cgtp_norm_query(h, *[ctypes.byref(a) for a in v]), "cgtp_norm_query")
         self.dim, self.channels, self.biases, self.num_groups = (a.value for a in v)
         self._acc = _acc_dtype(self.dtype_code)
-        self._sized, self._sizes = None, None
+        self._sized = None
 
     def workspace_size(self, samples, backward=False):
-        # sizes of the layout last used: layouts repeat from call to call
-        if self._sized is not samples:
+        # (layout last used, its two sizes): layouts repeat from call to call. One value,
+        # read once: another thread may put its own there meanwhile
+        sized = self._sized
+        if sized is None or sized[0]() is not samples:
             n, sizes = _size(), []
             for k in range(2):
                 _check(_lib.cgtp_norm_workspace_size(self._h, samples._h, k, ctypes.byref(n)),
                        "cgtp_norm_workspace_size")
                 sizes.append(n.value)
-            self._sized, self._sizes = samples, sizes
-        return self._sizes[1 if backward else 0]
+            sized = self._sized = weakref.ref(samples), sizes
+        return sized[1][1 if backward else 0]
 
     def _affine(self, weight, bias):
         dt = self.torch_dtype
