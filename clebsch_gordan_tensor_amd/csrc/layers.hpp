@@ -41,6 +41,9 @@ class DevMem {
   int device_ = 0;
 };
 
+// Most workgroups of 256 threads in one launch, whose threads are counted in 32 bits.
+constexpr int64_t kMaxWorkgroups = (int64_t(1) << 24) - 1;
+
 int current_device();
 void need_device(int device, const char* what);
 

@@ -371,14 +371,15 @@ __global__ __launch_bounds__(kNT) void norm_apply_kernel(const RowChunk* chunks,
 // A whole sample's strip by one workgroup, where samples are short: statistics,
 // then y; the second read of x comes from the caches.
 template <typename T, int VEC>
-__global__ __launch_bounds__(kNTS) void norm_sample_kernel(const int32_t* first_row, const NormStrip* strips, Order ord,
-                                                          const T* x, T* y, int64_t dim, int num_groups, const T* w, const T* b,
+__global__ __launch_bounds__(kNTS) void norm_sample_kernel(const int32_t* first_row, const NormStrip* strips,
+                                                          int sample_first, Order ord, const T* x, T* y, int64_t dim,
+                                                          int num_groups, const T* w, const T* b,
                                                           typename AccOf<T>::type* stats,
                                                           typename AccOf<T>::type eps, int act) {
   using A = typename AccOf<T>::type;
   __shared__ Moments<A> sh[kNTS];
   __shared__ A mean[kNTS], rstd[kNTS];
-  const int s = ord.unit(), r0 = first_row[s], r1 = first_row[s + 1];
+  const int s = sample_first + ord.unit(), r0 = first_row[s], r1 = first_row[s + 1];
   if (r0 == r1) return;
   const NormStrip st = ldc(strips + ord.strip());
   const Place p = place<VEC, kNTS>(st);
@@ -645,14 +646,15 @@ __global__ __launch_bounds__(kNT) void norm_grad_kernel(const RowChunk* chunks, 
 // A whole sample's strip by one workgroup: its channels' sums, then grad_x.
 template <typename T, int VEC>
 __global__ __launch_bounds__(kNTS) void norm_sample_grad_kernel(const int32_t* first_row, const NormStrip* strips,
-                                                               Order ord, const T* x, const T* g, T* gx, int64_t dim,
-                                                               int num_groups, int channels, const T* w, const T* b,
+                                                               int sample_first, Order ord, const T* x, const T* g,
+                                                               T* gx, int64_t dim, int num_groups, int channels,
+                                                               const T* w, const T* b,
                                                                const typename AccOf<T>::type* stats, int act,
                                                                typename AccOf<T>::type* sums) {
   using A = typename AccOf<T>::type;
   __shared__ A sh[kNTS][2 * VEC + 1];
   __shared__ A sha[kNTS], shb[kNTS], ma[kNTS], mb[kNTS];
-  const int s = ord.unit(), r0 = first_row[s], r1 = first_row[s + 1];
+  const int s = sample_first + ord.unit(), r0 = first_row[s], r1 = first_row[s + 1];
   const NormStrip st = ldc(strips + ord.strip());
   const Place p = place<VEC, kNTS>(st);
   const A* ss = stats + (int64_t(s) * num_groups + st.gid) * 2;
@@ -671,8 +673,9 @@ __global__ __launch_bounds__(kNTS) void norm_sample_grad_kernel(const int32_t* f
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+// (at most kMaxWorkgroups: see slices; a single sample has at most 512 runs, and a
+// norm some 6000 strips of 256 lanes)
 Order strip_order(int64_t units, int nstrip) {
-  if (units * nstrip > INT32_MAX) throw Error{CGTP_ERR_UNSUPPORTED, "norm: too many samples for one launch"};
   return {int(units), nstrip, units * nstrip <= 1280};  // 5 workgroups a compute unit
 }
 dim3 strip_grid(const Order& o) { return dim3(unsigned(o.units * o.strips)); }
@@ -708,16 +711,27 @@ bool by_sample(const cgtp_norm_s* n, const cgtp_samples_s* sm) {
 // 270 us, all at once 315 us).
 constexpr int64_t kSliceBytes = int64_t(160) << 20;
 
-// f(first sample, end sample) for each slice.
+// f(first sample, end sample) for each slice; one launch takes a slice's runs of
+// every strip, or its samples.
 template <typename F>
-void slices(const cgtp_samples_s* sm, int64_t row_bytes, F&& f) {
-  const int64_t rows = std::max<int64_t>(1, kSliceBytes / row_bytes);
+void slices(const cgtp_samples_s* sm, int64_t row_bytes, int nstrip, F&& f) {
+  const int64_t rows = std::max<int64_t>(1, kSliceBytes / row_bytes), most = kMaxWorkgroups / nstrip;
+  const auto runs = [&](int64_t s) { return int64_t(sm->sample_chunk[size_t(s)]); };
   for (int64_t s = 0; s < sm->S;) {
     int64_t e = s + 1;
-    while (e < sm->S && sm->ptr[size_t(e) + 1] - sm->ptr[size_t(s)] <= rows) ++e;
+    while (e < sm->S && sm->ptr[size_t(e) + 1] - sm->ptr[size_t(s)] <= rows && runs(e + 1) - runs(s) <= most &&
+           e + 1 - s <= kMaxWorkgroups)
+      ++e;
     f(s, e);
     s = e;
   }
+}
+
+// f(first sample, end sample) for the launches that take whole samples.
+template <typename F>
+void sample_launches(int64_t S, int nstrip, F&& f) {
+  const int64_t most = kMaxWorkgroups / nstrip;
+  for (int64_t s = 0; s < S; s += most) f(s, std::min(s + most, S));
 }
 
 template <typename T>
@@ -736,14 +750,16 @@ void forward_typed(const cgtp_norm_s* n, const cgtp_samples_s* sm, const void* x
   const int groups = int(n->num_groups);
   with_vec<T>(v ? n->vec : 1, [&](auto V) {
     if (one) {
-      const Order order = strip_order(sm->S, nstrip);
-      hipLaunchKernelGGL((norm_sample_kernel<T, V.value>), strip_grid(order), dim3(kNTS), 0, s,
-                         sm->first_row.as<int32_t>(), strips, order, tx, ty, n->row.dim, groups, tw, tb,
-                         static_cast<A*>(stats), A(n->eps), int(n->act));
-      CGTP_CHECK_HIP(hipGetLastError());
+      sample_launches(sm->S, nstrip, [&](int64_t s0, int64_t s1) {
+        const Order order = strip_order(s1 - s0, nstrip);
+        hipLaunchKernelGGL((norm_sample_kernel<T, V.value>), strip_grid(order), dim3(kNTS), 0, s,
+                           sm->first_row.as<int32_t>(), strips, int(s0), order, tx, ty, n->row.dim, groups, tw, tb,
+                           static_cast<A*>(stats), A(n->eps), int(n->act));
+        CGTP_CHECK_HIP(hipGetLastError());
+      });
       return;
     }
-    slices(sm, n->row.dim * int64_t(sizeof(T)), [&](int64_t s0, int64_t s1) {
+    slices(sm, n->row.dim * int64_t(sizeof(T)), nstrip, [&](int64_t s0, int64_t s1) {
       const int c0 = sm->sample_chunk[size_t(s0)], c1 = sm->sample_chunk[size_t(s1)];
       if (c0 == c1) return;  // empty samples
       const Order order = strip_order(c1 - c0, nstrip);
@@ -780,14 +796,16 @@ void backward_typed(const cgtp_norm_s* n, const cgtp_samples_s* sm, const void* 
   A* part = sums + 2 * size_t(C) * size_t(sm->S);
   with_vec<T>(v ? n->vec : 1, [&](auto V) {
     if (one) {
-      const Order order = strip_order(sm->S, nstrip);
-      hipLaunchKernelGGL((norm_sample_grad_kernel<T, V.value>), strip_grid(order), dim3(kNTS), 0, s,
-                         sm->first_row.as<int32_t>(), strips, order, tx, tg, static_cast<T*>(gx), n->row.dim, groups, C, tw,
-                         tb, st, int(n->act), sums);
-      CGTP_CHECK_HIP(hipGetLastError());
+      sample_launches(sm->S, nstrip, [&](int64_t s0, int64_t s1) {
+        const Order order = strip_order(s1 - s0, nstrip);
+        hipLaunchKernelGGL((norm_sample_grad_kernel<T, V.value>), strip_grid(order), dim3(kNTS), 0, s,
+                           sm->first_row.as<int32_t>(), strips, int(s0), order, tx, tg, static_cast<T*>(gx),
+                           n->row.dim, groups, C, tw, tb, st, int(n->act), sums);
+        CGTP_CHECK_HIP(hipGetLastError());
+      });
       return;
     }
-    slices(sm, 2 * n->row.dim * int64_t(sizeof(T)), [&](int64_t s0, int64_t s1) {
+    slices(sm, 2 * n->row.dim * int64_t(sizeof(T)), nstrip, [&](int64_t s0, int64_t s1) {
       const int c0 = sm->sample_chunk[size_t(s0)], c1 = sm->sample_chunk[size_t(s1)];
       const Order order = strip_order(c1 - c0, nstrip);
       const dim3 grid = strip_grid(order);

@@ -47,3 +47,76 @@ def test_smallest_eps_leaves_constant_groups_finite(dtype, eps):
     gx = norm.backward(sm, x, None, None, stats, torch.zeros_like(x), need=(True, False, False))[0]
     torch.cuda.synchronize()
     assert torch.all(y == 0) and torch.all(gx == 0)
+
+
+def test_more_workgroups_than_one_launch_holds():
+    """1.1 million samples of one row (every 1000th empty) and 16 blocks: more than 2^24
+    sample-strips, where a launch of 256 threads a workgroup ends. Against the formula
+    in torch's 64 bits, block by block.
+
+    x is at most 6 and a group of eight has a deviation of 1/15 at least, so its mean's
+    three roundings are 15 * 3 * 2^-24 * 6 = 2e-5 of y and 1e-3 of grad_x at most, 1e-5 and
+    1e-4 of the largest; a parameter's sum adds 16 rows of 7 * 10^4 terms in sequence,
+    each rounded to 2^-24 of a partial sum."""
+    S, blocks = 1_100_000, 8
+    irreps = "+".join(["8x0e+8x1o"] * blocks)
+    lens = np.ones(S, np.int64)
+    lens[::1000] = 0
+    sm, norm = layers.Samples(ptr_of(lens)), layers.GroupNorm(irreps, 1, activation="none", eps=EPS)
+    rows = int(lens.sum())
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    x, g = (torch.randn((rows, norm.dim), generator=gen, device="cuda") for _ in range(2))
+    w = torch.linspace(0.5, 1.5, norm.channels, device="cuda")
+    b = torch.linspace(-1, 1, norm.biases, device="cuda")
+    y, stats = norm.forward(sm, x, w, b)
+    gx, gw, gb = norm.backward(sm, x, w, b, stats, g)
+    for i in range(2 * blocks):
+        m, even = (1, True) if i % 2 == 0 else (3, False)
+        off = i // 2 * 32 + (0 if even else 8)
+        cols = slice(off, off + 8 * m)
+        xb, gb_ = (t[:, cols].double().view(rows, m, 8) for t in (x, g))
+        wi = w[8 * i:8 * i + 8].double()
+        xc = xb - xb.mean((1, 2), keepdim=True) if even else xb
+        r = (xc.square().mean((1, 2), keepdim=True) + EPS) ** -0.5
+        xh, gh = xc * r, gb_ * wi
+        want = xh * wi
+        d = gh - xh * (gh * xh).mean((1, 2), keepdim=True)
+        if even:
+            want = want + b[4 * i:4 * i + 8].double()
+            d = d - gh.mean((1, 2), keepdim=True)
+            sums = gb_.sum((0, 1))
+            assert (gb[4 * i:4 * i + 8].double() - sums).abs().max() <= 1e-5 * gb_.abs().sum((0, 1)).max()
+        assert (y[:, cols].double().view(rows, m, 8) - want).abs().max() <= 1e-5 * want.abs().max()
+        want = d * r
+        assert (gx[:, cols].double().view(rows, m, 8) - want).abs().max() <= 1e-4 * want.abs().max()
+        sums = (gb_ * xh).sum((0, 1))
+        assert (gw[8 * i:8 * i + 8].double() - sums).abs().max() <= 1e-5 * (gb_ * xh).abs().sum((0, 1)).max()
+
+
+def test_more_runs_than_one_launch_holds():
+    """17 million samples of one row and one of 70,000 rows, a row holding one element: more
+    than 2^24 runs in one slice. A lone odd scalar gives y = x w / sqrt(x^2 + eps)
+    and grad_x = g w eps / (x^2 + eps)^(3/2): the difference of two terms g w / sqrt(x^2 + eps),
+    each of some eight roundings of 2^-24."""
+    S = 17_000_001
+    lens = np.ones(S, np.int64)
+    lens[S // 2] = 70_000
+    sm, norm = layers.Samples(ptr_of(lens)), layers.GroupNorm("1x0o", 1, eps=EPS)
+    assert norm.workspace_size(sm) > 0
+    rows = int(lens.sum())
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    x, g = (torch.randn((rows, 1), generator=gen, device="cuda") for _ in range(2))
+    w = torch.full((1,), 1.25, device="cuda")
+    y, stats = norm.forward(sm, x, w)
+    gx, gw, _ = norm.backward(sm, x, w, None, stats, g, need=(True, True, False))
+    xd, gd = x.double(), 1.25 * g.double()
+    var, lo, hi = xd * xd, S // 2, S // 2 + 70_000
+    var[lo:hi] = var[lo:hi].mean()
+    r = (var + EPS) ** -0.5
+    xh = xd * r
+    along = gd * xh
+    along[lo:hi] = along[lo:hi].mean()
+    assert ((y - 1.25 * xh).abs() <= 1e-6 * (1.25 * xh).abs()).all()
+    assert ((gx - (gd - xh * along) * r).abs() <= 2e-6 * (gd.abs() + (xh * along).abs()) * r).all()
+    total = (g * xh).sum()
+    assert abs(gw.double().item() - total.item()) <= 1e-5 * (g * xh).abs().sum().item()
