@@ -114,6 +114,12 @@ int64_t part_cost(const std::vector<Unit>& u, int groups, int slots, int min_len
   return best;
 }
 
+// One launch takes all workgroups of a kernel.
+void need_launch(int64_t workgroups) {
+  if (workgroups > kMaxWorkgroups)
+    throw Error{CGTP_ERR_UNSUPPORTED, "attention: more tiles x context heads than one launch takes"};
+}
+
 // Splits long units (of at most `stride` tiles) and lays the items out for the
 // device. `slots` is the number of workgroups that the device works on at once.
 // Order: workgroups go to the 8 dies in turn, and each die has its own L2, so
@@ -122,6 +128,9 @@ int64_t part_cost(const std::vector<Unit>& u, int groups, int slots, int min_len
 // first, so that the short ones fill the end; a group bigger than a die's share
 // goes round several.
 void build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, int slots, int min_len) {
+  int64_t whole = 0;
+  for (const Unit& x : u) whole += int64_t(x.kinds.size()) * groups;
+  need_launch(whole);  // (before the lists are laid out)
   const int64_t cost = part_cost(u, groups, slots, min_len);
   struct Group {
     int64_t work = 0, longest = 0;
@@ -190,7 +199,7 @@ void build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, int 
       items.push_back(k < queue[size_t(x)].size() ? queue[size_t(x)][k] : Item{0, 0, 0, 0, 0, -1, stride, 0});
   // trailing empty places of the last turn
   while (!items.empty() && items.back().tiles == 0) items.pop_back();
-  if (items.size() > size_t(INT32_MAX)) throw Error{CGTP_ERR_UNSUPPORTED, "attention: too many work items"};
+  need_launch(int64_t(items.size()));
   w.items = int(items.size());
   w.item_mem.upload(items.data(), items.size() * sizeof(Item));
   for (int k = 0; k < 2; ++k) {
@@ -321,6 +330,7 @@ cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, co
   const Side qs = cut(q->ptr, at->G), ks = cut(k->ptr, 1);
   b->qtiles = int64_t(qs.tiles.size());
   b->ktiles = int64_t(ks.tiles.size());
+  need_launch((std::max(b->qtiles, b->ktiles) + 7) / 8 * 8 * at->kv_heads);  // of the packing
   b->qtile_mem.upload(qs.tiles.data(), qs.tiles.size() * sizeof(Tile));
   b->ktile_mem.upload(ks.tiles.data(), ks.tiles.size() * sizeof(Tile));
   const int g = at->kv_heads;

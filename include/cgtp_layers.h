@@ -133,7 +133,8 @@ cgtp_status cgtp_attn_query(cgtp_attn attn, int64_t* dim_q, int64_t* dim_kv, int
  * which workgroup takes which rows, and where a long context or a long run of
  * queries is split and joined. Keeps copies: attn must outlive it, the samples
  * need not. Host work and a synchronous upload; reusable for every call on
- * these layouts. Errors: INVALID_ARG, UNSUPPORTED (rows x heads beyond 2^31). */
+ * these layouts. Errors: INVALID_ARG, UNSUPPORTED (rows x heads beyond 2^31, or
+ * tiles of 32 rows x kv_heads beyond 2^24; a sample of any rows has its own tiles). */
 cgtp_status cgtp_attn_batch_create(cgtp_attn attn, cgtp_samples queries, cgtp_samples context, cgtp_attn_batch* out);
 cgtp_status cgtp_attn_batch_destroy(cgtp_attn_batch batch);
 

@@ -164,3 +164,12 @@ def test_scale_beyond_fp32_is_refused():
             with pytest.raises(cgtp.CgtpError) as e:
                 bad()
             assert e.value.status == 1
+
+
+def test_more_tiles_than_one_launch_takes_are_refused():
+    attn = layers.CrossAttention("256x0e", 256, dtype="bf16")
+    one, many = (layers.Samples(np.arange(n + 1)) for n in (1000, 65_600))       # 256 tiles a sample of one row
+    attn.batch(one, one)
+    with pytest.raises(cgtp.CgtpError) as e:
+        attn.batch(many, many)
+    assert e.value.status == 3
