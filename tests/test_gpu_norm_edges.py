@@ -120,3 +120,106 @@ def test_more_runs_than_one_launch_holds():
     assert ((gx - (gd - xh * along) * r).abs() <= 2e-6 * (gd.abs() + (xh * along).abs()) * r).all()
     total = (g * xh).sum()
     assert abs(gw.double().item() - total.item()) <= 1e-5 * (g * xh).abs().sum().item()
+
+
+# (irreps, groups, activation, lengths): the longest sample's part of a narrow strip exceeds 256 KB in every type
+RUNS = [
+    ("32x0e+32x1o", 4, "silu", [2800, 3]),
+    ("35x0e+21x1o+7x2e", 7, "gelu", [0, 4700, 0, 5, 5100, 0]),           # single-channel lanes in fp32 and bf16
+    ("16x0e+8x0o+8x3o+8x4e", 4, "gelu", [40, 5000]),                     # 7 and 9 components
+    ("1200x0e+300x1o", 1, "none", [150, 0, 400]),                        # groups wider than 256 lanes
+    ("8x0e", 2, "silu", [0, 17000, 1]),                                  # more rows than one span of 4096
+    ("64x0e+24x0o+8x1e", 2, "silu", [2500, 2500, 1, 900]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f64"])
+@pytest.mark.parametrize("irreps,groups,act,lens", RUNS)
+def test_runs_of_rows(irreps, groups, act, lens, dtype):
+    norm = layers.GroupNorm(irreps, groups, activation=act, eps=EPS, dtype=dtype)
+    assert norm.workspace_size(layers.Samples(ptr_of(lens))) > 0
+    x, w, b, g = inputs(irreps, lens, dtype)
+    a = check(irreps, groups, act, lens, dtype, x, w, b, g, norm)
+    # statistics of empty samples are not written
+    again = check(irreps, groups, act, lens, dtype, x, w, b, g, norm)
+    assert all(torch.equal(u, v) for u, v in zip(a[:1] + a[2:], again[:1] + again[2:]))
+
+    def shifted(t):
+        return torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape).copy_(t)
+
+    check(irreps, groups, act, lens, dtype, shifted(x), shifted(w), shifted(b), shifted(g), norm)
+
+
+def test_runs_in_a_graph():
+    irreps, lens = "32x0e+32x1o+32x2e", [0, 2800, 9]
+    x, w, b, g = inputs(irreps, lens, "f32")
+    sm, norm = layers.Samples(ptr_of(lens)), layers.GroupNorm(irreps, 4, activation="silu")
+    assert norm.workspace_size(sm) > 0
+
+    def step(x):
+        y, stats = norm.forward(sm, x, w, b)
+        return (y,) + norm.backward(sm, x, w, b, stats, g)
+
+    step(x)
+    torch.cuda.synchronize()
+    graph, xs = torch.cuda.CUDAGraph(), x.clone()
+    with torch.cuda.graph(graph):
+        res = step(xs)
+    for k in range(3):
+        xs.copy_(x * (k + 1) + k)
+        graph.replay()
+        want = step(xs)
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(res, want))
+
+
+def test_more_rows_than_one_slice():
+    """430 MB of rows, worked off in slices of at most 160 MB (forward) and 80 MB
+    (backward, two tensors): picked samples and the weights' gradients against the
+    oracle's formulas in torch's 64 bits."""
+    irreps, groups, lens = "128x0e+128x1o", 8, [9000, 0, 70000, 1, 60000, 64000, 0, 7000]
+    ptr = ptr_of(lens)
+    norm, sm = layers.GroupNorm(irreps, groups, activation="silu", eps=EPS), layers.Samples(ptr)
+    assert norm.workspace_size(sm) > 0
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x, g = (torch.randn((int(ptr[-1]), norm.dim), generator=gen, device="cuda") for _ in range(2))
+    w = torch.linspace(0.5, 1.5, norm.channels, device="cuda")
+    b = torch.linspace(-1, 1, norm.biases, device="cuda")
+    y, stats = norm.forward(sm, x, w, b)
+    gx, gw, gb = norm.backward(sm, x, w, b, stats, g)
+    rw, rb = (torch.zeros(n, dtype=torch.float64, device="cuda") for n in (norm.channels, norm.biases))
+    for lo, hi in zip(ptr[:-1], ptr[1:]):
+        if lo == hi:
+            continue
+        for m, off, ch in ((1, 0, 0), (3, 128, 128)):
+            cols = slice(off, off + 128 * m)
+            xb, gy = (t[lo:hi, cols].double().view(-1, m, groups, 16) for t in (x, g))
+            xc = xb - xb.mean((0, 1, 3), keepdim=True) if m == 1 else xb
+            r = (xc.square().mean((0, 1, 3), keepdim=True) + EPS) ** -0.5
+            xh, wb = xc * r, w[ch:ch + 128].double().view(groups, 16)
+            z, gz = xh * wb, gy
+            if m == 1:
+                z = z + b.double().view(groups, 16)
+                s = torch.sigmoid(z)
+                z, gz = z * s, gy * (s + z * s * (1 - s))
+                rb += gz.sum((0, 1)).view(-1)
+            rw[ch:ch + 128] += (gz * xh).sum((0, 1)).view(-1)
+            gh = gz * wb
+            d = gh - xh * (gh * xh).mean((0, 1, 3), keepdim=True)
+            if m == 1:
+                d = d - gh.mean((0, 1, 3), keepdim=True)
+            for got, want in ((y, z), (gx, d * r)):
+                want = want.reshape(-1, 128 * m)
+                assert (got[lo:hi, cols] - want).abs().max() <= TOL["f32"] * want.abs().max()
+    assert (gw - rw).abs().max() <= TOL["f32"] * rw.abs().max()
+    assert (gb - rb).abs().max() <= TOL["f32"] * rb.abs().max()
+
+
+@pytest.mark.parametrize("irreps,act,lens,runs", [("2x0e+1x1o", "silu", [9000, 3], False),     # one workgroup a sample
+                                                  ("2x0e+1x1e", "none", [2_200_000, 5], True)])
+def test_more_rows_than_one_span(irreps, act, lens, runs):
+    """A workgroup walks 4096 rows at a time; narrow rows give it more (a run is a 512th of its sample)."""
+    norm = layers.GroupNorm(irreps, 1, activation=act, eps=EPS)
+    assert (norm.workspace_size(layers.Samples(ptr_of(lens))) > 0) == runs
+    x, w, b, g = inputs(irreps, lens, "f32")
+    check(irreps, 1, act, lens, "f32", x, w, b, g, norm)
