@@ -618,11 +618,12 @@ constexpr float kBound = 40.0f;
 // which with the copies into it take 1.5 times as long as the products else. Two
 // paths: scores bounded beforehand by the rows' norms (what normalised features
 // give) go without maximum, branch and rescaling; others keep a running maximum
-// (for RT = 2 one 32-row half after the other; long contexts, head of 128: 1083 us
-// bounded, 1277 us with it).
-// Measured: 4 x 4096 queries against 8191 keys, 16 heads of 128, bf16: 945 us =
-// 1160 TFLOP/s with matrix cores busy 55 % of the cycles; a ragged batch of heads of
-// 144 (RT = 1): 140 us, 32 %; fp32, heads of 128: 66 %.
+// (for RT = 2 one 32-row half after the other; long contexts, head of 128: 1068 us
+// bounded, 1257 us with it).
+// Measured: 4 x 4096 queries against 8191 keys, 16 heads of 128, bf16: 934 us =
+// 1177 TFLOP/s (994 us over the first 50 passes of an idle card) with matrix cores busy
+// 56 % of the cycles; a ragged batch of heads of 144 (RT = 1): 144 us, 30 %; fp32, heads of
+// 128: 66 %.
 template <typename T, int DP, int RT>
 __global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T, DP>::UNITS)) void fwd_kernel(
     FwdArgs a) {
@@ -750,7 +751,7 @@ __global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T,
 // At most 32 query rows against a long context (single tokens): the four waves
 // take every fourth key tile, read straight into registers, and join. Bound: the
 // keys' and values' bytes: 64 tokens against 1000 - 8000 keys each, heads of 128,
-// bf16: 112 us = 5.4 TB/s.
+// bf16: 114 us = 5.4 TB/s.
 template <typename T, int DP>
 __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void fwd_few_kernel(FwdArgs a) {
   using D = Dims<T, DP>;
@@ -1122,8 +1123,8 @@ __device__ __forceinline__ void dkv_item(const BwdArgs& a, const Item& it, u32x4
 // All gradients in one launch: the items of the three kinds fill the device
 // together and end together (a ragged batch's three launches each left a quarter
 // of it idle at their end). Bound: matrix cores, exponentials and operand reads
-// from shared memory (1 KB a product and wave) after one another: 445 us for a
-// ragged bf16 batch of heads of 144, matrix cores busy 38 %; fp32, heads of 128, 166 us,
+// from shared memory (1 KB a product and wave) after one another: 448 us for a
+// ragged bf16 batch of heads of 144, matrix cores busy 38 %; fp32, heads of 128, 165 us,
 // 73 %. Workgroups of 8 waves copy half as much and were no faster (644 us against
 // 641 us for the whole step), nor were wave priorities.
 template <typename T, int DP>

@@ -16,7 +16,7 @@
 // sums free of cancellation, and means and squares are merged pairwise in a
 // fixed tree. All sums are in fp32 (fp64 for fp64 storage).
 //
-// Measured, fp32, 24,000 rows of 1152: statistics 19 us (5.9 TB/s), y 44 us (5.0),
+// Measured, fp32, 24,000 rows of 1152: statistics 19 us (5.9 TB/s), y 45 us (4.9),
 // backward's sums 35 us (6.4), grad_x 51 us (6.5); bf16, 96 samples of 20 - 220 rows in
 // one launch forward and two backward: 20 us and 31 + 4 us.
 #include <algorithm>
@@ -696,9 +696,13 @@ void with_vec(int vec, F&& f) {
   else f(std::integral_constant<int, 1>{});
 }
 
-// Short samples (at most this many bytes of a block in a sample): one workgroup
-// a sample and narrow strip, one launch forward and two backward (96 samples of
-// 20 - 220 rows 53 us, as runs 70 us; 8 molecules forward 8.9 us and 12.7 us).
+// Short samples (at most this many bytes of a narrow strip in a sample): one
+// workgroup a sample and strip, one launch forward and two backward (96 samples of
+// 20 - 220 rows 53 us, as runs 70 us; 8 molecules forward 8.9 us and 12.7 us). On
+// both sides of the limit, bf16 rows of 1152, forward + backward in one graph, so /
+// as runs: 32 samples of 128 KB 11 + 25 / 15 + 27 us, of 256 KB 18 + 34 / 21 + 43 us, of
+// 512 KB 33 + 54 / 38 + 68 us; but 4 samples, which leave most of the device idle, of
+// 128 KB 11 + 21 / 11 + 18 us, of 256 KB 14 + 27 / 11 + 18 us, of 1 MB 37 + 79 / 15 + 26 us.
 constexpr int64_t kSampleBytes = 256 << 10;
 
 bool by_sample(const cgtp_norm_s* n, const cgtp_samples_s* sm) {
