@@ -302,6 +302,8 @@ class CrossAttention(_Handle):
             raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (rows, dim)))
         if t.dtype != self.torch_dtype:
             raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, self.torch_dtype))
+        if t.numel() == 0:
+            return t.data_ptr(), dim                                      # (its strides mean nothing)
         step, unit = t.stride()
         ld = step if rows > 1 else dim
         if (dim > 1 and unit != 1) or ld < dim:

@@ -173,3 +173,13 @@ def test_more_tiles_than_one_launch_takes_are_refused():
     with pytest.raises(cgtp.CgtpError) as e:
         attn.batch(many, many)
     assert e.value.status == 3
+
+
+def test_strides_of_tensors_without_elements_are_not_judged():
+    attn = layers.CrossAttention("16x0e+8x1o", 4)
+    b = attn.batch(layers.Samples([0, 0]), layers.Samples([0, 0]))
+    none = torch.empty((0, attn.dim_q), device="cuda").as_strided((0, attn.dim_q), (0, 0))   # as NumPy's come
+    out, lse = attn.forward(b, none, none, none, need_lse=True)
+    grads = attn.backward(b, none, none, none, out, lse, none)
+    assert all(t.shape == none.shape for t in (out, *grads))
+    attn.forward_packed(b, none, attn.pack(b, none, none))
