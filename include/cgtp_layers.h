@@ -116,8 +116,8 @@ cgtp_status cgtp_dropout_backward(cgtp_dropout drop, int64_t B, const void* grad
  *   out_i = sum_j p_ij v_j,  lse_i = log sum_j exp s_ij
  * The products run over whole irreps, so s is invariant and out equivariant.
  * A query without any key gives out = 0, lse = -inf and zero gradients, and
- * masked keys' rows are never used (they may hold infinities or NaN; their
- * gradients are 0). fp32 (fp32 matrix cores) and bf16 (products of bf16 values
+ * masked keys' rows are never used (both may hold infinities or NaN; masked
+ * keys' gradients are 0). fp32 (fp32 matrix cores) and bf16 (products of bf16 values
  * summed in fp32; softmax weights and the score gradients are rounded to bf16
  * as matrix operands, and the weights are normalised by the sum of what they
  * were rounded to, so a row that sees one key gets exactly its value). D <= 256.
@@ -168,6 +168,7 @@ cgtp_status cgtp_attn_forward_packed(cgtp_attn_batch batch, const void* q, int64
  *   grad_v = P^T grad_out,  dS = P (grad_out v^T - rowsum(grad_out out)),
  *   grad_q = scale dS k,    grad_k = scale dS^T q,
  * grad_k and grad_v summed over the query heads that share a context head.
+ * (out as stored: in bf16 its rounding is in grad_q and grad_k, most with few keys.)
  * Gradients are contiguous rows. The summation orders are fixed. */
 cgtp_status cgtp_attn_backward(cgtp_attn_batch batch, const void* q, int64_t ldq, const void* k, int64_t ldk,
                                const void* v, int64_t ldv, const uint8_t* key_mask, double scale, const void* out,
