@@ -28,6 +28,15 @@ struct alignas(16) Join {
   int32_t stride, within, pad0, pad1;
 };
 
+// What the queries of a tile see of their sample's context. Key tiles are numbered
+// through the packed context: first those of the rows that all samples share, then
+// every sample's own. Work lists count the key tiles of a sample's queries on from 0:
+// tile t stands for t + (t < shared ? 0 : skip). In a causal batch query token i sees
+// the places (32 * tile + row within) of its own keys below i + shift.
+struct Reach {
+  int32_t skip, shift;
+};
+
 struct PackTensor {
   const void* src;
   int64_t ld;
@@ -80,6 +89,37 @@ struct FwdArgs {
   uint32_t q_sign;  // flips the queries' signs where the scale is negative
   int G, heads, groups;
   bool q_vec, out_quad;
+  const Reach* reach;  // of every query tile (sequence kernels only, as the next two)
+  int shared;          // key tiles of shared rows
+  bool causal;
+};
+
+// Joins the results of rows against their own context (`own`: the parts of its joins)
+// with those against rows that all samples share (parts of tiles of 32 consecutive
+// rows whatever their sample: unit u = per tiles, parts of unit u and context head hk
+// from slot (hk * units + u) * parts on).
+struct RowsJoinArgs {
+  FwdArgs own;
+  const float* part;  // of the shared rows, with their references and sums
+  const float4* part_ml;
+  int units, per, parts;     // parts = 0: nothing is shared
+  const int32_t* lengths;    // or NULL: a token whose length is not below `capacity` sees nothing
+  int capacity;
+};
+
+// One token a slot on caches of rows [slot][capacity][dim].
+struct StepArgs {
+  FwdArgs f;
+  const void *k_new, *v_new;
+  int64_t ldk, ldv;
+  void *k_cache, *v_cache;
+  const int32_t* lengths;
+  int64_t dim;
+  int slots, capacity, size;  // size: elements of a head
+  int splits, waves_a_head, heads_a_group, bundles, tiles_a_slot;  // how the work is cut (StepPlan)
+  int min_tiles;
+  bool whole;  // a slot's tile and head is one part, and nothing is shared: rows are final
+  bool vec;
 };
 
 // Packed forms of the gradients: row or column fragments of K, V, Q and grad_out, in
@@ -103,6 +143,9 @@ struct BwdArgs {
     return static_cast<const T*>(qforms_) + form * qstride;
   }
   const float *bias, *rows;
+  const Reach* reach;  // as in FwdArgs
+  int shared;
+  bool causal;
   void *dq, *dk, *dv;
   float *part_q, *part_k, *part_v;
   int64_t ldq, ldk;
@@ -123,6 +166,17 @@ struct KernelTable {
 KernelTable kernels_f32(int dp);
 KernelTable kernels_bf16(int dp);
 
+// Kernels of batches with shared rows or causal queries, and of steps on a cache;
+// inst/attn_seq_*.hip.
+struct SeqTable {
+  void (*fwd)(const FwdArgs&, int items, int tiles, hipStream_t);
+  void (*bwd)(const BwdArgs&, int items, hipStream_t);
+  void (*step)(const StepArgs&, hipStream_t);
+  void (*rows_join)(const RowsJoinArgs&, int joins, hipStream_t);
+};
+SeqTable seq_kernels_f32(int dp);
+SeqTable seq_kernels_bf16(int dp);
+
 // Whether the forward has a form of 64 query rows a wave (8 tiles an item): its
 // operands and accumulators fit the registers.
 constexpr bool wide_forward(int dp, size_t size) { return size == 2 && dp <= 128; }
@@ -140,6 +194,14 @@ struct WorkList {
   DevMem item_mem, join_mem[2];
 };
 
+// All query rows of several samples in tiles of 32, whatever their sample, against the
+// rows that the samples share; every result is a part.
+struct JointPlan {
+  int per = 0, units = 0, parts = 0;  // as RowsJoinArgs; per = 0: none
+  DevMem tiles;
+  WorkList list;
+};
+
 }  // namespace attn
 }  // namespace cgtp
 
@@ -150,6 +212,7 @@ struct cgtp_attn_s {
   cgtp_dtype dtype = CGTP_F32;
   int device = 0;
   cgtp::attn::KernelTable k{};
+  cgtp::attn::SeqTable seq{};
   cgtp::DevMem table;  // int4 [DP]
 };
 
@@ -161,12 +224,28 @@ struct cgtp_attn_batch_s {
   cgtp::DevMem qtile_mem, ktile_mem;
   cgtp::attn::WorkList few, fwd, wide;  // forward, items of up to 1, 4 and 8 query tiles
   cgtp::attn::WorkList bwd;
+  bool causal = false, sequence = false;  // sequence: causal, or with shared rows
+  int64_t shared_tiles = 0;
+  cgtp::DevMem reach;                 // Reach [qtiles]
+  cgtp::attn::JointPlan joint;        // used where every sample has few rows
+};
+
+struct cgtp_attn_cache_s {
+  cgtp_attn attn = nullptr;
+  int64_t slots = 0, capacity = 0, shared = 0, shared_tiles = 0, qtiles = 0;
+  int device = 0;
+  int splits = 1, waves_a_head = 1, heads_a_group = 1, bundles = 1, tiles_a_slot = 1, min_tiles = 1, parts = 1;
+  int joins = 0;
+  cgtp::DevMem qtile_mem, shared_tile_mem, join_mem;
+  cgtp::attn::JointPlan joint;
 };
 
 namespace cgtp {
 
 cgtp_attn_s* build_attn(const char* irreps, int64_t heads, int64_t kv_heads, cgtp_dtype dtype);
-cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, const cgtp_samples_s* k);
+cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, const cgtp_samples_s* k, bool causal,
+                                    int64_t shared);
+cgtp_attn_cache_s* build_attn_cache(cgtp_attn_s* at, int64_t slots, int64_t capacity, int64_t shared);
 size_t attn_context_bytes(const cgtp_attn_batch_s* b);
 size_t attn_forward_ws_bytes(const cgtp_attn_batch_s* b, bool packed);
 size_t attn_backward_ws_bytes(const cgtp_attn_batch_s* b);
@@ -179,6 +258,13 @@ void attn_pack_launch(const cgtp_attn_batch_s* b, RowsIn k, RowsIn v, const uint
                       hipStream_t s);
 void attn_forward_launch(const cgtp_attn_batch_s* b, RowsIn q, const void* context, double scale, void* out,
                          float* lse, void* ws, hipStream_t s);
+size_t attn_cache_shared_bytes(const cgtp_attn_cache_s* c);
+size_t attn_step_ws_bytes(const cgtp_attn_cache_s* c);
+void attn_share_launch(const cgtp_attn_cache_s* c, RowsIn k, RowsIn v, const uint8_t* mask, void* context,
+                       hipStream_t s);
+void attn_step_launch(const cgtp_attn_cache_s* c, RowsIn q, RowsIn k, RowsIn v, void* k_cache, void* v_cache,
+                      const int32_t* lengths, const void* context, double scale, void* out, float* lse, void* ws,
+                      hipStream_t s);
 void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn v, const uint8_t* mask, double scale,
                           const void* out, const float* lse, RowsIn g, void* dq, void* dk, void* dv, void* ws,
                           hipStream_t s);

@@ -486,6 +486,26 @@ __device__ __forceinline__ void mask_scores(f32x16& s, const float* bias, int h)
   }
 }
 
+// The key tile that tile t of a work list stands for.
+template <bool SEQ, typename A>
+__device__ __forceinline__ int key_tile(const A& a, int skip, int t) {
+  return SEQ && t >= a.shared ? t + skip : t;
+}
+
+// Causal queries: a token's first hidden place among its own keys.
+template <typename A>
+__device__ __forceinline__ int hidden_from(const A& a, const Reach& re, int row) {
+  return row / a.G + re.shift;
+}
+
+// -inf for the keys of a tile from place `hidden` on (replaced, not added to: see
+// mask_scores).
+__device__ __forceinline__ void hide_later(f32x16& s, int tile, int hidden, int h) {
+  const int left = hidden - 32 * tile - 4 * h;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s[i] = 8 * (i / 4) + i % 4 < left ? s[i] : -INFINITY;
+}
+
 // Query fragments of tile `tl` straight from the rows.
 template <typename T, int DP>
 __device__ __forceinline__ void load_queries(const FwdArgs& a, const Tile& tl, int hk, int lane,
@@ -543,6 +563,7 @@ __device__ __forceinline__ void finish(const FwdArgs& a, const Item& it, const T
                                        const Running<DP / 32>& st, float exact_sum) {
   const int lane = lane_id(), n = lane % 32, h = lane / 32;
   const float l = half_sum(st.l), e = sizeof(T) == 2 ? half_sum(exact_sum) : l;
+  if (n >= tl.n) return;
   if (it.slot >= 0) {
     const int64_t r = (int64_t(it.slot) * it.stride + tile_in_item) * 32 + n;
     float* o = a.part + r * DP;
@@ -560,12 +581,101 @@ __device__ __forceinline__ void finish(const FwdArgs& a, const Item& it, const T
     if (h == 0) a.part_ml[r] = make_float4(l == 0.0f ? -INFINITY : st.m, l, e, 0.0f);
     return;
   }
-  if (n >= tl.n) return;
   const int row = tl.row0 + n, token = row / a.G, head = it.hk * a.G + row % a.G;
   const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
   scatter_acc(static_cast<T*>(a.out) + int64_t(token) * a.ldo, a.table, true, head, a.out_quad, h, st.o, inv);
   if (a.lse && h == 0)
     a.lse[int64_t(token) * a.heads + head] = l > 0.0f || l != l ? (st.m + __log2f(e)) * 0.69314718055994531f : -INFINITY;
+}
+
+// Element d of row r of a packed tile.
+template <typename T, int DP>
+__device__ __forceinline__ float row_frag_at(const T* tile, int r, int d) {
+  constexpr int VE = Op<T>::VE;
+  return to_acc<float>(tile[(d / (2 * VE) * 64 + d / VE % 2 * 32 + r) * VE + d % VE]);
+}
+template <typename T, int DP>
+__device__ __forceinline__ float col_frag_at(const T* tile, int r, int d) {
+  constexpr int VE = Op<T>::VE, FR = 16 / VE;
+  const int reg = r / 8 * 4 + r % 4, h = r / 4 % 2;
+  return to_acc<float>(tile[((d / 32 * FR + reg / VE) * 64 + 32 * h + d % 32) * VE + reg % VE]);
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int off = 1; off < 64; off *= 2) v += lane_fetch(v, (int(threadIdx.x & 63) ^ off) << 2);
+  return v;
+}
+
+// A matrix product adds weight 0 times value for the keys that a causal query does not
+// see, which is NaN where such a value is infinite or NaN. Rows that came out NaN with a
+// finite sum of weights are formed again here, key by key over those they see (lanes
+// along the head's elements), after finish() wrote them.
+template <typename T, int DP>
+__device__ __forceinline__ void redo_rows(const FwdArgs& a, const Item& it, const Reach& re, const Tile& tl,
+                                          int tile_in_item, const Running<DP / 32>& st) {
+  constexpr int PER = (DP + 63) / 64;
+  const int lane = lane_id();
+  const float sum = half_sum(st.l);
+  bool nan = false;
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) nan = nan || st.o[d][i] != st.o[d][i];
+  uint64_t rows = __ballot(nan && sum == sum);
+  rows = (rows | rows >> 32) & 0xffffffffu;
+  if (!rows) return;
+  wait_copies();  // (finish's stores of the same rows come first)
+  while (rows) {
+    const int n = __builtin_ctzll(rows);
+    rows &= rows - 1;
+    if (n >= tl.n) return;
+    const float m = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(st.m), n));
+    const float ref = m == -INFINITY ? 0.0f : m;
+    const int row = tl.row0 + n, token = row / a.G, head = it.hk * a.G + row % a.G;
+    const int hidden = hidden_from(a, re, row);
+    float q[PER], o[PER], l = 0.0f;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) {
+      const int4 at = a.table[min(lane + 64 * c, DP - 1)];
+      T x = static_cast<const T*>(a.q)[int64_t(token) * a.ldq + elem(at, true, head)];
+      q[c] = lane + 64 * c < DP && at.w ? (a.q_sign ? -to_acc<float>(x) : to_acc<float>(x)) : 0.0f;
+      o[c] = 0.0f;
+    }
+    for (int t = it.b0; t < it.b1; ++t) {
+      const int tile = key_tile<true>(a, re.skip, t);
+      const int64_t at = (int64_t(tile) * a.groups + it.hk) * Dims<T, DP>::TILE;
+      const T *kt = static_cast<const T*>(a.kf) + at, *vt = static_cast<const T*>(a.vf) + at;
+      const int seen = t < a.shared ? 32 : min(32, hidden - 32 * tile);
+      for (int r = 0; r < seen; ++r) {
+        if (a.bias[int64_t(tile) * 32 + r] < 0.0f) continue;
+        float s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < PER; ++c)
+          if (lane + 64 * c < DP) s += q[c] * row_frag_at<T, DP>(kt, r, lane + 64 * c);
+        const float w = exp2_fast(fmaf(wave_sum(s), a.scale2, -ref));
+        T wt;
+        from_acc(wt, w);
+        const float p = to_acc<float>(wt);
+        l += p;
+#pragma unroll
+        for (int c = 0; c < PER; ++c)
+          if (lane + 64 * c < DP) o[c] += p * col_frag_at<T, DP>(vt, r, lane + 64 * c);
+      }
+    }
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+    const int64_t part = (int64_t(it.slot) * it.stride + tile_in_item) * 32 + n;
+    for (int c = 0; c < PER; ++c) {
+      const int d = lane + 64 * c;
+      if (d >= DP) break;
+      if (it.slot >= 0) {
+        a.part[part * DP + d] = o[c];
+        continue;
+      }
+      const int4 at = a.table[d];
+      if (at.w) from_acc(static_cast<T*>(a.out)[int64_t(token) * a.ldo + elem(at, true, head)], o[c] * inv);
+    }
+    if (lane == 0 && it.slot >= 0) a.part_ml[part].y = l;  // (reference and exact sum stay)
+  }
 }
 
 // Tiles of the keys and of the values in shared memory: R - 1 turns for a copy to
@@ -578,8 +688,8 @@ constexpr int fwd_ring() {
 
 // The square of a bound of all scores (log2 domain) of a wave's queries against
 // the tiles of an item: |q.k| <= |q| |k|. NaN where a row holds one.
-template <typename T, int DP, int RT>
-__device__ __forceinline__ float score_bound2(const FwdArgs& a, const Item& it, int lane,
+template <typename T, int DP, int RT, bool SEQ>
+__device__ __forceinline__ float score_bound2(const FwdArgs& a, const Item& it, int skip, int lane,
                                               const typename Op<T>::Frag (&q)[RT][Dims<T, DP>::KSTEPS]) {
   using D = Dims<T, DP>;
   float qn = 0.0f, kn = 0.0f;
@@ -597,7 +707,7 @@ __device__ __forceinline__ float score_bound2(const FwdArgs& a, const Item& it, 
     qn = n2 > qn || n2 != n2 ? n2 : qn;
   }
   for (int t = it.b0 + lane; t < it.b1; t += 64) {
-    const float n2 = a.norms[int64_t(t) * a.groups + it.hk];
+    const float n2 = a.norms[int64_t(key_tile<SEQ>(a, skip, t)) * a.groups + it.hk];
     kn = n2 > kn || n2 != n2 ? n2 : kn;
   }
   const bool nan = __any(qn != qn || kn != kn);
@@ -624,7 +734,11 @@ constexpr float kBound = 40.0f;
 // 1177 TFLOP/s (994 us over the first 50 passes of an idle card) with matrix cores busy
 // 56 % of the cycles; a ragged batch of heads of 144 (RT = 1): 144 us, 30 %; fp32, heads of
 // 128: 66 %.
-template <typename T, int DP, int RT>
+//
+// SEQ: key tiles by way of the queries' Reach, and in causal batches the scores of
+// later keys hidden in the tiles where some of the wave's queries see only a part (one
+// or two of a wave's; a wave leaves out the tiles that none of its queries sees).
+template <typename T, int DP, int RT, bool SEQ>
 __global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T, DP>::UNITS)) void fwd_kernel(
     FwdArgs a) {
   using D = Dims<T, DP>;
@@ -637,9 +751,10 @@ __global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T,
   const int lane = int(threadIdx.x) % 64, wave = wave_id(), h = lane / 32;
   const int mine = min(max(it.tiles - wave * RT, 0), RT);  // query tiles of this wave
   const int n = it.b1 - it.b0;
+  const Reach re = SEQ ? ldc(a.reach + it.a0) : Reach{0, 0};  // (all query tiles of an item are of one sample)
   // tile t of the keys and of the values, a quarter by each wave
   const auto copy = [&](int t, int slot) {
-    const int64_t at = (int64_t(min(it.b0 + t, it.b1 - 1)) * a.groups + it.hk) * D::TILE;
+    const int64_t at = (int64_t(key_tile<SEQ>(a, re.skip, min(it.b0 + t, it.b1 - 1))) * a.groups + it.hk) * D::TILE;
 #pragma unroll
     for (int k = 0; k < D::UNITS / 2; ++k) {
       const int u = k * 4 + wave;
@@ -662,7 +777,20 @@ __global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T,
 #pragma unroll
     for (int d = 0; d < D::DT; ++d) st[r].o[d] = zero16();
   }
-  const float b2 = score_bound2<T, DP, RT>(a, it, lane, q);
+  // causal: own key tiles from `part` on hold keys that some query of a row of tiles does
+  // not see, those from `none` on are seen by no query of the wave
+  int part[RT], none = INT_MAX;
+  if constexpr (SEQ)
+    if (a.causal) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const Tile tl = ldc(a.qtiles + it.a0 + (r < mine ? wave * RT + r : 0));
+        part[r] = hidden_from(a, re, tl.row0) >> 5;
+        const int end = (hidden_from(a, re, tl.row0 + tl.n - 1) + 31) >> 5;
+        none = r == 0 ? end : max(none, end);
+      }
+    }
+  const float b2 = score_bound2<T, DP, RT, SEQ>(a, it, re.skip, lane, q);
   if (lane == 0) bounds[wave] = b2;
   turn_end<0>();
   bool bounded = true;
@@ -685,9 +813,10 @@ __global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T,
     constexpr bool kMoving = decltype(moving)::value;
     int slot = 0;
     for (int t = 0; t < n; ++t) {
-      const int tile = it.b0 + t;
+      const int tile = key_tile<SEQ>(a, re.skip, it.b0 + t);
+      const bool later = SEQ && a.causal && it.b0 + t >= a.shared;
       copy(t + R - 1, slot == 0 ? R - 1 : slot - 1);
-      if (mine > R0) {
+      if (mine > R0 && !(later && tile >= none)) {
         f32x16 s[N];
         products(true);
 #pragma unroll
@@ -702,6 +831,14 @@ __global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T,
         if (ldc(a.flags + tile))
 #pragma unroll
           for (int r = 0; r < N; ++r) mask_scores(s[r], a.bias + int64_t(tile) * 32, h);
+        if constexpr (SEQ)
+          if (later)
+#pragma unroll
+            for (int r = 0; r < N; ++r)
+              if (tile >= part[R0 + r]) {
+                const Tile tl = ldc(a.qtiles + it.a0 + (R0 + r < mine ? wave * RT + R0 + r : 0));
+                hide_later(s[r], tile, hidden_from(a, re, tl.row0 + min(lane_id() % 32, tl.n - 1)), h);
+              }
         Frag p[N][D::FR];
 #pragma unroll
         for (int r = 0; r < N; ++r) {
@@ -745,14 +882,19 @@ __global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T,
   }
 #pragma unroll
   for (int r = 0; r < RT; ++r)
-    if (r < mine) finish<T, DP>(a, it, ldc(a.qtiles + it.a0 + wave * RT + r), wave * RT + r, st[r], sum(r));
+    if (r < mine) {
+      const Tile tl = ldc(a.qtiles + it.a0 + wave * RT + r);
+      finish<T, DP>(a, it, tl, wave * RT + r, st[r], sum(r));
+      if constexpr (SEQ)
+        if (a.causal) redo_rows<T, DP>(a, it, re, tl, wave * RT + r, st[r]);
+    }
 }
 
 // At most 32 query rows against a long context (single tokens): the four waves
 // take every fourth key tile, read straight into registers, and join. Bound: the
 // keys' and values' bytes: 64 tokens against 1000 - 8000 keys each, heads of 128,
 // bf16: 114 us = 5.4 TB/s.
-template <typename T, int DP>
+template <typename T, int DP, bool SEQ>
 __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void fwd_few_kernel(FwdArgs a) {
   using D = Dims<T, DP>;
   using Frag = typename Op<T>::Frag;
@@ -762,13 +904,15 @@ __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void fwd_few_ke
   if (it.tiles == 0) return;
   const int lane = int(threadIdx.x) % 64, wave = wave_id(), h = lane / 32;
   const Tile tl = ldc(a.qtiles + it.a0);
+  const Reach re = SEQ ? ldc(a.reach + it.a0) : Reach{0, 0};
   // the widest heads leave no registers for whole tiles: read as they are used
   constexpr bool kStream = DP * int(sizeof(T)) > 640;
   // a tile's units, in registers a turn ahead: the keys' are read again as soon as
   // the scores are done, the values' as soon as they are added
   u32x4 k[kStream ? 1 : D::UNITS], v[kStream ? 1 : D::UNITS];
   const auto tile = [&](const void* src, int t) {
-    return static_cast<const T*>(src) + (int64_t(min(t, it.b1 - 1)) * a.groups + it.hk) * D::TILE;
+    return static_cast<const T*>(src) +
+           (int64_t(key_tile<SEQ>(a, re.skip, min(t, it.b1 - 1))) * a.groups + it.hk) * D::TILE;
   };
   const auto fetch = [&](const T* src, auto& dst) {
     if constexpr (!kStream)
@@ -798,7 +942,11 @@ __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void fwd_few_ke
       }
     }
     fetch(tile(a.kf, t + 4), k);
-    if (ldc(a.flags + t)) mask_scores(sc, a.bias + int64_t(t) * 32, h);
+    const int at = key_tile<SEQ>(a, re.skip, t);
+    if (ldc(a.flags + at)) mask_scores(sc, a.bias + int64_t(at) * 32, h);
+    if constexpr (SEQ)
+      if (a.causal && t >= a.shared && at >= hidden_from(a, re, tl.row0) >> 5)
+        hide_later(sc, at, hidden_from(a, re, tl.row0 + min(lane % 32, tl.n - 1)), h);
     raise_reference(st, top_score(sc, a.scale2), e, exact);
     Frag p[D::FR];
     weigh<T, true>(st, sc, a.scale2, 0.0f, e, exact, p);
@@ -859,6 +1007,8 @@ __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void fwd_few_ke
     st.l = ml[0][1][lane] + ml[2][1][lane] + (ml[1][1][lane] + ml[3][1][lane]);
     e = ml[0][2][lane] + ml[2][2][lane] + (ml[1][2][lane] + ml[3][2][lane]);
     finish<T, DP>(a, it, tl, 0, st, e);
+    if constexpr (SEQ)
+      if (a.causal) redo_rows<T, DP>(a, it, re, tl, 0, st);
   }
 }
 
@@ -927,7 +1077,7 @@ __device__ __forceinline__ void finish_grad(const BwdArgs& a, const Item& it, co
 // S^T = K Q^T, P^T = exp2(S^T - lse), dP^T = V dO^T, dS^T = P^T (dP^T - delta),
 // dQ^T += K^T dS^T. Three packed forms of a tile pass through shared memory: K
 // rows, V rows, K columns.
-template <typename T, int DP>
+template <typename T, int DP, bool SEQ>
 __device__ __forceinline__ void dq_item(const BwdArgs& a, const Item& it, u32x4* pool, float* bias_pool) {
   using D = Dims<T, DP>;
   using Frag = typename Op<T>::Frag;
@@ -948,11 +1098,21 @@ __device__ __forceinline__ void dq_item(const BwdArgs& a, const Item& it, u32x4*
     g[t] = as_frag<Frag>(unit16(a.qforms<T>(kGRows) + qat * D::TILE, t, lane));
   }
   const float lse2 = a.rows[qat * 64 + n], delta = a.rows[qat * 64 + 32 + n];
+  const Reach re = SEQ ? ldc(a.reach + qt) : Reach{0, 0};
+  // causal: as in fwd_kernel
+  int hidden = 0, part = 0, none = 0;
+  if constexpr (SEQ)
+    if (a.causal) {
+      hidden = hidden_from(a, re, tl.row0 + min(n, tl.n - 1));
+      part = hidden_from(a, re, tl.row0) >> 5;
+      none = (hidden_from(a, re, tl.row0 + tl.n - 1) + 31) >> 5;
+    }
   f32x16 dq[D::DT];
 #pragma unroll
   for (int d = 0; d < D::DT; ++d) dq[d] = zero16();
 
-  const auto fetch = [&](int tile, int buf) {
+  const auto fetch = [&](int t, int buf) {
+    const int tile = key_tile<SEQ>(a, re.skip, t);
     const T* base = a.kforms<T>(0) + (int64_t(tile) * a.groups + it.hk) * D::TILE;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
@@ -968,7 +1128,9 @@ __device__ __forceinline__ void dq_item(const BwdArgs& a, const Item& it, u32x4*
   for (int t = it.b0; t < it.b1; ++t) {
     const int buf = BUFS == 2 ? (t - it.b0) & 1 : 0;
     if (BUFS == 2 && t + 1 < it.b1) fetch(t + 1, buf ^ 1);
-    if (active) {
+    const int tile = key_tile<SEQ>(a, re.skip, t);
+    const bool later = SEQ && a.causal && t >= a.shared;
+    if (active && !(later && tile >= none)) {
       f32x16 s = zero16(), dp = zero16();
 #pragma unroll
       for (int u = 0; u < D::KSTEPS; ++u) {
@@ -986,6 +1148,10 @@ __device__ __forceinline__ void dq_item(const BwdArgs& a, const Item& it, u32x4*
           s[4 * b + i] = p * (dp[4 * b + i] - delta);
         }
       }
+      if constexpr (SEQ)
+        if (later && tile >= part)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[i] = 8 * (i / 4) + i % 4 < hidden - 32 * tile - 4 * h ? s[i] : 0.0f;
       Frag ds[D::FR];
 #pragma unroll
       for (int f = 0; f < D::FR; ++f) ds[f] = Op<T>::from_acc(s, f);
@@ -1012,8 +1178,9 @@ __device__ __forceinline__ void dq_item(const BwdArgs& a, const Item& it, u32x4*
 // of the group): S = Q K^T, P = exp2(S - lse), dV^T += dO^T P, dP = dO V^T,
 // dS = P (dP - delta), dK^T += Q^T dS. PART 0: both (one_pass); else as PART 1
 // (grad_v) and 2 (grad_k).
-template <typename T, int DP, int PART>
-__device__ __forceinline__ void dkv_item(const BwdArgs& a, const Item& it, u32x4* pool, float* row_pool) {
+template <typename T, int DP, int PART, bool SEQ>
+__device__ __forceinline__ void dkv_item(const BwdArgs& a, const Item& it, u32x4* pool, float* row_pool,
+                                         int* hidden_pool) {
   using D = Dims<T, DP>;
   using Frag = typename Op<T>::Frag;
   constexpr bool WANT_V = PART != 2, WANT_K = PART != 1;
@@ -1023,6 +1190,7 @@ __device__ __forceinline__ void dkv_item(const BwdArgs& a, const Item& it, u32x4
   constexpr int BUFS = stage_buffers(STAGE);
   const auto sh = reinterpret_cast<u32x4(*)[STAGE * 64]>(pool);
   const auto rows = reinterpret_cast<float(*)[64]>(row_pool);
+  const auto hidden = reinterpret_cast<int(*)[32]>(hidden_pool);  // causal: of every query row of a tile
   const int lane = int(threadIdx.x) % 64, wave = wave_id(), n = lane % 32, h = lane / 32;
   const bool active = wave < it.tiles;
   const int kt = it.a0 + (active ? wave : 0);
@@ -1055,6 +1223,11 @@ __device__ __forceinline__ void dkv_item(const BwdArgs& a, const Item& it, u32x4
       copy_unit(base + form * a.qstride, u % D::UNITS, lane, &sh[buf][u * 64]);
     }
     if (threadIdx.x < 64) rows[buf][threadIdx.x] = a.rows[at * 64 + threadIdx.x];
+    if constexpr (SEQ)
+      if (a.causal && threadIdx.x < 32) {
+        const Tile ql = ldc(a.qtiles + tile);
+        hidden[buf][threadIdx.x] = hidden_from(a, ldc(a.reach + tile), ql.row0 + min(int(threadIdx.x), ql.n - 1));
+      }
   };
   if (it.b0 < it.b1) fetch(it.b0, 0);
   wait_copies();
@@ -1062,7 +1235,15 @@ __device__ __forceinline__ void dkv_item(const BwdArgs& a, const Item& it, u32x4
   for (int t = it.b0; t < it.b1; ++t) {
     const int buf = BUFS == 2 ? (t - it.b0) & 1 : 0;
     if (BUFS == 2 && t + 1 < it.b1) fetch(t + 1, buf ^ 1);
-    if (active) {
+    // keys that all samples share are seen by every query
+    const bool later = SEQ && a.causal && kt >= a.shared;
+    bool some = true, all = true;
+    if constexpr (SEQ)
+      if (later) {
+        some = 32 * kt < __builtin_amdgcn_readfirstlane(hidden[buf][31]);
+        all = 32 * kt + 31 < __builtin_amdgcn_readfirstlane(hidden[buf][0]);
+      }
+    if (active && some) {
       f32x16 s = zero16(), dp = zero16();
 #pragma unroll
       for (int u = 0; u < D::KSTEPS; ++u) {
@@ -1081,6 +1262,14 @@ __device__ __forceinline__ void dkv_item(const BwdArgs& a, const Item& it, u32x4
           if (WANT_K) dp[4 * b + i] = s[4 * b + i] * (dp[4 * b + i] - de[i]);
         }
       }
+      if constexpr (SEQ)
+        if (!all)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const bool seen = 32 * kt + n < hidden[buf][8 * (i / 4) + 4 * h + i % 4];
+            s[i] = seen ? s[i] : 0.0f;
+            if (WANT_K) dp[i] = seen ? dp[i] : 0.0f;
+          }
       Frag p[D::FR], ds[D::FR];
 #pragma unroll
       for (int f = 0; f < D::FR; ++f) {
@@ -1134,20 +1323,21 @@ constexpr int bwd_units() {
   constexpr int a = stage_units(3 * U), b = stage_units(dkv_forms(one_pass(DP, sizeof(T)) ? 0 : 1) * U);
   return a > b ? a : b;
 }
-template <typename T, int DP>
+template <typename T, int DP, bool SEQ>
 __global__ __launch_bounds__(kThreads, lds_waves(bwd_units<T, DP>())) void bwd_kernel(BwdArgs a) {
   __shared__ u32x4 pool[bwd_units<T, DP>() * 64];
   __shared__ __attribute__((aligned(16))) float rows[2 * 64];
+  __shared__ __attribute__((aligned(16))) int hidden[SEQ ? 2 * 32 : 4];
   const Item it = ldc(a.items + blockIdx.x);
   if (it.tiles == 0) return;
   if (it.kind == kItemQ) {
-    if (a.dq) dq_item<T, DP>(a, it, pool, rows);
+    if (a.dq) dq_item<T, DP, SEQ>(a, it, pool, rows);
   } else if constexpr (one_pass(DP, sizeof(T))) {
-    if (a.dk || a.dv) dkv_item<T, DP, 0>(a, it, pool, rows);
+    if (a.dk || a.dv) dkv_item<T, DP, 0, SEQ>(a, it, pool, rows, hidden);
   } else if (it.kind == kItemV) {
-    if (a.dv) dkv_item<T, DP, 1>(a, it, pool, rows);
+    if (a.dv) dkv_item<T, DP, 1, SEQ>(a, it, pool, rows, hidden);
   } else {
-    if (a.dk) dkv_item<T, DP, 2>(a, it, pool, rows);
+    if (a.dk) dkv_item<T, DP, 2, SEQ>(a, it, pool, rows, hidden);
   }
 }
 
@@ -1181,16 +1371,16 @@ struct Kernels {
     hipLaunchKernelGGL(k, dim3(unsigned((a.ntiles + 7) / 8 * 8 * a.groups)), dim3(kThreads), 0, s, a);
   }
   static void fwd(const FwdArgs& a, int items, int tiles, hipStream_t s) {
-    if (tiles == 1) hipLaunchKernelGGL((fwd_few_kernel<T, DP>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
-    if (tiles == 4) hipLaunchKernelGGL((fwd_kernel<T, DP, 1>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
+    if (tiles == 1) hipLaunchKernelGGL((fwd_few_kernel<T, DP, false>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
+    if (tiles == 4) hipLaunchKernelGGL((fwd_kernel<T, DP, 1, false>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
     if constexpr (wide_forward(DP, sizeof(T)))
-      if (tiles == 8) hipLaunchKernelGGL((fwd_kernel<T, DP, 2>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
+      if (tiles == 8) hipLaunchKernelGGL((fwd_kernel<T, DP, 2, false>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
   }
   static void fwd_join(const FwdArgs& a, int joins, hipStream_t s) {
     hipLaunchKernelGGL((fwd_join_kernel<T, DP>), dim3(unsigned(joins), DP / 32), dim3(kThreads), 0, s, a);
   }
   static void bwd(const BwdArgs& a, int items, hipStream_t s) {
-    hipLaunchKernelGGL((bwd_kernel<T, DP>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((bwd_kernel<T, DP, false>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
   }
   static void grad_join(const GradJoinArgs& a, int joins, int tensors, hipStream_t s) {
     hipLaunchKernelGGL((grad_join_kernel<T, DP>), dim3(unsigned(joins), DP / 32, unsigned(tensors)), dim3(kThreads), 0,

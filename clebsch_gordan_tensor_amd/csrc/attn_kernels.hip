@@ -17,6 +17,12 @@ KernelTable kernels_bf16_a(int dp);
 KernelTable kernels_bf16_b(int dp);
 KernelTable kernels_f32(int dp) { return dp <= 128 ? kernels_f32_a(dp) : kernels_f32_b(dp); }
 KernelTable kernels_bf16(int dp) { return dp <= 128 ? kernels_bf16_a(dp) : kernels_bf16_b(dp); }
+SeqTable seq_kernels_f32_a(int dp);
+SeqTable seq_kernels_f32_b(int dp);
+SeqTable seq_kernels_bf16_a(int dp);
+SeqTable seq_kernels_bf16_b(int dp);
+SeqTable seq_kernels_f32(int dp) { return dp <= 128 ? seq_kernels_f32_a(dp) : seq_kernels_f32_b(dp); }
+SeqTable seq_kernels_bf16(int dp) { return dp <= 128 ? seq_kernels_bf16_a(dp) : seq_kernels_bf16_b(dp); }
 
 namespace {
 
@@ -26,18 +32,21 @@ constexpr int kCus = 256;
 // head of 128: 1095 us against 1183 us with 32)
 constexpr int kWideTiles = 8;
 
-// One side of a batch cut into 32-row tiles, per sample.
+// One side of a batch cut into 32-row tiles, per sample, after those of `shared` rows
+// that come before the samples'.
 struct Side {
   std::vector<Tile> tiles;
   std::vector<int32_t> first;  // first tile of each sample, [S + 1]
 };
 
-Side cut(const std::vector<int64_t>& ptr, int64_t G) {
+Side cut(const std::vector<int64_t>& ptr, int64_t G, int64_t shared = 0) {
   Side s;
-  if (ptr.back() * G > INT32_MAX - 64) throw Error{CGTP_ERR_UNSUPPORTED, "attention: rows x heads beyond 2^31"};
+  if (ptr.back() * G + shared > INT32_MAX - 64)
+    throw Error{CGTP_ERR_UNSUPPORTED, "attention: rows x heads beyond 2^31"};
+  for (int64_t r = 0; r < shared; r += 32) s.tiles.push_back({int32_t(r), int32_t(std::min<int64_t>(32, shared - r))});
   for (size_t i = 0; i + 1 < ptr.size(); ++i) {
     s.first.push_back(int32_t(s.tiles.size()));
-    const int64_t a = ptr[i] * G, b = ptr[i + 1] * G;
+    const int64_t a = shared + ptr[i] * G, b = shared + ptr[i + 1] * G;
     for (int64_t r = a; r < b; r += 32) s.tiles.push_back({int32_t(r), int32_t(std::min<int64_t>(32, b - r))});
   }
   s.first.push_back(int32_t(s.tiles.size()));
@@ -61,6 +70,62 @@ void add_units(std::vector<Unit>& u, const Side& a, const Side& b, int side, int
     if (!take(n)) continue;
     for (int t = 0; t < n; t += per)
       u.push_back({int32_t(s), side, a.first[s] + t, std::min(per, n - t), b.first[s], b.first[s + 1], weight, kinds});
+  }
+}
+
+// How the queries of a sequence batch see the context: key tiles of shared rows, and
+// whether a query's own keys end with its place (Reach).
+struct Sight {
+  const std::vector<int64_t>&qptr, &kptr;
+  const Side &q, &k;
+  int64_t G, shared_tiles;
+  bool causal;
+  // own keys of sample s, counted from its first, that query token i of the sample sees
+  int64_t seen(size_t s, int64_t i) const {
+    const int64_t nq = qptr[s + 1] - qptr[s], nk = kptr[s + 1] - kptr[s];
+    return causal ? std::max<int64_t>(0, std::min(nk, i + nk - nq + 1)) : nk;
+  }
+  int32_t skip(size_t s) const { return shared_tiles ? int32_t(k.first[s] - shared_tiles) : 0; }
+  Reach reach(size_t s) const {
+    const int64_t nq = qptr[s + 1] - qptr[s], nk = kptr[s + 1] - kptr[s];
+    return {skip(s), int32_t(32 * int64_t(k.first[s]) + nk - nq + 1 - qptr[s])};
+  }
+};
+
+// Query tiles against the keys that some query of a unit sees: shared and own ones
+// (`own_only`: those alone). Longest units first: in a causal sample the last.
+template <typename F>
+void add_query_units(std::vector<Unit>& u, const Sight& v, int per, int weight, int32_t kind, bool own_only, F&& take) {
+  for (size_t s = 0; s + 1 < v.q.first.size(); ++s) {
+    const int n = v.q.first[s + 1] - v.q.first[s];
+    if (n == 0 || !take(n)) continue;
+    for (int t = (n - 1) / per * per; t >= 0; t -= per) {
+      const int tiles = std::min(per, n - t);
+      const Tile& last = v.q.tiles[size_t(v.q.first[s] + t + tiles - 1)];
+      const int64_t token = (last.row0 + last.n - 1) / v.G - v.qptr[s];
+      const int32_t own0 = v.k.first[s] - v.skip(s);  // in the numbering of work lists
+      u.push_back({int32_t(s), 0, v.q.first[s] + t, tiles, v.shared_tiles && !own_only ? 0 : own0,
+                   own0 + int32_t((v.seen(s, token) + 31) / 32), weight, {kind}});
+    }
+  }
+}
+
+// Key tiles against the query tiles that see some of their keys: those of shared rows
+// (as one more sample) against all, every sample's own against those from the first
+// query on that sees the first key.
+void add_key_units(std::vector<Unit>& u, const Sight& v, int per, int weight, const std::vector<int32_t>& kinds) {
+  const int S = int(v.q.first.size()) - 1;
+  for (int t = 0; t < v.shared_tiles; t += per)
+    u.push_back({S, 1, t, int(std::min<int64_t>(per, v.shared_tiles - t)), 0, v.q.first[size_t(S)], weight, kinds});
+  for (size_t s = 0; s < size_t(S); ++s) {
+    const int n = v.k.first[s + 1] - v.k.first[s];
+    const int64_t nq = v.qptr[s + 1] - v.qptr[s], nk = v.kptr[s + 1] - v.kptr[s];
+    for (int t = 0; t < n; t += per) {
+      const int64_t i = v.causal ? std::max<int64_t>(0, 32 * int64_t(t) - (nk - nq)) : 0;
+      const int32_t end = v.q.first[s + 1];
+      const int32_t b0 = i >= nq ? end : v.q.first[s] + int32_t(i * v.G / 32);
+      u.push_back({int32_t(s), 1, v.k.first[s] + t, std::min(per, n - t), b0, end, weight, kinds});
+    }
   }
 }
 
@@ -127,7 +192,10 @@ void need_launch(int64_t workgroups) {
 // are given to one die and follow each other there, those with the longest items
 // first, so that the short ones fill the end; a group bigger than a die's share
 // goes round several.
-void build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, int slots, int min_len) {
+// With all_parts every result is a part, also that of an unsplit unit. Returns the
+// largest number of parts of a unit.
+int64_t build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, int slots, int min_len,
+              bool all_parts = false) {
   int64_t whole = 0;
   for (const Unit& x : u) whole += int64_t(x.kinds.size()) * groups;
   need_launch(whole);  // (before the lists are laid out)
@@ -139,7 +207,7 @@ void build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, int 
   };
   std::vector<Group> gs;
   std::vector<Join> joins[2];
-  int64_t nslot[2] = {0, 0};
+  int64_t nslot[2] = {0, 0}, most = 1;
   for (size_t i = 0; i < u.size();) {
     size_t j = i;
     while (j < u.size() && u[j].sample == u[i].sample && u[j].side == u[i].side) ++j;
@@ -148,17 +216,19 @@ void build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, int 
       for (size_t k = i; k < j; ++k) {
         const Unit& x = u[k];
         const int64_t n = x.b1 - x.b0, parts = parts_of(x, cost);
+        const bool split = all_parts || parts > 1;
+        most = std::max(most, parts);
         int64_t& slot = nslot[x.side];
         for (size_t q = 0; q < g.size(); ++q)
           for (int64_t p = 0; p < parts; ++p) {
             const int32_t b0 = int32_t(x.b0 + n * p / parts), b1 = int32_t(x.b0 + n * (p + 1) / parts);
             g[q].items.push_back(
-                {x.a0, x.tiles, b0, b1, hk, parts > 1 ? int32_t(slot + p) : -1, stride, x.kinds[q]});
+                {x.a0, x.tiles, b0, b1, hk, split ? int32_t(slot + p) : -1, stride, x.kinds[q]});
             g[q].costs.push_back(int64_t(b1 - b0 + 1) * x.weight);
             g[q].work += g[q].costs.back();
             g[q].longest = std::max(g[q].longest, g[q].costs.back());
           }
-        if (parts > 1) {
+        if (split) {
           for (int t = 0; t < x.tiles; ++t)
             joins[x.side].push_back({x.a0 + t, hk, int32_t(slot), int32_t(parts), stride, t, 0, 0});
           slot += parts;
@@ -208,7 +278,35 @@ void build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, int 
     w.joins[k] = int(joins[k].size());
     w.join_mem[k].upload(joins[k].data(), joins[k].size() * sizeof(Join));
   }
+  return most;
 }
+
+// Workgroups of the forward at once: two a compute unit where registers and shared
+// memory allow.
+int forward_slots(const cgtp_attn_s* at) { return at->DP * int(dtype_size(at->dtype)) <= 512 ? 2 * kCus : kCus; }
+
+// The rows of `tokens` tokens in tiles whatever their sample, against shared_tiles key
+// tiles. All units see the same tiles, so they have equally many parts.
+void build_joint(JointPlan& j, const cgtp_attn_s* at, int64_t tokens, int64_t shared_tiles) {
+  const Side rows = cut({0, tokens}, at->G);
+  const int n = int(rows.tiles.size());
+  if (n == 0) return;
+  j.per = n == 1 ? 1 : n >= kWideTiles && wide_forward(at->DP, dtype_size(at->dtype)) ? 8 : 4;
+  j.units = (n + j.per - 1) / j.per;
+  j.tiles.upload(rows.tiles.data(), rows.tiles.size() * sizeof(Tile));
+  std::vector<Unit> u;
+  for (int t = 0; t < n; t += j.per)
+    u.push_back({0, 0, t, std::min(j.per, n - t), 0, int32_t(shared_tiles), 1, {0}});
+  j.parts = int(build(j.list, u, j.per, at->kv_heads, j.per == 8 ? 2 * kCus : forward_slots(at), j.per == 1 ? 8 : 4,
+                      true));
+}
+
+// Partial results of both sides of a join by rows.
+struct RowParts {
+  float4 *own_ml, *joint_ml;
+  float *own, *joint;
+  size_t bytes;
+};
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
@@ -224,6 +322,17 @@ struct Carve {
   }
 };
 
+RowParts carve_row_parts(void* p, int64_t own_tiles, int64_t joint_tiles, int dp) {
+  Carve c{static_cast<char*>(p)};
+  RowParts x{};
+  x.own_ml = static_cast<float4*>(c.take(size_t(own_tiles) * 32 * sizeof(float4)));
+  x.joint_ml = static_cast<float4*>(c.take(size_t(joint_tiles) * 32 * sizeof(float4)));
+  x.own = static_cast<float*>(c.take(size_t(own_tiles) * 32 * size_t(dp) * 4));
+  x.joint = static_cast<float*>(c.take(size_t(joint_tiles) * 32 * size_t(dp) * 4));
+  x.bytes = c.used;
+  return x;
+}
+
 size_t tile_bytes(const cgtp_attn_s* a) { return size_t(a->DP) * 32 * dtype_size(a->dtype); }
 
 // Packed context: key row fragments, value column fragments, key biases.
@@ -233,18 +342,19 @@ struct Context {
   int32_t* flags;
   size_t bytes;
 };
-Context carve_context(const cgtp_attn_batch_s* b, void* p) {
+Context carve_context(const cgtp_attn_s* a, int64_t ktiles, void* p) {
   Carve c{static_cast<char*>(p)};
-  const size_t n = size_t(b->ktiles) * size_t(b->attn->kv_heads) * tile_bytes(b->attn);
+  const size_t n = size_t(ktiles) * size_t(a->kv_heads) * tile_bytes(a);
   Context x{};
   x.kf = c.take(n);
   x.vf = c.take(n);
-  x.bias = static_cast<float*>(c.take(size_t(b->ktiles) * 32 * 4));
-  x.norms = static_cast<float*>(c.take(size_t(b->ktiles) * size_t(b->attn->kv_heads) * 4));
-  x.flags = static_cast<int32_t*>(c.take(size_t(b->ktiles) * 4));
+  x.bias = static_cast<float*>(c.take(size_t(ktiles) * 32 * 4));
+  x.norms = static_cast<float*>(c.take(size_t(ktiles) * size_t(a->kv_heads) * 4));
+  x.flags = static_cast<int32_t*>(c.take(size_t(ktiles) * 4));
   x.bytes = c.used;
   return x;
 }
+Context carve_context(const cgtp_attn_batch_s* b, void* p) { return carve_context(b->attn, b->ktiles, p); }
 
 struct Backward {
   char *kforms, *qforms;  // at strides of kbytes and qbytes
@@ -315,53 +425,134 @@ cgtp_attn_s* build_attn(const char* irreps, int64_t heads, int64_t kv_heads, cgt
   }
   table.resize(size_t(a->DP), int4{0, 0, 0, 0});
   a->k = dtype == CGTP_BF16 ? kernels_bf16(a->DP) : kernels_f32(a->DP);
+  a->seq = dtype == CGTP_BF16 ? seq_kernels_bf16(a->DP) : seq_kernels_f32(a->DP);
   a->device = current_device();
   a->table.upload(table.data(), table.size() * sizeof(int4));
   return a.release();
 }
 
-cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, const cgtp_samples_s* k) {
+cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, const cgtp_samples_s* k, bool causal,
+                                    int64_t shared) {
   if (q->S != k->S) throw Error{CGTP_ERR_INVALID_ARG, "attention: the two sides have different numbers of samples"};
   auto b = std::make_unique<cgtp_attn_batch_s>();
   b->attn = at;
   b->nq = q->rows;
-  b->nk = k->rows;
+  b->nk = shared + k->rows;
   b->device = current_device();
-  const Side qs = cut(q->ptr, at->G), ks = cut(k->ptr, 1);
+  if (b->nk > INT32_MAX - 64) throw Error{CGTP_ERR_UNSUPPORTED, "attention: context of more than 2^31 rows"};
+  const Side qs = cut(q->ptr, at->G), ks = cut(k->ptr, 1, shared);
   b->qtiles = int64_t(qs.tiles.size());
   b->ktiles = int64_t(ks.tiles.size());
+  b->shared_tiles = (shared + 31) / 32;
+  b->causal = causal;
+  b->sequence = causal || shared > 0;
+  // tokens and places (32 a tile) are compared in 32 bits
+  if (causal && (b->nq > 1 << 30 || 32 * b->ktiles > 1 << 30))
+    throw Error{CGTP_ERR_UNSUPPORTED, "attention: a causal batch of more than 2^30 rows"};
   need_launch((std::max(b->qtiles, b->ktiles) + 7) / 8 * 8 * at->kv_heads);  // of the packing
   b->qtile_mem.upload(qs.tiles.data(), qs.tiles.size() * sizeof(Tile));
   b->ktile_mem.upload(ks.tiles.data(), ks.tiles.size() * sizeof(Tile));
   const int g = at->kv_heads;
+  const Sight sight{q->ptr, k->ptr, qs, ks, at->G, b->shared_tiles, causal};
+  bool few = true;
+  if (b->sequence) {
+    std::vector<Reach> reach;
+    for (size_t s = 0; s + 1 < qs.first.size(); ++s) {
+      const int32_t n = qs.first[s + 1] - qs.first[s];
+      few = few && n <= 1;
+      reach.insert(reach.end(), size_t(n), sight.reach(s));
+    }
+    b->reach.upload(reach.data(), reach.size() * sizeof(Reach));
+  }
   // samples with one query tile take the kernel whose waves share the queries,
   // those with enough rows the one of 64 rows a wave
   const int wide = wide_forward(at->DP, dtype_size(at->dtype)) ? kWideTiles : INT32_MAX;
   // workgroups at once: two a compute unit where registers and shared memory allow
   const int es = int(dtype_size(at->dtype)), two = 2 * kCus, one = kCus;
-  const int slots = at->DP * es <= 512 ? two : one;
+  const int slots = forward_slots(at);
+  // samples of a tile at most, which mostly hold less than 32 rows: their rows go
+  // against the shared rows together
+  if (shared > 0 && few && b->qtiles > (b->nq * at->G + 31) / 32) build_joint(b->joint, at, b->nq, b->shared_tiles);
+  const bool joint = b->joint.per > 0;
   const auto forward = [&](WorkList& w, int per, int slots, int min_len, auto&& take) {
     std::vector<Unit> u;
-    add_units(u, qs, ks, 0, per, 1, {0}, take);
-    build(w, u, per, g, slots, min_len);
+    if (b->sequence)
+      add_query_units(u, sight, per, 1, 0, joint, take);
+    else
+      add_units(u, qs, ks, 0, per, 1, {0}, take);
+    build(w, u, per, g, slots, min_len, joint);
   };
   forward(b->fwd, 4, slots, 4, [&](int n) { return n > 1 && n < wide; });
   forward(b->wide, 8, two, 4, [&](int n) { return n >= wide; });
   forward(b->few, 1, slots, 8, [](int n) { return n == 1; });
   std::vector<Unit> u;
   const auto all = [](int) { return true; };
-  add_units(u, qs, ks, 0, 4, 3, {kItemQ}, all);
-  if (one_pass(at->DP, dtype_size(at->dtype)))
-    add_units(u, ks, qs, 1, 4, 4, {kItemV}, all);
-  else
-    add_units(u, ks, qs, 1, 4, 3, {kItemV, kItemK}, all);
+  const bool one_kind = one_pass(at->DP, dtype_size(at->dtype));
+  const std::vector<int32_t> kinds = one_kind ? std::vector<int32_t>{kItemV} : std::vector<int32_t>{kItemV, kItemK};
+  if (b->sequence) {
+    add_query_units(u, sight, 4, 3, kItemQ, false, all);
+    add_key_units(u, sight, 4, one_kind ? 4 : 3, kinds);
+  } else {
+    add_units(u, qs, ks, 0, 4, 3, {kItemQ}, all);
+    add_units(u, ks, qs, 1, 4, one_kind ? 4 : 3, kinds, all);
+  }
   build(b->bwd, u, 4, g, at->DP * es <= 384 ? two : one, 4);
   return b.release();
+}
+
+cgtp_attn_cache_s* build_attn_cache(cgtp_attn_s* at, int64_t slots, int64_t capacity, int64_t shared) {
+  auto c = std::make_unique<cgtp_attn_cache_s>();
+  c->attn = at;
+  c->slots = slots;
+  c->capacity = capacity;
+  c->shared = shared;
+  c->device = current_device();
+  if (capacity > INT32_MAX - 64 || slots > INT32_MAX || shared > INT32_MAX - 64)
+    throw Error{CGTP_ERR_UNSUPPORTED, "attention cache: more than 2^31 rows"};
+  std::vector<int64_t> ptr;
+  if (slots * at->G > INT32_MAX - 64) throw Error{CGTP_ERR_UNSUPPORTED, "attention: rows x heads beyond 2^31"};
+  for (int64_t s = 0; s <= slots; ++s) ptr.push_back(s);
+  const Side qs = cut(ptr, at->G);
+  c->qtiles = int64_t(qs.tiles.size());
+  c->tiles_a_slot = (at->G + 31) / 32;
+  // neighbouring heads on the waves of a workgroup; where there are less than three, a
+  // head's waves share the places
+  c->heads_a_group = std::min(4, at->kv_heads);
+  c->waves_a_head = 4 / c->heads_a_group;
+  c->bundles = (at->kv_heads + c->heads_a_group - 1) / c->heads_a_group;
+  const int64_t tiles = (capacity + 31) / 32, groups = c->qtiles * c->bundles;
+  c->min_tiles = 4;
+  const int64_t fill = std::max<int64_t>(1, 4 * 2 * kCus / std::max<int64_t>(1, groups));
+  const int64_t useful = (tiles + c->min_tiles * c->waves_a_head - 1) / (c->min_tiles * c->waves_a_head);
+  c->splits = int(std::max<int64_t>(1, std::min({fill, useful, int64_t(64)})));
+  c->parts = c->splits * c->waves_a_head;
+  need_launch((c->qtiles * c->splits + 7) / 8 * 8 * c->bundles);
+  if (c->qtiles * at->kv_heads * c->parts > INT32_MAX / 32)
+    throw Error{CGTP_ERR_UNSUPPORTED, "attention: too many partial tiles"};
+  std::vector<Join> joins;
+  for (int64_t t = 0; t < c->qtiles; ++t)
+    for (int hk = 0; hk < at->kv_heads; ++hk)
+      joins.push_back({int32_t(t), hk, int32_t((t * at->kv_heads + hk) * c->parts), c->parts, 1, 0, 0, 0});
+  need_launch(int64_t(joins.size()));
+  c->joins = int(joins.size());
+  c->qtile_mem.upload(qs.tiles.data(), qs.tiles.size() * sizeof(Tile));
+  c->join_mem.upload(joins.data(), joins.size() * sizeof(Join));
+  if (shared > 0) {
+    const Side ks = cut({0}, 1, shared);
+    c->shared_tiles = int64_t(ks.tiles.size());
+    need_launch((c->shared_tiles + 7) / 8 * 8 * at->kv_heads);
+    c->shared_tile_mem.upload(ks.tiles.data(), ks.tiles.size() * sizeof(Tile));
+    build_joint(c->joint, at, slots, c->shared_tiles);
+  }
+  return c.release();
 }
 
 size_t attn_context_bytes(const cgtp_attn_batch_s* b) { return carve_context(b, nullptr).bytes; }
 
 size_t attn_forward_ws_bytes(const cgtp_attn_batch_s* b, bool packed) {
+  if (b->joint.per)
+    return carve_row_parts(nullptr, b->few.part_tiles[0], b->joint.list.part_tiles[0], b->attn->DP).bytes +
+           (packed ? 0 : attn_context_bytes(b));
   const size_t part = size_t(fwd_part_tiles(b)) * 32 * (size_t(b->attn->DP) + 4) * 4;
   return up16(part) + (packed ? 0 : attn_context_bytes(b));
 }
@@ -378,8 +569,8 @@ bool quad_rows(const cgtp_attn_s* a, const void* p) {
   return a->quad && aligned(p, 4 * dtype_size(a->dtype));
 }
 
-PackArgs context_pack(const cgtp_attn_batch_s* b, RowsIn k, RowsIn v, const uint8_t* mask) {
-  const cgtp_attn_s* a = b->attn;
+PackArgs context_pack(const cgtp_attn_s* a, const DevMem& tiles, int64_t ktiles, RowsIn k, RowsIn v,
+                      const uint8_t* mask) {
   PackArgs p{};
   p.t[0].src = k.p;
   p.t[0].ld = k.ld;
@@ -387,8 +578,8 @@ PackArgs context_pack(const cgtp_attn_batch_s* b, RowsIn k, RowsIn v, const uint
   p.t[1].src = v.p;
   p.t[1].ld = v.ld;
   p.t[1].vec = vec_rows(a, v.p, v.ld);
-  p.tiles = b->ktile_mem.as<Tile>();
-  p.ntiles = int(b->ktiles);
+  p.tiles = tiles.as<Tile>();
+  p.ntiles = int(ktiles);
   p.table = a->table.as<int4>();
   p.size = a->D;
   p.mask = mask;
@@ -397,56 +588,100 @@ PackArgs context_pack(const cgtp_attn_batch_s* b, RowsIn k, RowsIn v, const uint
   return p;
 }
 
-}  // namespace
-
-void attn_pack_launch(const cgtp_attn_batch_s* b, RowsIn k, RowsIn v, const uint8_t* mask, void* context,
-                      hipStream_t s) {
-  if (b->ktiles == 0) return;
-  const Context c = carve_context(b, context);
-  PackArgs p = context_pack(b, k, v, mask);
+// Packs the context's keys and values for the forward.
+void pack_forward(const cgtp_attn_s* a, const DevMem& tiles, int64_t ktiles, RowsIn k, RowsIn v, const uint8_t* mask,
+                  const Context& c, hipStream_t s) {
+  PackArgs p = context_pack(a, tiles, ktiles, k, v, mask);
   p.t[0].row_frags = c.kf;
   p.bias = c.bias;
   p.flags = c.flags;
   p.norms = c.norms;
   p.t[1].col_frags = c.vf;
-  b->attn->k.pack(p, s);
+  a->k.pack(p, s);
   CGTP_CHECK_HIP(hipGetLastError());
 }
 
-void attn_forward_launch(const cgtp_attn_batch_s* b, RowsIn q, const void* context, double scale, void* out,
-                         float* lse, void* ws, hipStream_t s) {
-  const cgtp_attn_s* a = b->attn;
-  const Context c = carve_context(b, const_cast<void*>(context));
+FwdArgs forward_args(const cgtp_attn_s* a, RowsIn q, double scale, void* out, float* lse) {
   FwdArgs f{};
-  f.qtiles = b->qtile_mem.as<Tile>();
   f.table = a->table.as<int4>();
   f.q = q.p;
   f.ldq = q.ld;
   f.q_vec = vec_rows(a, q.p, q.ld);
-  f.kf = c.kf;
-  f.vf = c.vf;
-  f.bias = c.bias;
-  f.flags = c.flags;
-  f.norms = c.norms;
   f.out = out;
   f.ldo = a->qrow.dim;
   f.out_quad = quad_rows(a, out);
   f.lse = lse;
-  f.part_ml = static_cast<float4*>(ws);
-  f.part = reinterpret_cast<float*>(f.part_ml + size_t(fwd_part_tiles(b)) * 32);
   // a zero scale stays a small positive one: every score is then 0 all the same
   f.scale2 = std::max(float(std::fabs(scale) * 1.4426950408889634), 1e-37f);
   f.q_sign = scale < 0.0 ? (a->dtype == CGTP_BF16 ? 0x80008000u : 0x80000000u) : 0u;
   f.G = a->G;
   f.heads = a->heads;
   f.groups = a->kv_heads;
+  return f;
+}
+
+void use_context(FwdArgs& f, const Context& c) {
+  f.kf = c.kf;
+  f.vf = c.vf;
+  f.bias = c.bias;
+  f.flags = c.flags;
+  f.norms = c.norms;
+}
+
+// All rows against the shared ones, as parts.
+void joint_launch(const cgtp_attn_s* a, const JointPlan& j, FwdArgs f, const RowParts& w, hipStream_t s) {
+  f.qtiles = j.tiles.as<Tile>();
+  f.items = j.list.item_mem.as<Item>();
+  f.part = w.joint;
+  f.part_ml = w.joint_ml;
+  a->k.fwd(f, j.list.items, j.per, s);
+  CGTP_CHECK_HIP(hipGetLastError());
+}
+
+void rows_join_launch(const cgtp_attn_s* a, const JointPlan& j, const FwdArgs& own, const RowParts& w, int joins,
+                      const int32_t* lengths, int64_t capacity, hipStream_t s) {
+  const RowsJoinArgs r{own, w.joint, w.joint_ml, j.units, j.per, j.per ? j.parts : 0, lengths, int(capacity)};
+  a->seq.rows_join(r, joins, s);
+  CGTP_CHECK_HIP(hipGetLastError());
+}
+
+}  // namespace
+
+void attn_pack_launch(const cgtp_attn_batch_s* b, RowsIn k, RowsIn v, const uint8_t* mask, void* context,
+                      hipStream_t s) {
+  if (b->ktiles) pack_forward(b->attn, b->ktile_mem, b->ktiles, k, v, mask, carve_context(b, context), s);
+}
+
+void attn_forward_launch(const cgtp_attn_batch_s* b, RowsIn q, const void* context, double scale, void* out,
+                         float* lse, void* ws, hipStream_t s) {
+  const cgtp_attn_s* a = b->attn;
+  FwdArgs f = forward_args(a, q, scale, out, lse);
+  use_context(f, carve_context(b, const_cast<void*>(context)));
+  f.qtiles = b->qtile_mem.as<Tile>();
+  f.reach = b->reach.as<Reach>();
+  f.shared = int(b->shared_tiles);
+  f.causal = b->causal;
+  if (b->joint.per) {
+    const RowParts w = carve_row_parts(ws, b->few.part_tiles[0], b->joint.list.part_tiles[0], a->DP);
+    joint_launch(a, b->joint, f, w, s);
+    f.items = b->few.item_mem.as<Item>();
+    f.joins = b->few.join_mem[0].as<Join>();
+    f.part = w.own;
+    f.part_ml = w.own_ml;
+    a->seq.fwd(f, b->few.items, 1, s);
+    CGTP_CHECK_HIP(hipGetLastError());
+    rows_join_launch(a, b->joint, f, w, b->few.joins[0], nullptr, 0, s);
+    return;
+  }
+  f.part_ml = static_cast<float4*>(ws);
+  f.part = reinterpret_cast<float*>(f.part_ml + size_t(fwd_part_tiles(b)) * 32);
   // the lists share the partial buffers: each is joined before the next starts
   for (const int tiles : {8, 4, 1}) {
     const WorkList& w = tiles == 8 ? b->wide : tiles == 4 ? b->fwd : b->few;
     if (w.items == 0) continue;
     f.items = w.item_mem.as<Item>();
     f.joins = w.join_mem[0].as<Join>();
-    a->k.fwd(f, w.items, tiles, s);
+    (b->sequence ? a->seq.fwd : a->k.fwd)(f, w.items, tiles, s);
     CGTP_CHECK_HIP(hipGetLastError());
     if (w.joins[0]) {
       a->k.fwd_join(f, w.joins[0], s);
@@ -455,13 +690,77 @@ void attn_forward_launch(const cgtp_attn_batch_s* b, RowsIn q, const void* conte
   }
 }
 
+size_t attn_cache_shared_bytes(const cgtp_attn_cache_s* c) {
+  return carve_context(c->attn, c->shared_tiles, nullptr).bytes;
+}
+
+namespace {
+// tiles of partial results of a step against the caches (0: rows are final)
+bool step_whole(const cgtp_attn_cache_s* c) { return c->parts == 1 && c->joint.per == 0; }
+int64_t step_part_tiles(const cgtp_attn_cache_s* c) {
+  return step_whole(c) ? 0 : c->qtiles * c->attn->kv_heads * c->parts;
+}
+RowParts carve_step(const cgtp_attn_cache_s* c, void* ws) {
+  return carve_row_parts(ws, step_part_tiles(c), c->joint.list.part_tiles[0], c->attn->DP);
+}
+}  // namespace
+
+size_t attn_step_ws_bytes(const cgtp_attn_cache_s* c) { return carve_step(c, nullptr).bytes; }
+
+void attn_share_launch(const cgtp_attn_cache_s* c, RowsIn k, RowsIn v, const uint8_t* mask, void* context,
+                       hipStream_t s) {
+  if (c->shared_tiles)
+    pack_forward(c->attn, c->shared_tile_mem, c->shared_tiles, k, v, mask,
+                 carve_context(c->attn, c->shared_tiles, context), s);
+}
+
+void attn_step_launch(const cgtp_attn_cache_s* c, RowsIn q, RowsIn k, RowsIn v, void* k_cache, void* v_cache,
+                      const int32_t* lengths, const void* context, double scale, void* out, float* lse, void* ws,
+                      hipStream_t s) {
+  const cgtp_attn_s* a = c->attn;
+  const RowParts w = carve_step(c, ws);
+  FwdArgs f = forward_args(a, q, scale, out, lse);
+  if (c->joint.per) {
+    use_context(f, carve_context(a, c->shared_tiles, const_cast<void*>(context)));
+    joint_launch(a, c->joint, f, w, s);
+  }
+  f.qtiles = c->qtile_mem.as<Tile>();
+  f.joins = c->join_mem.as<Join>();
+  f.part = w.own;
+  f.part_ml = w.own_ml;
+  StepArgs x{};
+  x.f = f;
+  x.k_new = k.p;
+  x.v_new = v.p;
+  x.ldk = k.ld;
+  x.ldv = v.ld;
+  x.k_cache = k_cache;
+  x.v_cache = v_cache;
+  x.lengths = lengths;
+  x.dim = a->krow.dim;
+  x.slots = int(c->slots);
+  x.capacity = int(c->capacity);
+  x.size = a->D;
+  x.splits = c->splits;
+  x.waves_a_head = c->waves_a_head;
+  x.heads_a_group = c->heads_a_group;
+  x.bundles = c->bundles;
+  x.tiles_a_slot = c->tiles_a_slot;
+  x.min_tiles = c->min_tiles;
+  x.whole = step_whole(c);
+  x.vec = vec_rows(a, k.p, k.ld) && vec_rows(a, v.p, v.ld) && vec_rows(a, k_cache, x.dim) && vec_rows(a, v_cache, x.dim);
+  a->seq.step(x, s);
+  CGTP_CHECK_HIP(hipGetLastError());
+  if (!x.whole) rows_join_launch(a, c->joint, f, w, c->joins, lengths, c->capacity, s);
+}
+
 void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn v, const uint8_t* mask, double scale,
                           const void* out, const float* lse, RowsIn g, void* dq, void* dk, void* dv, void* ws,
                           hipStream_t s) {
   const cgtp_attn_s* a = b->attn;
   const Backward w = carve_backward(b, ws);
   if (b->ktiles) {
-    PackArgs p = context_pack(b, k, v, mask);
+    PackArgs p = context_pack(a, b->ktile_mem, b->ktiles, k, v, mask);
     p.t[0].row_frags = w.kforms + kKRows * w.kbytes;
     p.t[0].col_frags = dq ? w.kforms + kKCols * w.kbytes : nullptr;
     p.bias = w.bias;
@@ -507,6 +806,9 @@ void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn
   x.qstride = int64_t(w.qbytes / dtype_size(a->dtype));
   x.bias = w.bias;
   x.rows = w.rows;
+  x.reach = b->reach.as<Reach>();
+  x.shared = int(b->shared_tiles);
+  x.causal = b->causal;
   x.dq = dq;
   x.dk = dk;
   x.dv = dv;
@@ -525,7 +827,7 @@ void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn
   const WorkList& l = b->bwd;
   if (l.items == 0) return;
   x.items = l.item_mem.as<Item>();
-  a->k.bwd(x, l.items, s);
+  (b->sequence ? a->seq.bwd : a->k.bwd)(x, l.items, s);
   CGTP_CHECK_HIP(hipGetLastError());
   if (dq && l.joins[0]) {
     const GradJoinArgs j{l.join_mem[0].as<Join>(), x.qtiles, x.table, w.part_q, nullptr, dq, nullptr, x.ldq, a->G,

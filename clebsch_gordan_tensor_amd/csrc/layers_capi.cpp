@@ -78,10 +78,14 @@ void need_rows(int64_t rows, const void* p, int64_t ld, int64_t dim, const char*
   if (rows > 0 && !p) throw Error{CGTP_ERR_INVALID_ARG, std::string(name) + " is NULL"};
 }
 
-void need_batch(const cgtp_attn_batch_s* b, double scale) {
-  need(b != nullptr, "batch is NULL");
+void need_scale(double scale) {
   // as the kernels hold it, times log2 e in 32 bits: 0 * inf would make NaN of scores of 0
   need(std::isfinite(float(scale * 1.4426950408889634)), "scale must be finite in 32 bits");
+}
+
+void need_batch(const cgtp_attn_batch_s* b, double scale) {
+  need(b != nullptr, "batch is NULL");
+  need_scale(scale);
   need_device(b->device, "the batch");
 }
 
@@ -323,7 +327,20 @@ cgtp_status cgtp_attn_batch_create(cgtp_attn attn, cgtp_samples queries, cgtp_sa
     *out = nullptr;
     need(attn != nullptr && queries != nullptr && context != nullptr, "NULL handle");
     need_device(attn->device, "the attention");
-    *out = build_attn_batch(attn, queries, context);
+    *out = build_attn_batch(attn, queries, context, false, 0);
+  });
+}
+
+cgtp_status cgtp_attn_batch_create_seq(cgtp_attn attn, cgtp_samples queries, cgtp_samples context, int causal,
+                                       int64_t shared, cgtp_attn_batch* out) {
+  return guarded([&] {
+    need(out != nullptr, "out handle is NULL");
+    *out = nullptr;
+    need(attn != nullptr && queries != nullptr && context != nullptr, "NULL handle");
+    need(shared >= 0, "shared < 0");
+    need_device(attn->device, "the attention");
+    if (shared > INT32_MAX) throw Error{CGTP_ERR_UNSUPPORTED, "attention: more than 2^31 shared rows"};
+    *out = build_attn_batch(attn, queries, context, causal != 0, shared);
   });
 }
 
@@ -402,6 +419,63 @@ cgtp_status cgtp_attn_backward(cgtp_attn_batch batch, const void* q, int64_t ldq
     need_ws(ws, ws_bytes, attn_backward_ws_bytes(batch), "attention backward");
     attn_backward_launch(batch, {q, ldq}, {k, ldk}, {v, ldv}, key_mask, scale, out, lse, {grad_out, ldg}, grad_q,
                          grad_k, grad_v, ws, as_stream(stream));
+  });
+}
+
+cgtp_status cgtp_attn_cache_create(cgtp_attn attn, int64_t slots, int64_t capacity, int64_t shared,
+                                   cgtp_attn_cache* out) {
+  return guarded([&] {
+    need(out != nullptr, "out handle is NULL");
+    *out = nullptr;
+    need(attn != nullptr, "attn is NULL");
+    need(slots >= 0 && capacity >= 1 && shared >= 0, "slots < 0, capacity < 1 or shared < 0");
+    need_device(attn->device, "the attention");
+    *out = build_attn_cache(attn, slots, capacity, shared);
+  });
+}
+
+cgtp_status cgtp_attn_cache_destroy(cgtp_attn_cache cache) {
+  return guarded([&] { delete cache; });
+}
+
+cgtp_status cgtp_attn_cache_query(cgtp_attn_cache cache, size_t* shared_bytes, size_t* ws_bytes) {
+  return guarded([&] {
+    need(cache != nullptr, "cache is NULL");
+    if (shared_bytes) *shared_bytes = attn_cache_shared_bytes(cache);
+    if (ws_bytes) *ws_bytes = attn_step_ws_bytes(cache);
+  });
+}
+
+cgtp_status cgtp_attn_cache_share(cgtp_attn_cache cache, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                  const uint8_t* key_mask, void* context, size_t context_bytes, void* stream) {
+  return guarded([&] {
+    need(cache != nullptr, "cache is NULL");
+    need_device(cache->device, "the cache");
+    need_rows(cache->shared, k, ldk, cache->attn->krow.dim, "k");
+    need_rows(cache->shared, v, ldv, cache->attn->krow.dim, "v");
+    need_ws(context, context_bytes, attn_cache_shared_bytes(cache), "the packed shared rows");
+    attn_share_launch(cache, {k, ldk}, {v, ldv}, key_mask, context, as_stream(stream));
+  });
+}
+
+cgtp_status cgtp_attn_step(cgtp_attn_cache cache, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                           const void* v, int64_t ldv, void* k_cache, void* v_cache, const int32_t* lengths,
+                           const void* context, size_t context_bytes, double scale, void* out, float* lse, void* ws,
+                           size_t ws_bytes, void* stream) {
+  return guarded([&] {
+    need(cache != nullptr, "cache is NULL");
+    need_scale(scale);
+    need_device(cache->device, "the cache");
+    const cgtp_attn_s* a = cache->attn;
+    need_rows(cache->slots, q, ldq, a->qrow.dim, "q");
+    need_rows(cache->slots, k, ldk, a->krow.dim, "k");
+    need_rows(cache->slots, v, ldv, a->krow.dim, "v");
+    if (cache->slots == 0) return;
+    need(k_cache && v_cache && lengths && out, "NULL cache, lengths or out");
+    need_ws(const_cast<void*>(context), context_bytes, attn_cache_shared_bytes(cache), "the packed shared rows");
+    need_ws(ws, ws_bytes, attn_step_ws_bytes(cache), "attention step");
+    attn_step_launch(cache, {q, ldq}, {k, ldk}, {v, ldv}, k_cache, v_cache, lengths, context, scale, out, lse, ws,
+                     as_stream(stream));
   });
 }
 

@@ -36,6 +36,7 @@ _SIGS = {
     "cgtp_attn_destroy": [_vp],
     "cgtp_attn_query": [_vp, _i64p, _i64p, _i64p],
     "cgtp_attn_batch_create": [_vp, _vp, _vp, _vpp],
+    "cgtp_attn_batch_create_seq": [_vp, _vp, _vp, ctypes.c_int, _i64, _vpp],
     "cgtp_attn_batch_destroy": [_vp],
     "cgtp_attn_workspace_size": [_vp, ctypes.c_int, _sizep],
     "cgtp_attn_forward": [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _dbl, _vp, _vp, _vp, _size, _vp],
@@ -43,6 +44,11 @@ _SIGS = {
     "cgtp_attn_forward_packed": [_vp, _vp, _i64, _vp, _size, _dbl, _vp, _vp, _vp, _size, _vp],
     "cgtp_attn_backward": [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _dbl, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp,
                            _size, _vp],
+    "cgtp_attn_cache_create": [_vp, _i64, _i64, _i64, _vpp],
+    "cgtp_attn_cache_destroy": [_vp],
+    "cgtp_attn_cache_query": [_vp, _sizep, _sizep],
+    "cgtp_attn_cache_share": [_vp, _vp, _i64, _vp, _i64, _vp, _vp, _size, _vp],
+    "cgtp_attn_step": [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _size, _dbl, _vp, _vp, _vp, _size, _vp],
 }
 for _name, _args in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -251,14 +257,21 @@ ATTN_FORWARD, ATTN_BACKWARD, ATTN_CONTEXT, ATTN_FORWARD_PACKED = 1, 2, 3, 4
 
 
 class AttentionBatch(_Handle):
-    """The work lists of one pair of sample layouts (cgtp_attn_batch_create);
-    made by CrossAttention.batch, reusable for every call on these layouts."""
+    """The work lists of one pair of sample layouts (cgtp_attn_batch_create,
+    cgtp_attn_batch_create_seq); made by CrossAttention.batch, reusable for every call
+    on these layouts. ``nk`` counts the shared rows too."""
 
-    def __init__(self, attn, queries, context):
-        self.attn, self.nq, self.nk = attn, queries.rows, context.rows     # attn outlives the handle
+    def __init__(self, attn, queries, context, causal=False, shared=0):
+        shared = int(shared)
+        self.attn, self.nq, self.nk = attn, queries.rows, shared + context.rows     # attn outlives the handle
+        self.causal, self.shared = bool(causal), shared
         h = _vp()
-        _check(_lib.cgtp_attn_batch_create(attn._h, queries._h, context._h, ctypes.byref(h)),
-               "cgtp_attn_batch_create")
+        if causal or shared:
+            _check(_lib.cgtp_attn_batch_create_seq(attn._h, queries._h, context._h, 1 if causal else 0, shared,
+                                                   ctypes.byref(h)), "cgtp_attn_batch_create_seq")
+        else:
+            _check(_lib.cgtp_attn_batch_create(attn._h, queries._h, context._h, ctypes.byref(h)),
+                   "cgtp_attn_batch_create")
         self._own(h, "cgtp_attn_batch_destroy")
         self._sizes = {}
 
@@ -270,11 +283,46 @@ class AttentionBatch(_Handle):
         return self._sizes[op]
 
 
+class AttentionCache(_Handle):
+    """Keys and values of ``slots`` sequences for CrossAttention.step
+    (cgtp_attn_cache_create); made by CrossAttention.cache. ``k`` and ``v`` are
+    ordinary tensors of irreps rows [slots, capacity, dim_kv], to be filled with a
+    prompt's rows, copied or cut like any other."""
+
+    def __init__(self, attn, slots, capacity, shared=0, device="cuda"):
+        torch = _torch()
+        self.attn, self.slots, self.capacity, self.shared = attn, int(slots), int(capacity), int(shared)
+        h = _vp()
+        _check(_lib.cgtp_attn_cache_create(attn._h, self.slots, self.capacity, self.shared, ctypes.byref(h)),
+               "cgtp_attn_cache_create")
+        self._own(h, "cgtp_attn_cache_destroy")
+        sizes = _size(), _size()
+        _check(_lib.cgtp_attn_cache_query(h, ctypes.byref(sizes[0]), ctypes.byref(sizes[1])), "cgtp_attn_cache_query")
+        self._context_bytes, self.workspace_size = sizes[0].value, sizes[1].value
+        shape = (self.slots, self.capacity, attn.dim_kv)
+        self.k = torch.zeros(shape, dtype=attn.torch_dtype, device=device)
+        self.v = torch.zeros(shape, dtype=attn.torch_dtype, device=device)
+        self._context = None
+
+    def share(self, k, v, key_mask=None):
+        """Lays out the rows that all sequences see before their own (cgtp_attn_cache_share)."""
+        a = self.attn
+        pk, ldk = a._rows(k, self.shared, a.dim_kv, "k")
+        pv, ldv = a._rows(v, self.shared, a.dim_kv, "v")
+        mask = a._mask(key_mask, self.shared)
+        if self._context is None:
+            self._context = _torch().empty(max(self._context_bytes, 16), dtype=_torch().uint8, device=self.k.device)
+        _check(_lib.cgtp_attn_cache_share(self._h, pk, ldk, pv, ldv, mask, self._context.data_ptr(),
+                                          _ws_bytes(self._context), _stream_of(self.k)), "cgtp_attn_cache_share")
+
+
 class CrossAttention(_Handle):
     """Attention of irreps rows to a context of another length, sample by sample
     (cgtp_attn_create). ``irreps`` are the queries'; the context's have
     multiplicities kv_heads / heads as large (``dim_kv`` elements a row). q, k, v
-    and grad_out may be slices of wider rows (unit stride within a row)."""
+    and grad_out may be slices of wider rows (unit stride within a row). With a causal
+    batch whose context is the queries' own samples it is the self attention of
+    sequences; ``cache`` and ``step`` continue them token by token."""
 
     def __init__(self, irreps, heads, kv_heads=None, dtype="f32"):
         self.irreps, self.heads = irreps, int(heads)
@@ -289,8 +337,15 @@ class CrossAttention(_Handle):
         self.dim_q, self.dim_kv, self.head_dim = (a.value for a in v)
         self.scale = self.head_dim ** -0.5
 
-    def batch(self, queries, context):
-        return AttentionBatch(self, queries, context)
+    def batch(self, queries, context, causal=False, shared=0):
+        """``causal``: a query sees its sample's keys up to its own place, counted from
+        the end. ``shared``: the first rows of k and v, before the samples' own, are seen
+        by every sample (k and v have shared + context.rows rows)."""
+        return AttentionBatch(self, queries, context, causal, shared)
+
+    def cache(self, slots, capacity, shared=0, device="cuda"):
+        """Caches of ``slots`` sequences for ``step``; ``shared`` rows come before all of them."""
+        return AttentionCache(self, slots, capacity, shared, device)
 
     def _rows(self, t, rows, dim, name):
         """(pointer, row stride) of rows with unit stride inside a row."""
@@ -391,3 +446,33 @@ class CrossAttention(_Handle):
                                        self.scale if scale is None else float(scale), po, pl, pg, ldg, pr[0], pr[1],
                                        pr[2], pws, nws, _stream_of(q)), "cgtp_attn_backward")
         return tuple(res)
+
+    def step(self, cache, q, k, v, lengths, scale=None, need_lse=False, out=None, lse=None, ws=None):
+        """out, or (out, lse): one token of every slot, put at place lengths[s] of the caches
+        and attending to the shared rows and its slot's places 0 .. lengths[s]
+        (cgtp_attn_step). ``lengths`` (int32, on the device) is not changed; a slot whose
+        length is not in 0 .. capacity - 1 takes no part."""
+        torch = _torch()
+        if cache.attn is not self:
+            raise ValueError("the cache belongs to another CrossAttention")
+        n, dt = cache.slots, self.torch_dtype
+        if cache.shared and cache._context is None:
+            raise ValueError("the cache's shared rows have not been laid out (share)")
+        pq, ldq = self._rows(q, n, self.dim_q, "q")
+        pk, ldk = self._rows(k, n, self.dim_kv, "k")
+        pv, ldv = self._rows(v, n, self.dim_kv, "v")
+        shape = (n, cache.capacity, self.dim_kv)
+        ck, cv = _tensor(cache.k, shape, dt, "cache.k"), _tensor(cache.v, shape, dt, "cache.v")
+        pn = _tensor(lengths, (n,), torch.int32, "lengths")
+        if out is None:
+            out = torch.empty((n, self.dim_q), dtype=dt, device=q.device)
+        if need_lse and lse is None:
+            lse = torch.empty((n, self.heads), dtype=torch.float32, device=q.device)
+        po = _tensor(out, (n, self.dim_q), dt, "out")
+        pl = None if lse is None else _tensor(lse, (n, self.heads), torch.float32, "lse")
+        ws, pws, nws = _ws(ws, cache.workspace_size, q.device)
+        shared = (None, 0) if not cache.shared else (cache._context.data_ptr(), _ws_bytes(cache._context))
+        _check(_lib.cgtp_attn_step(cache._h, pq, ldq, pk, ldk, pv, ldv, ck, cv, pn, shared[0], shared[1],
+                                   self.scale if scale is None else float(scale), po, pl, pws, nws, _stream_of(q)),
+               "cgtp_attn_step")
+        return (out, lse) if need_lse else out

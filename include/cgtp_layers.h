@@ -1,6 +1,7 @@
 /* cgtp_layers.h - the layers between equivariant convolutions and linear maps,
  * on irreps rows, for AMD Instinct MI355X (gfx950): group norm with its
- * activation, cross attention to a context of another length, and dropout.
+ * activation, attention to a context of another length (whole, causal, with rows
+ * that all samples share, by single tokens on a cache), and dropout.
  *
  * Conventions are those of cgtp.h: rows are ir_mul blocks ([2l+1][mul], channel
  * index fastest) concatenated in irreps order; tensor arguments are DEVICE
@@ -28,6 +29,7 @@ typedef struct cgtp_norm_s* cgtp_norm;
 typedef struct cgtp_dropout_s* cgtp_dropout;
 typedef struct cgtp_attn_s* cgtp_attn;
 typedef struct cgtp_attn_batch_s* cgtp_attn_batch;
+typedef struct cgtp_attn_cache_s* cgtp_attn_cache;
 
 /* ------------------------------------------------------------------ samples */
 
@@ -136,6 +138,22 @@ cgtp_status cgtp_attn_query(cgtp_attn attn, int64_t* dim_q, int64_t* dim_kv, int
  * these layouts. Errors: INVALID_ARG, UNSUPPORTED (rows x heads beyond 2^31, or
  * tiles of 32 rows x kv_heads beyond 2^24; a sample of any rows has its own tiles). */
 cgtp_status cgtp_attn_batch_create(cgtp_attn attn, cgtp_samples queries, cgtp_samples context, cgtp_attn_batch* out);
+/* A batch along sequences, used with the same calls:
+ * shared > 0: the first `shared` rows of k and v (and of key_mask, grad_k and
+ *   grad_v) are seen by the queries of every sample, before the sample's own rows,
+ *   which follow them: k and v have shared + context rows. They are packed once, and
+ *   their gradients are the sums over all samples.
+ * causal != 0: query i of a sample with nq queries and nk own keys sees its own keys
+ *   0 .. i + nk - nq, i.e. the last query sees all and each earlier one a key less
+ *   (nk = nq: a whole prompt; nk > nq: its next rows after nk - nq earlier ones;
+ *   nk < nq: the first nq - nk queries see no own key). What later keys hold,
+ *   infinities and NaN included, does not reach out and lse of a query that does not
+ *   see them (but for their last bits: the kernels choose how scores are kept from
+ *   overflowing by the norms of 32-row tiles).
+ * Errors: as above, INVALID_ARG for shared < 0, UNSUPPORTED for shared + context rows
+ * beyond 2^31 or a causal batch beyond 2^30 rows. */
+cgtp_status cgtp_attn_batch_create_seq(cgtp_attn attn, cgtp_samples queries, cgtp_samples context, int causal,
+                                       int64_t shared, cgtp_attn_batch* out);
 cgtp_status cgtp_attn_batch_destroy(cgtp_attn_batch batch);
 
 typedef enum {
@@ -174,6 +192,36 @@ cgtp_status cgtp_attn_backward(cgtp_attn_batch batch, const void* q, int64_t ldq
                                const void* v, int64_t ldv, const uint8_t* key_mask, double scale, const void* out,
                                const float* lse, const void* grad_out, int64_t ldg, void* grad_q, void* grad_k,
                                void* grad_v, void* ws, size_t ws_bytes, void* stream);
+
+/* --------------------------------------------- single tokens on a cache
+ *
+ * Serving: `slots` sequences, each with a cache of `capacity` rows of keys and of
+ * values, ordinary irreps rows [slots][capacity][dim_kv] that the caller owns, fills
+ * (a prompt's rows), copies and cuts as any tensor; and optionally `shared` rows that
+ * all sequences see before their own (one document, one surrounding). Keeps copies
+ * of nothing but the layout: attn must outlive it. Host work and a synchronous upload.
+ * Errors: INVALID_ARG (slots or shared < 0, capacity < 1), UNSUPPORTED (slots x heads,
+ * capacity or shared beyond 2^31, or slots x kv_heads beyond 2^24). */
+cgtp_status cgtp_attn_cache_create(cgtp_attn attn, int64_t slots, int64_t capacity, int64_t shared,
+                                   cgtp_attn_cache* out);
+cgtp_status cgtp_attn_cache_destroy(cgtp_attn_cache cache);
+/* Bytes of the packed shared rows and of the workspace of a step. */
+cgtp_status cgtp_attn_cache_query(cgtp_attn_cache cache, size_t* shared_bytes, size_t* ws_bytes);
+/* Lay the shared rows out once, as cgtp_attn_pack (k, v: shared rows). */
+cgtp_status cgtp_attn_cache_share(cgtp_attn_cache cache, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                  const uint8_t* key_mask, void* context, size_t context_bytes, void* stream);
+/* One token of every slot s, with n = lengths[s] (DEVICE, int32) tokens in its cache:
+ *   k_cache[s][n] = k[s], v_cache[s][n] = v[s],
+ *   out[s] = attention of q[s] over the shared rows and places 0 .. n,
+ * lse as in cgtp_attn_forward. A slot whose length lies outside 0 .. capacity - 1
+ * (not in use, or full) takes no part: nothing of it is read or written, its out is 0
+ * and its lse -inf. Places behind n are not used, whatever they hold. lengths is only read: the caller counts
+ * on. Rows of q, k and v with strides as in cgtp_attn_forward (not rows of the caches); caches are contiguous.
+ * `context`: the packed shared rows (NULL where shared = 0). */
+cgtp_status cgtp_attn_step(cgtp_attn_cache cache, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                           const void* v, int64_t ldv, void* k_cache, void* v_cache, const int32_t* lengths,
+                           const void* context, size_t context_bytes, double scale, void* out, float* lse, void* ws,
+                           size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

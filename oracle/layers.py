@@ -166,3 +166,70 @@ def attn_backward(irreps, heads, kv_heads, qptr, kptr, q, k, v, mask, scale, g):
         dk[ki] += ds.T @ q[qi]
         dv[ki] += p.T @ g[qi]
     return dq, dk, dv
+
+
+def _seq_pairs(irreps, heads, kv_heads, qptr, kptr, mask, causal, shared):
+    """Per sample and head: rows, seen [rows, keys], head, indices into q and into k, v."""
+    kvi = kv_irreps(irreps, heads, kv_heads)
+    for s in range(len(qptr) - 1):
+        rows = np.arange(qptr[s], qptr[s + 1])
+        n, nq = kptr[s + 1] - kptr[s], len(rows)
+        keys = np.concatenate([np.arange(shared), shared + kptr[s] + np.arange(n)]).astype(int)
+        seen = np.ones((nq, len(keys)), bool)
+        if causal:
+            for i in range(nq):
+                seen[i, shared + max(0, min(n, i + n - nq + 1)):] = False
+        if mask is not None:
+            seen &= mask[keys] != 0
+        for h in range(heads):
+            yield rows, seen, h, np.ix_(rows, head_columns(irreps, heads, h)), \
+                np.ix_(keys, head_columns(kvi, kv_heads, h * kv_heads // heads))
+
+
+def seq_forward(irreps, heads, kv_heads, qptr, kptr, q, k, v, mask, scale, causal=False, shared=0):
+    """(out, lse) of queries that see the first `shared` rows of k and v and their own
+    sample's after them, causally or whole."""
+    out = np.zeros_like(q)
+    lse = np.full((q.shape[0], heads), -np.inf)
+    for rows, seen, h, qi, ki in _seq_pairs(irreps, heads, kv_heads, qptr, kptr, mask, causal, shared):
+        s = scale * (q[qi] @ k[ki].T)
+        for r, i in enumerate(rows):
+            at = np.flatnonzero(seen[r])
+            if not len(at):
+                continue
+            top = s[r, at].max()
+            e = np.exp(s[r, at] - top)
+            out[i, qi[1][0]] = e @ v[ki][at] / e.sum()
+            lse[i, h] = np.log(e.sum()) + top
+    return out, lse
+
+
+def seq_backward(irreps, heads, kv_heads, qptr, kptr, q, k, v, mask, scale, g, causal=False, shared=0):
+    dq, dk, dv = np.zeros_like(q), np.zeros_like(k), np.zeros_like(v)
+    out, lse = seq_forward(irreps, heads, kv_heads, qptr, kptr, q, k, v, mask, scale, causal, shared)
+    for rows, seen, h, qi, ki in _seq_pairs(irreps, heads, kv_heads, qptr, kptr, mask, causal, shared):
+        top = np.where(np.isinf(lse[rows, h]), 0.0, lse[rows, h])
+        p = np.where(seen, np.exp(np.where(seen, scale * (q[qi] @ k[ki].T), 0.0) - top[:, None]), 0.0)
+        ds = p * (g[qi] @ v[ki].T - (g[qi] * out[qi]).sum(1, keepdims=True)) * scale
+        dq[qi] += ds @ k[ki]
+        dk[ki] += ds.T @ q[qi]
+        dv[ki] += p.T @ g[qi]
+    return dq, dk, dv
+
+
+def cache_step(irreps, heads, kv_heads, q, k, v, k_cache, v_cache, lengths, scale, shared=None):
+    """(out, lse, k_cache, v_cache): a token of every slot put at its length; `shared`:
+    (keys, values, mask) of rows that all slots see first."""
+    k_cache, v_cache = k_cache.copy(), v_cache.copy()
+    out, lse = np.zeros_like(q), np.full((len(q), heads), -np.inf)
+    for s, n in enumerate(lengths):
+        if not 0 <= n < k_cache.shape[1]:
+            continue
+        k_cache[s, n], v_cache[s, n] = k[s], v[s]
+        keys, values, mask = k_cache[s, :n + 1], v_cache[s, :n + 1], np.ones(n + 1)
+        if shared is not None:
+            keys, values = np.concatenate([shared[0], keys]), np.concatenate([shared[1], values])
+            mask = np.concatenate([np.ones(len(shared[0])) if shared[2] is None else shared[2], mask])
+        o, l = attn_forward(irreps, heads, kv_heads, [0, 1], [0, len(keys)], q[s:s + 1], keys, values, mask, scale)
+        out[s], lse[s] = o[0], l[0]
+    return out, lse, k_cache, v_cache
