@@ -94,31 +94,51 @@ struct FwdArgs {
   bool causal;
 };
 
-// Joins the results of rows against their own context (`own`: the parts of its joins)
-// with those against rows that all samples share (parts of tiles of 32 consecutive
-// rows whatever their sample: unit u = per tiles, parts of unit u and context head hk
-// from slot (hk * units + u) * parts on).
+// How a step's places are shared out. A turn is a tile of 32 keys for each of the waves of a
+// head; the turns of all slots (those of a slot with several tiles of query rows one tile
+// after another) lie end to end, and workgroup i of `shares` takes the i-th stretch of
+// max(min_turns, turns / shares). Slots of any lengths so keep all workgroups busy alike.
+// Tile of rows e gets its results from consecutive workgroups, one part each, and part
+// (i, e) is number i + e: the pairs go along a staircase, so no two are alike.
+struct StepCut {
+  const int32_t* lengths;  // NULL: no step
+  int slots, capacity, tiles_a_slot, waves_a_head, shares, min_turns;
+};
+
+// Joins the results of rows against their own context (`own`: the parts of its joins, or
+// of a step) with those against rows that all samples share (parts of tiles of 32
+// consecutive rows whatever their sample: unit u = per tiles, parts of unit u and context
+// head hk from slot (hk * units + u) * parts on).
 struct RowsJoinArgs {
   FwdArgs own;
   const float* part;  // of the shared rows, with their references and sums
   const float4* part_ml;
   int units, per, parts;     // parts = 0: nothing is shared
-  const int32_t* lengths;    // or NULL: a token whose length is not below `capacity` sees nothing
-  int capacity;
+  StepCut cut;
+};
+
+// Waves of a step's workgroup: what its shared memory holds of their keys and values.
+constexpr int step_waves(int dp, size_t size) { return dp * int(size) <= 512 ? 4 : 2; }
+
+// 16 bytes of a context row: elements off + head * cw on, with the first head of the
+// workgroup for `head`, are elements d on of the workgroup's head j.
+struct alignas(16) StepPiece {
+  int32_t off, cw, j, d;
 };
 
 // One token a slot on caches of rows [slot][capacity][dim].
 struct StepArgs {
   FwdArgs f;
+  StepCut cut;
   const void *k_new, *v_new;
   int64_t ldk, ldv;
   void *k_cache, *v_cache;
-  const int32_t* lengths;
   int64_t dim;
-  int slots, capacity, size;  // size: elements of a head
-  int splits, waves_a_head, heads_a_group, bundles, tiles_a_slot;  // how the work is cut (StepPlan)
-  int min_tiles;
-  bool whole;  // a slot's tile and head is one part, and nothing is shared: rows are final
+  int size;                            // elements of a head
+  int heads_a_group, bundles, pieces;  // heads of a workgroup; workgroups of a row's heads; pieces of a row for them
+  const StepPiece* piece;
+  bool whole;   // a workgroup takes a whole tile of rows (no shares): rows are final
+  bool joined;  // rows are joined with those against shared rows: all results are parts
   bool vec;
 };
 
@@ -234,9 +254,10 @@ struct cgtp_attn_cache_s {
   cgtp_attn attn = nullptr;
   int64_t slots = 0, capacity = 0, shared = 0, shared_tiles = 0, qtiles = 0;
   int device = 0;
-  int splits = 1, waves_a_head = 1, heads_a_group = 1, bundles = 1, tiles_a_slot = 1, min_tiles = 1, parts = 1;
-  int joins = 0;
-  cgtp::DevMem qtile_mem, shared_tile_mem, join_mem;
+  int heads_a_group = 1, waves_a_head = 1, bundles = 1, tiles_a_slot = 1, shares = 1, min_turns = 1;
+  bool whole = false;
+  int joins = 0, pieces = 0;
+  cgtp::DevMem qtile_mem, shared_tile_mem, join_mem, piece_mem;
   cgtp::attn::JointPlan joint;
 };
 

@@ -557,15 +557,16 @@ constexpr int stage_units(int units) { return stage_buffers(units) * units; }
 // columns [grad_k].
 constexpr int dkv_forms(int part) { return part == 0 ? 4 : part == 1 ? 2 : 3; }
 
-// Writes a wave's result: final rows, or an unnormalised part of a split.
+// Writes a wave's result: final rows, or an unnormalised part of a split (of
+// `part_rows` rows a tile).
 template <typename T, int DP>
 __device__ __forceinline__ void finish(const FwdArgs& a, const Item& it, const Tile& tl, int tile_in_item,
-                                       const Running<DP / 32>& st, float exact_sum) {
+                                       const Running<DP / 32>& st, float exact_sum, int part_rows = 32) {
   const int lane = lane_id(), n = lane % 32, h = lane / 32;
   const float l = half_sum(st.l), e = sizeof(T) == 2 ? half_sum(exact_sum) : l;
   if (n >= tl.n) return;
   if (it.slot >= 0) {
-    const int64_t r = (int64_t(it.slot) * it.stride + tile_in_item) * 32 + n;
+    const int64_t r = (int64_t(it.slot) * it.stride + tile_in_item) * part_rows + n;
     float* o = a.part + r * DP;
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d)

@@ -136,11 +136,11 @@ int64_t parts_of(const Unit& x, int64_t cost) {
 
 // Largest cost of a part: of some candidates the one whose parts, the longest
 // first onto `slots` places, end earliest. An item costs its products plus about
-// two tiles' for its start and end, a part of a split one about three more for
-// its partial result and the join (measured: parts of a ragged batch cut to
-// twice the number cost as much as the better balance gained). Parts have at least
+// two tiles' for its start and end, a part of a split one `part_extra` for these, its
+// partial result and the join (5 of batches whose samples' queries all see the same
+// keys; measured: parts of a ragged batch cut to twice the number cost as much as the better balance gained). Parts have at least
 // min_len tiles, and batches with many more items than places are not split.
-int64_t part_cost(const std::vector<Unit>& u, int groups, int slots, int min_len) {
+int64_t part_cost(const std::vector<Unit>& u, int groups, int slots, int min_len, int part_extra) {
   int64_t longest = 1, count = 0;
   int weight = 1;
   for (const Unit& x : u) {
@@ -156,7 +156,7 @@ int64_t part_cost(const std::vector<Unit>& u, int groups, int slots, int min_len
     std::vector<int64_t> costs;
     for (const Unit& x : u) {
       const int64_t k = parts_of(x, cost), n = (x.b1 - x.b0 + k - 1) / k;
-      costs.insert(costs.end(), size_t(k) * size_t(groups) * x.kinds.size(), (n + (k > 1 ? 5 : 2)) * x.weight);
+      costs.insert(costs.end(), size_t(k) * size_t(groups) * x.kinds.size(), (n + (k > 1 ? part_extra : 2)) * x.weight);
     }
     if (parts > 1 && int64_t(costs.size()) > 16 * int64_t(slots)) break;
     std::sort(costs.begin(), costs.end(), std::greater<int64_t>());
@@ -192,14 +192,18 @@ void need_launch(int64_t workgroups) {
 // are given to one die and follow each other there, those with the longest items
 // first, so that the short ones fill the end; a group bigger than a die's share
 // goes round several.
-// With all_parts every result is a part, also that of an unsplit unit. Returns the
-// largest number of parts of a unit.
+// Returns the largest number of parts of a unit.
+struct How {
+  bool all_parts = false;  // every result is a part, also that of an unsplit unit
+  bool uneven = false;     // the items of a group differ in length (causal queries)
+  int part_extra = 5;      // of part_cost
+};
 int64_t build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, int slots, int min_len,
-              bool all_parts = false) {
+              const How& how = {}) {
   int64_t whole = 0;
   for (const Unit& x : u) whole += int64_t(x.kinds.size()) * groups;
   need_launch(whole);  // (before the lists are laid out)
-  const int64_t cost = part_cost(u, groups, slots, min_len);
+  const int64_t cost = part_cost(u, groups, slots, min_len, how.part_extra);
   struct Group {
     int64_t work = 0, longest = 0;
     std::vector<Item> items;
@@ -216,7 +220,7 @@ int64_t build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, i
       for (size_t k = i; k < j; ++k) {
         const Unit& x = u[k];
         const int64_t n = x.b1 - x.b0, parts = parts_of(x, cost);
-        const bool split = all_parts || parts > 1;
+        const bool split = how.all_parts || parts > 1;
         most = std::max(most, parts);
         int64_t& slot = nslot[x.side];
         for (size_t q = 0; q < g.size(); ++q)
@@ -239,10 +243,26 @@ int64_t build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, i
     i = j;
   }
 
+  // long and short items in turn, so that every run of them has alike shares of both, and
+  // then every die's longest first (long causal prompts 782 us without, 744 us with both)
+  if (how.uneven)
+    for (Group& g : gs) {
+      std::vector<size_t> by(g.items.size());
+      std::iota(by.begin(), by.end(), size_t(0));
+      std::stable_sort(by.begin(), by.end(), [&](size_t a, size_t b) { return g.costs[a] > g.costs[b]; });
+      Group mixed = g;
+      for (size_t k = 0; k < by.size(); ++k) {
+        const size_t from = k % 2 == 0 ? by[k / 2] : by[by.size() - 1 - k / 2];
+        mixed.items[k] = g.items[from];
+        mixed.costs[k] = g.costs[from];
+      }
+      g = std::move(mixed);
+    }
   int64_t total = 0;
   for (const Group& g : gs) total += g.work;
   const int64_t share = std::max<int64_t>(1, total / kXcds);
   std::vector<std::vector<Item>> queue(kXcds);
+  std::vector<std::vector<int64_t>> queue_costs(kXcds);
   std::vector<int64_t> load(kXcds, 0);
   std::vector<size_t> order(gs.size());
   std::iota(order.begin(), order.end(), size_t(0));
@@ -256,11 +276,21 @@ int64_t build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, i
       while (at < g.items.size() && room > 0) {
         const int64_t c = g.costs[at];
         queue[size_t(x)].push_back(g.items[at++]);
+        queue_costs[size_t(x)].push_back(c);
         load[size_t(x)] += c;
         room -= c;
       }
     }
   }
+  if (how.uneven)
+    for (size_t x = 0; x < size_t(kXcds); ++x) {
+      std::vector<size_t> by(queue[x].size());
+      std::iota(by.begin(), by.end(), size_t(0));
+      std::stable_sort(by.begin(), by.end(), [&](size_t a, size_t b) { return queue_costs[x][a] > queue_costs[x][b]; });
+      std::vector<Item> sorted;
+      for (size_t k : by) sorted.push_back(queue[x][k]);
+      queue[x] = std::move(sorted);
+    }
   size_t longest = 0;
   for (const auto& q : queue) longest = std::max(longest, q.size());
   std::vector<Item> items;
@@ -285,6 +315,14 @@ int64_t build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, i
 // memory allow.
 int forward_slots(const cgtp_attn_s* at) { return at->DP * int(dtype_size(at->dtype)) <= 512 ? 2 * kCus : kCus; }
 
+// A part's start, end, partial result and join in tiles of its keys, for sequence
+// batches. In bf16 the partial result of 128 or 256 rows (64 KB for every 32 columns of 128
+// rows, written and read) costs as much as some twenty tiles' products (us with 5, 12, 24: long
+// causal prompts 744, 679, 677; a chunk after earlier rows 202, 202, 154; prompts with a shared
+// beginning 335, 335, 318); products in fp32 take eight times as long, and the rows of one
+// tile are few.
+int part_extra(const cgtp_attn_s* at, int per) { return dtype_size(at->dtype) == 2 && per > 1 ? 24 : 5; }
+
 // The rows of `tokens` tokens in tiles whatever their sample, against shared_tiles key
 // tiles. All units see the same tiles, so they have equally many parts.
 void build_joint(JointPlan& j, const cgtp_attn_s* at, int64_t tokens, int64_t shared_tiles) {
@@ -298,7 +336,7 @@ void build_joint(JointPlan& j, const cgtp_attn_s* at, int64_t tokens, int64_t sh
   for (int t = 0; t < n; t += j.per)
     u.push_back({0, 0, t, std::min(j.per, n - t), 0, int32_t(shared_tiles), 1, {0}});
   j.parts = int(build(j.list, u, j.per, at->kv_heads, j.per == 8 ? 2 * kCus : forward_slots(at), j.per == 1 ? 8 : 4,
-                      true));
+                      {true, false, part_extra(at, j.per)}));
 }
 
 // Partial results of both sides of a join by rows.
@@ -322,12 +360,12 @@ struct Carve {
   }
 };
 
-RowParts carve_row_parts(void* p, int64_t own_tiles, int64_t joint_tiles, int dp) {
+RowParts carve_row_parts(void* p, int64_t own_rows, int64_t joint_tiles, int dp) {
   Carve c{static_cast<char*>(p)};
   RowParts x{};
-  x.own_ml = static_cast<float4*>(c.take(size_t(own_tiles) * 32 * sizeof(float4)));
+  x.own_ml = static_cast<float4*>(c.take(size_t(own_rows) * sizeof(float4)));
   x.joint_ml = static_cast<float4*>(c.take(size_t(joint_tiles) * 32 * sizeof(float4)));
-  x.own = static_cast<float*>(c.take(size_t(own_tiles) * 32 * size_t(dp) * 4));
+  x.own = static_cast<float*>(c.take(size_t(own_rows) * size_t(dp) * 4));
   x.joint = static_cast<float*>(c.take(size_t(joint_tiles) * 32 * size_t(dp) * 4));
   x.bytes = c.used;
   return x;
@@ -480,7 +518,7 @@ cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, co
       add_query_units(u, sight, per, 1, 0, joint, take);
     else
       add_units(u, qs, ks, 0, per, 1, {0}, take);
-    build(w, u, per, g, slots, min_len, joint);
+    build(w, u, per, g, slots, min_len, {joint, causal, b->sequence ? part_extra(at, per) : 5});
   };
   forward(b->fwd, 4, slots, 4, [&](int n) { return n > 1 && n < wide; });
   forward(b->wide, 8, two, 4, [&](int n) { return n >= wide; });
@@ -496,9 +534,24 @@ cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, co
     add_units(u, qs, ks, 0, 4, 3, {kItemQ}, all);
     add_units(u, ks, qs, 1, 4, one_kind ? 4 : 3, kinds, all);
   }
-  build(b->bwd, u, 4, g, at->DP * es <= 384 ? two : one, 4);
+  build(b->bwd, u, 4, g, at->DP * es <= 384 ? two : one, 4, {false, causal, b->sequence ? part_extra(at, 4) : 5});
   return b.release();
 }
+
+namespace {
+// Key tiles of a cache up to which a slot is one workgroup's.
+constexpr int kWholeTiles = 4;
+// Workgroups of a step that a compute unit holds at once, by their shared memory.
+int64_t step_workgroups(int dp, size_t es) {
+  const int64_t bytes = step_waves(dp, es) * 32 * int64_t(dp) * int64_t(es) * 5 / 2;
+  return std::max<int64_t>(1, std::min<int64_t>(4, 160 * 1024 / bytes));
+}
+// Rows of partial results of a step against the caches (0: rows are final): StepCut.
+int64_t step_part_rows(const cgtp_attn_cache_s* c) {
+  if (c->whole || c->slots == 0) return 0;
+  return (c->shares + c->qtiles) * c->waves_a_head * c->attn->kv_heads * std::min(c->attn->G, 32);
+}
+}  // namespace
 
 cgtp_attn_cache_s* build_attn_cache(cgtp_attn_s* at, int64_t slots, int64_t capacity, int64_t shared) {
   auto c = std::make_unique<cgtp_attn_cache_s>();
@@ -515,24 +568,42 @@ cgtp_attn_cache_s* build_attn_cache(cgtp_attn_s* at, int64_t slots, int64_t capa
   const Side qs = cut(ptr, at->G);
   c->qtiles = int64_t(qs.tiles.size());
   c->tiles_a_slot = (at->G + 31) / 32;
-  // neighbouring heads on the waves of a workgroup; where there are less than three, a
-  // head's waves share the places
-  c->heads_a_group = std::min(4, at->kv_heads);
-  c->waves_a_head = 4 / c->heads_a_group;
+  const size_t es = dtype_size(at->dtype);
+  const int waves = step_waves(at->DP, es);
+  const int64_t tiles = (capacity + 31) / 32;
+  if (c->qtiles * tiles > 1 << 30) throw Error{CGTP_ERR_UNSUPPORTED, "attention cache: more than 2^30 tiles of 32 places"};
+  // short caches: a workgroup a slot, in one launch (8 slots of up to 64 places: 16.8 us, with
+  // a share of two workgroups each and the join 18.5 us)
+  c->whole = shared == 0 && tiles <= kWholeTiles;
+  // neighbouring heads on the waves of a workgroup; where there are fewer heads than waves,
+  // a head's waves take tiles in turn
+  c->heads_a_group = std::min(waves, at->kv_heads);
+  c->waves_a_head = c->whole ? 1 : waves / c->heads_a_group;
   c->bundles = (at->kv_heads + c->heads_a_group - 1) / c->heads_a_group;
-  const int64_t tiles = (capacity + 31) / 32, groups = c->qtiles * c->bundles;
-  c->min_tiles = 4;
-  const int64_t fill = std::max<int64_t>(1, 4 * 2 * kCus / std::max<int64_t>(1, groups));
-  const int64_t useful = (tiles + c->min_tiles * c->waves_a_head - 1) / (c->min_tiles * c->waves_a_head);
-  c->splits = int(std::max<int64_t>(1, std::min({fill, useful, int64_t(64)})));
-  c->parts = c->splits * c->waves_a_head;
-  need_launch((c->qtiles * c->splits + 7) / 8 * 8 * c->bundles);
-  if (c->qtiles * at->kv_heads * c->parts > INT32_MAX / 32)
-    throw Error{CGTP_ERR_UNSUPPORTED, "attention: too many partial tiles"};
+  // as many workgroups as the device works on at once, each with two turns or more (64
+  // sequences of up to 8000 tokens, heads of 128 in bf16: 133 us, with twice as many 139 us)
+  c->shares = int(std::max<int64_t>(1, kCus * step_workgroups(at->DP, es) / c->bundles));
+  c->min_turns = 2;
+  need_launch((std::max<int64_t>(c->qtiles, c->shares) + 7) / 8 * 8 * c->bundles);
+  if (step_part_rows(c.get()) > INT32_MAX) throw Error{CGTP_ERR_UNSUPPORTED, "attention: too many partial rows"};
+  // a row's 16-byte pieces of the heads of a workgroup in their order in memory
+  if (at->vec16) {
+    const int ve = 16 / int(dtype_size(at->dtype));
+    std::vector<StepPiece> pieces;
+    int d = 0;
+    for (const RowBlock& k : at->krow.blocks) {
+      const int cw = k.mul / at->kv_heads;
+      for (int m = 0; m < k.nc; ++m, d += cw)
+        for (int j = 0; j < c->heads_a_group; ++j)
+          for (int e = 0; e < cw; e += ve) pieces.push_back({k.off + m * k.mul + j * cw + e, cw, j, d + e});
+    }
+    c->pieces = int(pieces.size());
+    c->piece_mem.upload(pieces.data(), pieces.size() * sizeof(StepPiece));
+  }
   std::vector<Join> joins;
   for (int64_t t = 0; t < c->qtiles; ++t)
     for (int hk = 0; hk < at->kv_heads; ++hk)
-      joins.push_back({int32_t(t), hk, int32_t((t * at->kv_heads + hk) * c->parts), c->parts, 1, 0, 0, 0});
+      joins.push_back({int32_t(t), hk, 0, 0, 1, 0, 0, 0});  // (parts: by the lengths)
   need_launch(int64_t(joins.size()));
   c->joins = int(joins.size());
   c->qtile_mem.upload(qs.tiles.data(), qs.tiles.size() * sizeof(Tile));
@@ -551,7 +622,7 @@ size_t attn_context_bytes(const cgtp_attn_batch_s* b) { return carve_context(b, 
 
 size_t attn_forward_ws_bytes(const cgtp_attn_batch_s* b, bool packed) {
   if (b->joint.per)
-    return carve_row_parts(nullptr, b->few.part_tiles[0], b->joint.list.part_tiles[0], b->attn->DP).bytes +
+    return carve_row_parts(nullptr, b->few.part_tiles[0] * 32, b->joint.list.part_tiles[0], b->attn->DP).bytes +
            (packed ? 0 : attn_context_bytes(b));
   const size_t part = size_t(fwd_part_tiles(b)) * 32 * (size_t(b->attn->DP) + 4) * 4;
   return up16(part) + (packed ? 0 : attn_context_bytes(b));
@@ -638,9 +709,14 @@ void joint_launch(const cgtp_attn_s* a, const JointPlan& j, FwdArgs f, const Row
   CGTP_CHECK_HIP(hipGetLastError());
 }
 
+StepCut step_cut(const cgtp_attn_cache_s* c, const int32_t* lengths) {
+  return {lengths, int(c->slots), int(c->capacity), c->tiles_a_slot, c->waves_a_head, c->shares, c->min_turns};
+}
+
 void rows_join_launch(const cgtp_attn_s* a, const JointPlan& j, const FwdArgs& own, const RowParts& w, int joins,
-                      const int32_t* lengths, int64_t capacity, hipStream_t s) {
-  const RowsJoinArgs r{own, w.joint, w.joint_ml, j.units, j.per, j.per ? j.parts : 0, lengths, int(capacity)};
+                      const cgtp_attn_cache_s* c, const int32_t* lengths, hipStream_t s) {
+  RowsJoinArgs r{own, w.joint, w.joint_ml, j.units, j.per, j.per ? j.parts : 0, {}};
+  if (c) r.cut = step_cut(c, lengths);
   a->seq.rows_join(r, joins, s);
   CGTP_CHECK_HIP(hipGetLastError());
 }
@@ -662,7 +738,7 @@ void attn_forward_launch(const cgtp_attn_batch_s* b, RowsIn q, const void* conte
   f.shared = int(b->shared_tiles);
   f.causal = b->causal;
   if (b->joint.per) {
-    const RowParts w = carve_row_parts(ws, b->few.part_tiles[0], b->joint.list.part_tiles[0], a->DP);
+    const RowParts w = carve_row_parts(ws, b->few.part_tiles[0] * 32, b->joint.list.part_tiles[0], a->DP);
     joint_launch(a, b->joint, f, w, s);
     f.items = b->few.item_mem.as<Item>();
     f.joins = b->few.join_mem[0].as<Join>();
@@ -670,7 +746,7 @@ void attn_forward_launch(const cgtp_attn_batch_s* b, RowsIn q, const void* conte
     f.part_ml = w.own_ml;
     a->seq.fwd(f, b->few.items, 1, s);
     CGTP_CHECK_HIP(hipGetLastError());
-    rows_join_launch(a, b->joint, f, w, b->few.joins[0], nullptr, 0, s);
+    rows_join_launch(a, b->joint, f, w, b->few.joins[0], nullptr, nullptr, s);
     return;
   }
   f.part_ml = static_cast<float4*>(ws);
@@ -695,13 +771,8 @@ size_t attn_cache_shared_bytes(const cgtp_attn_cache_s* c) {
 }
 
 namespace {
-// tiles of partial results of a step against the caches (0: rows are final)
-bool step_whole(const cgtp_attn_cache_s* c) { return c->parts == 1 && c->joint.per == 0; }
-int64_t step_part_tiles(const cgtp_attn_cache_s* c) {
-  return step_whole(c) ? 0 : c->qtiles * c->attn->kv_heads * c->parts;
-}
 RowParts carve_step(const cgtp_attn_cache_s* c, void* ws) {
-  return carve_row_parts(ws, step_part_tiles(c), c->joint.list.part_tiles[0], c->attn->DP);
+  return carve_row_parts(ws, step_part_rows(c), c->joint.list.part_tiles[0], c->attn->DP);
 }
 }  // namespace
 
@@ -736,22 +807,19 @@ void attn_step_launch(const cgtp_attn_cache_s* c, RowsIn q, RowsIn k, RowsIn v, 
   x.ldv = v.ld;
   x.k_cache = k_cache;
   x.v_cache = v_cache;
-  x.lengths = lengths;
   x.dim = a->krow.dim;
-  x.slots = int(c->slots);
-  x.capacity = int(c->capacity);
+  x.cut = step_cut(c, lengths);
   x.size = a->D;
-  x.splits = c->splits;
-  x.waves_a_head = c->waves_a_head;
   x.heads_a_group = c->heads_a_group;
   x.bundles = c->bundles;
-  x.tiles_a_slot = c->tiles_a_slot;
-  x.min_tiles = c->min_tiles;
-  x.whole = step_whole(c);
+  x.pieces = c->pieces;
+  x.piece = c->piece_mem.as<StepPiece>();
+  x.whole = c->whole;
+  x.joined = c->joint.per > 0;
   x.vec = vec_rows(a, k.p, k.ld) && vec_rows(a, v.p, v.ld) && vec_rows(a, k_cache, x.dim) && vec_rows(a, v_cache, x.dim);
   a->seq.step(x, s);
   CGTP_CHECK_HIP(hipGetLastError());
-  if (!x.whole) rows_join_launch(a, c->joint, f, w, c->joins, lengths, c->capacity, s);
+  if (!x.whole) rows_join_launch(a, c->joint, f, w, c->joins, c, lengths, s);
 }
 
 void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn v, const uint8_t* mask, double scale,

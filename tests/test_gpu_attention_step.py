@@ -36,6 +36,12 @@ CASES = [
     ("128x0e+128x1o+128x2e+128x3o", 8, 8, [70, 9], 80, 0),                   # 256
     ("128x0e+128x1o+128x2e+128x3o", 16, 4, [1500, 1, 900], 1600, 0),         # splits
     ("128x0e+128x1o+128x2e+128x3o", 16, 16, [200, 33], 256, 0),              # several workgroups of heads
+    ("64x0e", 4, 2, [3, -1, 0] * 250 + [900, 127], 1000, 0),                 # more slots than workgroups at once
+    ("64x0e", 4, 4, [-1] * 70 + [2000] + [-1] * 10 + [31], 2001, 0),         # one long among idle ones
+    ("64x0e", 64, 1, [300, 0, 700, -1, 40], 701, 0),                         # two tiles of heads, shared out
+    ("128x0e+128x1o+128x2e+128x3o", 8, 8, [500, 9, 31, 470], 600, 0),        # 256, shared out
+    ("35x0e+21x1o+7x2e", 7, 1, [100, 3, 900, 0, 64], 1000, 0),
+    ("64x0e", 4, 2, [-1, -1, 300], 300, 0),                                  # nobody
     ("8x0e", 1, 1, [0], 1, 1),
     ("32x0e+32x1o+32x2e", 4, 2, [5, 0, -1, 30, 40], 40, 50),
     ("35x0e+21x1o+7x2e", 7, 1, [100, 3], 101, 333),
