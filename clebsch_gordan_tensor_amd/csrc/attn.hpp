@@ -120,7 +120,7 @@ struct RowsJoinArgs {
 // Waves of a step's workgroup: what its shared memory holds of their keys and values.
 constexpr int step_waves(int dp, size_t size) { return dp * int(size) <= 512 ? 4 : 2; }
 
-// 16 bytes of a context row: elements off + head * cw on, with the first head of the
+// Channels of a context row next to each other: elements off + head * cw on, with the first head of the
 // workgroup for `head`, are elements d on of the workgroup's head j.
 struct alignas(16) StepPiece {
   int32_t off, cw, j, d;
@@ -137,9 +137,9 @@ struct StepArgs {
   int size;                            // elements of a head
   int heads_a_group, bundles, pieces;  // heads of a workgroup; workgroups of a row's heads; pieces of a row for them
   const StepPiece* piece;
+  int width;    // channels of a piece
   bool whole;   // a workgroup takes a whole tile of rows (no shares): rows are final
   bool joined;  // rows are joined with those against shared rows: all results are parts
-  bool vec;
 };
 
 // Packed forms of the gradients: row or column fragments of K, V, Q and grad_out, in
@@ -256,8 +256,9 @@ struct cgtp_attn_cache_s {
   int device = 0;
   int heads_a_group = 1, waves_a_head = 1, bundles = 1, tiles_a_slot = 1, shares = 1, min_turns = 1;
   bool whole = false;
-  int joins = 0, pieces = 0;
-  cgtp::DevMem qtile_mem, shared_tile_mem, join_mem, piece_mem;
+  int joins = 0;
+  int width[3] = {0, 0, 0}, pieces[3] = {0, 0, 0};  // channels of a piece (0: none such), pieces of a row
+  cgtp::DevMem qtile_mem, shared_tile_mem, join_mem, piece_mem[3];
   cgtp::attn::JointPlan joint;
 };
 

@@ -549,7 +549,7 @@ int64_t step_workgroups(int dp, size_t es) {
 // Rows of partial results of a step against the caches (0: rows are final): StepCut.
 int64_t step_part_rows(const cgtp_attn_cache_s* c) {
   if (c->whole || c->slots == 0) return 0;
-  return (c->shares + c->qtiles) * c->waves_a_head * c->attn->kv_heads * std::min(c->attn->G, 32);
+  return (c->shares + c->qtiles) * c->attn->kv_heads * std::min(c->attn->G, 32);
 }
 }  // namespace
 
@@ -575,10 +575,11 @@ cgtp_attn_cache_s* build_attn_cache(cgtp_attn_s* at, int64_t slots, int64_t capa
   // short caches: a workgroup a slot, in one launch (8 slots of up to 64 places: 16.8 us, with
   // a share of two workgroups each and the join 18.5 us)
   c->whole = shared == 0 && tiles <= kWholeTiles;
+  const int whole_waves = tiles >= 4 ? 4 : tiles >= 2 ? 2 : 1;
   // neighbouring heads on the waves of a workgroup; where there are fewer heads than waves,
   // a head's waves take tiles in turn
-  c->heads_a_group = std::min(waves, at->kv_heads);
-  c->waves_a_head = c->whole ? 1 : waves / c->heads_a_group;
+  c->heads_a_group = std::min(c->whole ? std::max(1, waves / whole_waves) : waves, at->kv_heads);
+  c->waves_a_head = c->whole ? std::min(waves, whole_waves) : waves / c->heads_a_group;
   c->bundles = (at->kv_heads + c->heads_a_group - 1) / c->heads_a_group;
   // as many workgroups as the device works on at once, each with two turns or more (64
   // sequences of up to 8000 tokens, heads of 128 in bf16: 133 us, with twice as many 139 us)
@@ -586,19 +587,23 @@ cgtp_attn_cache_s* build_attn_cache(cgtp_attn_s* at, int64_t slots, int64_t capa
   c->min_turns = 2;
   need_launch((std::max<int64_t>(c->qtiles, c->shares) + 7) / 8 * 8 * c->bundles);
   if (step_part_rows(c.get()) > INT32_MAX) throw Error{CGTP_ERR_UNSUPPORTED, "attention: too many partial rows"};
-  // a row's 16-byte pieces of the heads of a workgroup in their order in memory
-  if (at->vec16) {
-    const int ve = 16 / int(dtype_size(at->dtype));
+  // a row's pieces of the heads of a workgroup in their order in memory, of 16 bytes, 4
+  // channels (where that is less) and one
+  const int ve = 16 / int(es);
+  const int widths[3] = {at->vec16 ? ve : 0, ve > 4 && at->quad ? 4 : 0, 1};
+  for (int i = 0; i < 3; ++i) {
+    if (widths[i] == 0) continue;
     std::vector<StepPiece> pieces;
     int d = 0;
     for (const RowBlock& k : at->krow.blocks) {
       const int cw = k.mul / at->kv_heads;
       for (int m = 0; m < k.nc; ++m, d += cw)
         for (int j = 0; j < c->heads_a_group; ++j)
-          for (int e = 0; e < cw; e += ve) pieces.push_back({k.off + m * k.mul + j * cw + e, cw, j, d + e});
+          for (int e = 0; e < cw; e += widths[i]) pieces.push_back({k.off + m * k.mul + j * cw + e, cw, j, d + e});
     }
-    c->pieces = int(pieces.size());
-    c->piece_mem.upload(pieces.data(), pieces.size() * sizeof(StepPiece));
+    c->width[i] = widths[i];
+    c->pieces[i] = int(pieces.size());
+    c->piece_mem[i].upload(pieces.data(), pieces.size() * sizeof(StepPiece));
   }
   std::vector<Join> joins;
   for (int64_t t = 0; t < c->qtiles; ++t)
@@ -812,11 +817,18 @@ void attn_step_launch(const cgtp_attn_cache_s* c, RowsIn q, RowsIn k, RowsIn v, 
   x.size = a->D;
   x.heads_a_group = c->heads_a_group;
   x.bundles = c->bundles;
-  x.pieces = c->pieces;
-  x.piece = c->piece_mem.as<StepPiece>();
   x.whole = c->whole;
   x.joined = c->joint.per > 0;
-  x.vec = vec_rows(a, k.p, k.ld) && vec_rows(a, v.p, v.ld) && vec_rows(a, k_cache, x.dim) && vec_rows(a, v_cache, x.dim);
+  // the widest pieces that the caches' rows are made of, by their alignment
+  for (int i = 2; i >= 0; --i) {
+    const size_t bytes = size_t(c->width[i]) * dtype_size(a->dtype);
+    if (c->width[i] == 0 || !aligned(k_cache, bytes) || !aligned(v_cache, bytes) ||
+        size_t(x.dim) * dtype_size(a->dtype) % bytes != 0)
+      continue;
+    x.width = c->width[i];
+    x.pieces = c->pieces[i];
+    x.piece = c->piece_mem[i].as<StepPiece>();
+  }
   a->seq.step(x, s);
   CGTP_CHECK_HIP(hipGetLastError());
   if (!x.whole) rows_join_launch(a, c->joint, f, w, c->joins, c, lengths, s);

@@ -22,58 +22,67 @@ namespace attn {
 // in the same cache lines, and the other heads' workgroups follow on the same die
 // (workgroup index modulo 8).
 
-// Quads: 4 keys x VE channels from rows in registers to VE columns of 4 keys.
+// W channels of one row in registers.
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+template <typename T, int W>
+struct Piece {
+  static constexpr int kBytes = W * int(sizeof(T)), kWords = (kBytes + 3) / 4;
+  using V = std::conditional_t<kBytes == 16, u32x4, std::conditional_t<kBytes == 8, u32x2, uint32_t>>;
+  using M = std::conditional_t<kBytes == 2, uint16_t, V>;  // in memory
+  V d;
+  __device__ __forceinline__ void load(const char* p) { d = V(*reinterpret_cast<const M*>(p)); }
+  __device__ __forceinline__ void store(char* p) const { *reinterpret_cast<M*>(p) = M(d); }
+  __device__ __forceinline__ void clear_unless(bool keep) { d = keep ? d : V(0); }
+  __device__ __forceinline__ uint32_t word(int i) const {
+    if constexpr (kWords == 1) return d;
+    else return d[i];
+  }
+};
+
+// The values of a tile by columns (a head's elements) of 32 keys, as operands: quads of 4
+// keys turned from rows in registers.
 template <typename T>
-struct Quad;
+struct Columns;
 template <>
-struct Quad<bf16> {
+struct Columns<bf16> {
   static constexpr int kStride = 80;  // bytes a column: 32 keys and 16 against bank conflicts
   // Byte of quad q in column d: column fragment f, half h hold quads 4 f + h and
-  // 4 f + 2 + h next to each other, as 16 bytes whose place turns with d / 16: the columns of
-  // 16 bytes of a row start at two banks only.
+  // 4 f + 2 + h next to each other, as 16 bytes whose place turns with d / 16 (else the
+  // columns that a wave writes at once would start at two banks: 174 us, with it 142 us).
   static __device__ __forceinline__ int at(int d, int q) {
     return d * kStride + ((q / 4 * 2 + q % 2) ^ (d / 16 & 3)) * 16 + q / 2 % 2 * 8;
   }
   static __device__ __forceinline__ int frag(int d, int f, int h) {
     return d * kStride + ((2 * f + h) ^ (d / 16 & 3)) * 16;
   }
-  static __device__ __forceinline__ void turn(const u32x4 (&r)[4], char* column) {
+  template <int W>
+  static __device__ __forceinline__ void turn(const Piece<bf16, W> (&r)[4], char* column) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint32_t a = r[0][c], b = r[1][c], d = r[2][c], e = r[3][c];
-      uint2 lo, hi;
-      lo.x = __builtin_amdgcn_perm(b, a, 0x05040100);
-      lo.y = __builtin_amdgcn_perm(e, d, 0x05040100);
-      hi.x = __builtin_amdgcn_perm(b, a, 0x07060302);
-      hi.y = __builtin_amdgcn_perm(e, d, 0x07060302);
-      *reinterpret_cast<uint2*>(column + 2 * c * kStride) = lo;
-      *reinterpret_cast<uint2*>(column + (2 * c + 1) * kStride) = hi;
+    for (int c = 0; c < Piece<bf16, W>::kWords; ++c) {
+      uint2 v;
+      v.x = __builtin_amdgcn_perm(r[1].word(c), r[0].word(c), 0x05040100);
+      v.y = __builtin_amdgcn_perm(r[3].word(c), r[2].word(c), 0x05040100);
+      *reinterpret_cast<uint2*>(column + 2 * c * kStride) = v;
+      if constexpr (W > 1) {
+        v.x = __builtin_amdgcn_perm(r[1].word(c), r[0].word(c), 0x07060302);
+        v.y = __builtin_amdgcn_perm(r[3].word(c), r[2].word(c), 0x07060302);
+        *reinterpret_cast<uint2*>(column + (2 * c + 1) * kStride) = v;
+      }
     }
   }
 };
 template <>
-struct Quad<float> {
+struct Columns<float> {
   static constexpr int kStride = 144;
   static __device__ __forceinline__ int at(int d, int q) { return d * kStride + (q ^ (d / 16 & 7)) * 16; }
   static __device__ __forceinline__ int frag(int d, int f, int h) { return at(d, 2 * f + h); }
-  static __device__ __forceinline__ void turn(const u32x4 (&r)[4], char* column) {
+  template <int W>
+  static __device__ __forceinline__ void turn(const Piece<float, W> (&r)[4], char* column) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      *reinterpret_cast<u32x4*>(column + c * kStride) = u32x4{r[0][c], r[1][c], r[2][c], r[3][c]};
+    for (int c = 0; c < W; ++c)
+      *reinterpret_cast<u32x4*>(column + c * kStride) = u32x4{r[0].word(c), r[1].word(c), r[2].word(c), r[3].word(c)};
   }
 };
-
-// Elements d0 .. d0 + VE - 1 of a context row's head; those outside the head are 0.
-template <typename T>
-__device__ __forceinline__ u32x4 row_piece(const T* row, const int4* table, int d0, int head, int size) {
-  constexpr int VE = Op<T>::VE;
-  u32x4 v;
-  T t[VE];
-#pragma unroll
-  for (int j = 0; j < VE; ++j) t[j] = row[elem(table[d0 + j], false, head)];
-  __builtin_memcpy(&v, t, 16);
-  return inside_head<T, false>(v, d0, size);
-}
 
 // A barrier for what is in shared memory: loads from memory stay on their way.
 __device__ __forceinline__ void turn_lds() {
@@ -140,9 +149,9 @@ __device__ __forceinline__ int2 step_find(const StepCut& c, const StepTurns& s, 
   }
 }
 
-// The first of the parts (one for each wave of the head) of workgroup `index` and tile of rows qt.
+// The part of workgroup `index` and tile of rows qt.
 __device__ __forceinline__ int step_part(const StepCut& c, int hk, int index, int qt) {
-  return (hk * (c.shares + c.slots * c.tiles_a_slot) + index + qt) * c.waves_a_head;
+  return hk * (c.shares + c.slots * c.tiles_a_slot) + index + qt;
 }
 
 // What a workgroup does next: turns a .. b - 1 of tile of rows qt.
@@ -156,10 +165,10 @@ struct StepWork {
   Item it;
 };
 // False: the workgroup has nothing to do.
-__device__ __forceinline__ bool step_begin(const StepArgs& a, int wave, StepWork& w) {
-  const int turn = int(blockIdx.x) / 8;
+__device__ __forceinline__ bool step_begin(const StepArgs& a, int block, int wave, StepWork& w) {
+  const int turn = block / 8;
   w.bundle = turn % a.bundles;
-  w.index = turn / a.bundles * 8 + int(blockIdx.x) % 8;
+  w.index = turn / a.bundles * 8 + block % 8;
   const int j = wave / a.cut.waves_a_head;
   w.hk = w.bundle * a.heads_a_group + j;
   w.on = j < a.heads_a_group && w.hk < a.f.groups;
@@ -212,24 +221,9 @@ __device__ __forceinline__ bool step_next(const StepArgs& a, int wave, StepWork&
   w.t0 = first * wph;
   w.t1 = min(last * wph, w.len / 32 + 1);
   w.last = last == turns;
-  const bool alone = first == 0 && last == turns && wph == 1 && !a.joined;
-  w.it = {w.qt, 1, w.t0, w.t1, w.hk, alone ? -1 : step_part(a.cut, w.hk, w.index, w.qt) + wave % wph, 1, 0};
+  const bool alone = first == 0 && last == turns && !a.joined;
+  w.it = {w.qt, 1, w.t0, w.t1, w.hk, alone ? -1 : step_part(a.cut, w.hk, w.index, w.qt), 1, 0};
   return true;
-}
-
-template <typename T>
-struct StepRows {
-  const T *cache, *fresh;
-  int64_t dim;
-  int len;
-  // the new row at the end, also for places behind it, which are hidden
-  __device__ __forceinline__ const T* at(int key) const { return key >= len ? fresh : cache + int64_t(key) * dim; }
-};
-template <typename T>
-__device__ __forceinline__ StepRows<T> step_rows(const StepArgs& a, const StepWork& w, const void* cache,
-                                                 const void* fresh, int64_t ld) {
-  return {static_cast<const T*>(cache) + int64_t(w.slot) * a.cut.capacity * a.dim,
-          static_cast<const T*>(fresh) + w.slot * ld, a.dim, w.len};
 }
 
 // The new rows' elements of the wave's head into the caches, and what else `also` does
@@ -267,121 +261,146 @@ __device__ __forceinline__ void step_values(const char* columns, int lane, Runni
   for (int d = 0; d < D::DT; ++d)
 #pragma unroll
     for (int f = 0; f < D::FR; ++f) {
-      const u32x4 x = *reinterpret_cast<const u32x4*>(columns + Quad<T>::frag(32 * d + lane % 32, f, lane / 32));
+      const u32x4 x = *reinterpret_cast<const u32x4*>(columns + Columns<T>::frag(32 * d + lane % 32, f, lane / 32));
       st.o[d] = Op<T>::mma(as_frag<typename Op<T>::Frag>(x), w[f], st.o[d]);
     }
 }
 
+// Shared memory of a step: for every wave its rows of keys and its columns of values, with
+// paddings against bank conflicts.
+template <typename T, int DP>
+struct StepShared {
+  static constexpr int kWaves = step_waves(DP, sizeof(T));
+  static constexpr int kRow = DP * int(sizeof(T)) + 16, kKeys = 32 * kRow, kPlace = kKeys + DP * Columns<T>::kStride + 64;
+  char place[kWaves][kPlace];
+  float ml[kWaves][3][64];
+  // two workgroups a compute unit, where its 160 KB hold this twice
+  static constexpr int kWavesASimd = kWaves * (kPlace + 768) <= 80 * 1024 ? few_waves(DP, sizeof(T)) : 1;
+};
 // Whether the registers hold the next turn's rows.
 constexpr bool step_ahead(int dp, size_t size) { return dp * int(size) <= 512 && dp <= 192; }
 
-// Bytes of shared memory of a step's waves: a row of keys, a wave's rows, its columns of values
-// (with paddings against bank conflicts).
-constexpr int step_row(int dp, size_t size) { return dp * int(size) + 16; }
-constexpr int step_rows_bytes(int dp, size_t size) { return 32 * step_row(dp, size) + 64; }
-template <typename T>
-constexpr int step_columns_bytes(int dp) { return dp * Quad<T>::kStride + 64; }
-template <typename T>
-constexpr int step_waves_a_simd(int dp) {
-  return step_waves(dp, sizeof(T)) * (step_rows_bytes(dp, sizeof(T)) + step_columns_bytes<T>(dp)) <= 80 * 1024
-             ? few_waves(dp, sizeof(T)) : 1;
+// The waves of a head joined in the first of them, in a fixed order, by way of their places.
+template <typename T, int DP>
+__device__ __forceinline__ void join_waves(StepShared<T, DP>& sh, int wave, int wph, Running<DP / 32>& st, float& e) {
+  const int lane = lane_id(), head = wave / wph * wph;
+  sh.ml[wave][0][lane] = st.m;
+  turn_lds();
+  float m = -INFINITY;
+  for (int k = 0; k < wph; ++k) m = fmaxf(m, sh.ml[min(head + k, StepShared<T, DP>::kWaves - 1)][0][lane]);
+  const float f = m == -INFINITY ? 1.0f : exp2_fast(st.m - m);
+  st.m = m;
+  st.l *= f;
+  e *= f;
+  sh.ml[wave][1][lane] = st.l;
+  sh.ml[wave][2][lane] = e;
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d) {
+    st.o[d] *= f;
+    f32x4* const box = reinterpret_cast<f32x4*>(sh.place[wave]);
+    if (wave != head)
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        box[b * 64 + lane] = f32x4{st.o[d][4 * b], st.o[d][4 * b + 1], st.o[d][4 * b + 2], st.o[d][4 * b + 3]};
+    turn_lds();
+    if (wave == head)
+      for (int k = 1; k < wph; ++k) {
+        const f32x4* const from = reinterpret_cast<const f32x4*>(sh.place[head + k]);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const f32x4 x = from[b * 64 + lane];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st.o[d][4 * b + i] += x[i];
+        }
+      }
+    turn_lds();
+  }
+  if (wave == head)
+    for (int k = 1; k < wph; ++k) {
+      st.l += sh.ml[head + k][1][lane];
+      e += sh.ml[head + k][2][lane];
+    }
 }
 
-// Rows whose heads are whole aligned 16-byte pieces. The workgroup reads the rows of its
-// heads in their order in memory, quads of 4 keys x 16 bytes a lane, a turn ahead in
-// registers (reading every head's pieces straight as operands took twice as long: each load
-// then touches 64 cache lines), and lays them out in shared memory: keys by rows, values
-// by columns, each wave's tile in a place of its own.
-template <typename T, int DP>
-__global__ __launch_bounds__(64 * step_waves(DP, sizeof(T)), step_waves_a_simd<T>(DP)) void step_kernel(StepArgs a) {
+// The workgroup reads the rows of its heads in their order in memory, quads of 4 keys x
+// W channels a lane, a turn ahead in registers (reading every head's pieces straight as
+// operands took twice as long: each load then touches 64 cache lines), and lays them out in
+// shared memory: keys by rows, values by columns, each wave's tile in a place of its own.
+// W: 16 bytes, 8 or one channel, by the heads' sizes and the tensors' alignment.
+// Measured: 64 sequences of 1000 - 8000 tokens, heads of 128, bf16: 116 us = 5.1 TB/s.
+template <typename T, int DP, int W>
+__device__ __forceinline__ void step_body(const StepArgs& a, int block, StepShared<T, DP>& sh) {
   using D = Dims<T, DP>;
   using Frag = typename Op<T>::Frag;
-  using Q = Quad<T>;
-  constexpr int VE = D::VE, WAVES = step_waves(DP, sizeof(T)), PER = (DP / VE + 7) / 8;
-  constexpr int ROW = step_row(DP, sizeof(T)), ROWS = step_rows_bytes(DP, sizeof(T)), COLUMNS = step_columns_bytes<T>(DP);
-  __shared__ __attribute__((aligned(16))) char key_rows[WAVES][ROWS], columns[WAVES][COLUMNS];
+  using C = Columns<T>;
+  using S = StepShared<T, DP>;
+  constexpr int WAVES = S::kWaves, THREADS = 64 * WAVES, PER = (DP / W + 7) / 8;
+  constexpr bool kSingle = W == 1;  // too many quads a thread to keep their places
   StepWork w;
   const int tid = int(threadIdx.x), wave = wave_id(), lane = lane_id(), n = lane % 32, h = lane / 32;
-  if (!step_begin(a, wave, w)) return;
+  if (!step_begin(a, block, wave, w)) return;
   const int wph = a.cut.waves_a_head;
   const int hk0 = w.hk - wave / wph, heads = min(a.heads_a_group, a.f.groups - hk0);
   // quads of this thread: one piece of four keys each (threads without one, and those of
   // heads that the last workgroup of a row does not have, repeat another's)
   const int row_bytes = int(a.dim * int64_t(sizeof(T)));
-  int key[PER], row_at[PER], column_at[PER];
-  uint32_t off[PER];  // bytes from the row's start
-#pragma unroll
-  for (int g = 0; g < PER; ++g) {
-    const int i = (tid + 64 * WAVES * g) % (8 * wph * a.pieces), quad = i / a.pieces;
+  struct Spot {
+    int key, row_at, column_at;
+    uint32_t off;  // bytes from the row's start
+  };
+  const auto spot = [&](int i) {
+    i %= 8 * wph * a.pieces;
+    const int quad = i / a.pieces;
     StepPiece p = a.piece[i % a.pieces];
     if (p.j >= heads) p = a.piece[0];
-    key[g] = 4 * quad;
-    off[g] = uint32_t(p.off + hk0 * p.cw) * uint32_t(sizeof(T));
-    const int place = p.j * wph + quad / 8;
-    row_at[g] = place * ROWS + quad % 8 * 4 * ROW + p.d * int(sizeof(T));
-    column_at[g] = place * COLUMNS + Q::at(p.d, quad % 8);
-  }
-  // Quads first .. first + count - 1 of the turn from tile t on. Places behind the
-  // sequence's end are read as well (they are hidden), but none behind the caches' end.
-  const auto load = [&](const void* cache, int t, auto first, auto count, u32x4 (&x)[decltype(count)::value][4]) {
+    const int place = (p.j * wph + quad / 8) * S::kPlace;
+    return Spot{4 * quad, place + quad % 8 * 4 * S::kRow + p.d * int(sizeof(T)), place + S::kKeys + C::at(p.d, quad % 8),
+                uint32_t(p.off + hk0 * p.cw) * uint32_t(sizeof(T))};
+  };
+  char* const mem = &sh.place[0][0];
+  // Quad of the turn from tile t on. Places behind the sequence's end are read as well
+  // (they are hidden), but none behind the caches' end.
+  const auto load = [&](const void* cache, int t, const Spot& p, Piece<T, W> (&x)[4]) {
     const int64_t row = int64_t(w.slot) * a.cut.capacity + int64_t(t) * 32;
     const char* const base = static_cast<const char*>(cache) + row * row_bytes;
     const int rows = int(min(int64_t(a.cut.slots) * a.cut.capacity - row, int64_t(32 * WAVES)));
 #pragma unroll
-    for (int i = 0; i < decltype(count)::value; ++i) {
-      const int g = decltype(first)::value + i;
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        x[i][r] = *reinterpret_cast<const u32x4*>(
-            base + (off[g] + (key[g] + r < rows ? uint32_t(key[g] + r) * uint32_t(row_bytes) : 0u)));
-    }
+    for (int r = 0; r < 4; ++r)
+      x[r].load(base + (p.off + (p.key + r < rows ? uint32_t(p.key + r) * uint32_t(row_bytes) : 0u)));
   };
-  const auto put_keys = [&](auto first, auto count, const u32x4 (&x)[decltype(count)::value][4]) {
+  const auto put_keys = [&](const Spot& p, const Piece<T, W> (&x)[4]) {
 #pragma unroll
-    for (int i = 0; i < decltype(count)::value; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        *reinterpret_cast<u32x4*>(&key_rows[0][0] + row_at[decltype(first)::value + i] + r * ROW) = x[i][r];
+    for (int r = 0; r < 4; ++r) x[r].store(mem + p.row_at + r * S::kRow);
   };
-  const auto put_values = [&](int t, auto first, auto count, u32x4 (&x)[decltype(count)::value][4]) {
+  const auto put_values = [&](int t, const Spot& p, Piece<T, W> (&x)[4]) {
     // weight 0 times what a place from the end on holds would be NaN for infinities
     if (32 * (t + wph) > w.len)
 #pragma unroll
-      for (int i = 0; i < decltype(count)::value; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          x[i][r] = 32 * t + key[decltype(first)::value + i] + r >= w.len ? u32x4{0, 0, 0, 0} : x[i][r];
-#pragma unroll
-    for (int i = 0; i < decltype(count)::value; ++i)
-      Q::turn(x[i], &columns[0][0] + column_at[decltype(first)::value + i]);
+      for (int r = 0; r < 4; ++r) x[r].clear_unless(32 * t + p.key + r < w.len);
+    C::turn(x, mem + p.column_at);
   };
-  using none = std::integral_constant<int, 0>;
-  using every = std::integral_constant<int, PER>;
+  Spot spots[kSingle ? 1 : PER];
+  if constexpr (!kSingle)
+#pragma unroll
+    for (int g = 0; g < PER; ++g) spots[g] = spot(tid + THREADS * g);
   // the widest heads leave no registers for the next turn's rows
-  constexpr bool kAhead = step_ahead(DP, sizeof(T));
-  constexpr int HELD = kAhead ? PER : 1;
-  // both tensors' rows of a turn, half of the quads at a time
-  const auto pass = [&](int t, auto first, auto count) {
-    u32x4 x[decltype(count)::value][4];
-    load(a.k_cache, t, first, count, x);
-    put_keys(first, count, x);
-    __builtin_amdgcn_sched_barrier(0);
-    load(a.v_cache, t, first, count, x);
-    put_values(t, first, count, x);
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  // (keys' places beyond the head meet zeros of the queries, and must not be NaN)
-  if (a.size < DP)
-    for (int i = lane; i < 32 * (DP - a.size); i += 64)
-      *reinterpret_cast<T*>(&key_rows[wave][i % 32 * ROW + (a.size + i / 32) * int(sizeof(T))]) = T{};
+  constexpr bool kAhead = !kSingle && step_ahead(DP, sizeof(T)) && (W == D::VE || DP <= 96);
   const bool exact = sizeof(T) == 2 && a.f.lse != nullptr;
   while (step_next(a, wave, w)) {
-    u32x4 k[HELD][4], v[HELD][4];
-    if constexpr (kAhead)
-      if (w.t0 < w.t1) {
-        load(a.k_cache, w.t0, none{}, every{}, k);
-        load(a.v_cache, w.t0, none{}, every{}, v);
-      }
+    Piece<T, W> k[kAhead ? PER : 1][4], v[kAhead ? PER : 1][4];
+    const auto load_all = [&](const void* cache, int t, Piece<T, W> (&x)[kAhead ? PER : 1][4]) {
+#pragma unroll
+      for (int g = 0; g < (kAhead ? PER : 0); ++g) load(cache, t, spots[g], x[g]);
+    };
+    if (kAhead && w.t0 < w.t1) {
+      load_all(a.k_cache, w.t0, k);
+      load_all(a.v_cache, w.t0, v);
+    }
+    // (keys' places beyond the head meet zeros of the queries, and must not be NaN; the
+    // join of waves writes there)
+    if (a.size < DP)
+      for (int i = lane; i < 32 * (DP - a.size); i += 64)
+        *reinterpret_cast<T*>(&sh.place[wave][i % 32 * S::kRow + (a.size + i / 32) * int(sizeof(T))]) = T{};
     const Tile tl = ldc(a.f.qtiles + w.qt);
     Frag q[D::KSTEPS];
     load_queries<T, DP>(a.f, tl, w.on ? w.hk : 0, lane, q);
@@ -395,96 +414,76 @@ __global__ __launch_bounds__(64 * step_waves(DP, sizeof(T)), step_waves_a_simd<T
         // (each tensor's registers are on their way again as soon as they are written out, so
         // that the reads of memory do not run dry)
         const int next = t + wph < w.t1 ? t + wph : t;
-        put_keys(none{}, every{}, k);
-        load(a.k_cache, next, none{}, every{}, k);
-        put_values(t, none{}, every{}, v);
-        load(a.v_cache, next, none{}, every{}, v);
+#pragma unroll
+        for (int g = 0; g < PER; ++g) put_keys(spots[g], k[g]);
+        load_all(a.k_cache, next, k);
+#pragma unroll
+        for (int g = 0; g < PER; ++g) put_values(t, spots[g], v[g]);
+        load_all(a.v_cache, next, v);
+      } else if constexpr (!kSingle) {
+        // some quads of both tensors at a time
+        constexpr int SOME = DP * int(sizeof(T)) > 768 ? 2 : 4;
+#pragma unroll
+        for (int g0 = 0; g0 < PER; g0 += SOME) {
+          Piece<T, W> x[SOME][4];
+#pragma unroll
+          for (int tensor = 0; tensor < 2; ++tensor) {
+#pragma unroll
+            for (int g = g0; g < min(g0 + SOME, PER); ++g) load(tensor ? a.v_cache : a.k_cache, t, spots[g], x[g - g0]);
+#pragma unroll
+            for (int g = g0; g < min(g0 + SOME, PER); ++g) {
+              if (tensor) put_values(t, spots[g], x[g - g0]);
+              else put_keys(spots[g], x[g - g0]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
       } else {
-        using half = std::integral_constant<int, PER / 2>;
-        pass(t, none{}, half{});
-        pass(t, half{}, std::integral_constant<int, PER - PER / 2>{});
+        const int count = 8 * wph * a.pieces;
+#pragma unroll 4
+        for (int i = tid; i < count; i += THREADS) {
+          const Spot p = spot(i);
+          Piece<T, W> x[4], y[4];
+          load(a.k_cache, t, p, x);
+          load(a.v_cache, t, p, y);
+          put_keys(p, x);
+          put_values(t, p, y);
+        }
       }
       turn_lds();
       if (w.on && mine < w.t1) {
         if (mine == w.len / 32) {
           const int r = w.len % 32;
           take_new<T>(a, w, [&](int d, T x, T y) {
-            *reinterpret_cast<T*>(&key_rows[wave][r * ROW + d * int(sizeof(T))]) = x;
-            *reinterpret_cast<T*>(&columns[wave][Q::at(d, r / 4) + r % 4 * int(sizeof(T))]) = y;
+            *reinterpret_cast<T*>(&sh.place[wave][r * S::kRow + d * int(sizeof(T))]) = x;
+            *reinterpret_cast<T*>(&sh.place[wave][S::kKeys + C::at(d, r / 4) + r % 4 * int(sizeof(T))]) = y;
           });
           wave_fence();
         }
         f32x16 sc = zero16();
 #pragma unroll
         for (int u = 0; u < D::KSTEPS; ++u) {
-          const u32x4 x = *reinterpret_cast<const u32x4*>(&key_rows[wave][n * ROW + (2 * u + h) * 16]);
+          // (products of fp32 take eight times as long: none with padding alone)
+          if (sizeof(T) == 4 && 2 * D::VE * u >= a.size) break;
+          const u32x4 x = *reinterpret_cast<const u32x4*>(&sh.place[wave][n * S::kRow + (2 * u + h) * 16]);
           sc = Op<T>::mma(as_frag<Frag>(x), q[u], sc);
         }
         Frag p[D::FR];
         step_weigh<T, DP>(a, mine, w.len, st, sc, e, exact, p);
-        step_values<T, DP>(columns[wave], lane, st, p);
+        step_values<T, DP>(&sh.place[wave][S::kKeys], lane, st, p);
       }
       turn_lds();
     }
-    if (w.on) finish<T, DP>(a.f, w.it, tl, 0, st, e, min(a.f.G, 32));
+    if (wph > 1) join_waves<T, DP>(sh, wave, wph, st, e);
+    if (w.on && wave % wph == 0) finish<T, DP>(a.f, w.it, tl, 0, st, e, min(a.f.G, 32));
   }
 }
 
-// Rows of any alignment, read element by element: keys straight as operands, values
-// turned in a wave's own place.
-template <typename T, int DP>
-__global__ __launch_bounds__(64 * step_waves(DP, sizeof(T)), few_waves(DP, sizeof(T))) void step_elements_kernel(
+template <typename T, int DP, int W>
+__global__ __launch_bounds__(64 * step_waves(DP, sizeof(T)), (StepShared<T, DP>::kWavesASimd)) void step_kernel(
     StepArgs a) {
-  using D = Dims<T, DP>;
-  using Frag = typename Op<T>::Frag;
-  using Q = Quad<T>;
-  constexpr int VE = D::VE, PIECES = DP / VE, PER = (PIECES + 7) / 8;
-  __shared__ __attribute__((aligned(16))) char columns[step_waves(DP, sizeof(T))][DP * Q::kStride];
-  StepWork w;
-  const int wave = wave_id(), lane = lane_id(), n = lane % 32;
-  if (!step_begin(a, wave, w) || !w.on) return;
-  char* const mine = columns[wave];
-  const bool exact = sizeof(T) == 2 && a.f.lse != nullptr;
-  while (step_next(a, wave, w)) {
-    const auto kr = step_rows<T>(a, w, a.k_cache, a.k_new, a.ldk), vr = step_rows<T>(a, w, a.v_cache, a.v_new, a.ldv);
-    const Tile tl = ldc(a.f.qtiles + w.qt);
-    Frag q[D::KSTEPS];
-    load_queries<T, DP>(a.f, tl, w.hk, lane, q);
-    Running<D::DT> st;
-    float e = 0.0f;
-#pragma unroll
-    for (int d = 0; d < D::DT; ++d) st.o[d] = zero16();
-    for (int t = w.t0 + wave % a.cut.waves_a_head; t < w.t1; t += a.cut.waves_a_head) {
-      f32x16 sc = zero16();
-#pragma unroll
-      for (int u = 0; u < D::KSTEPS; ++u) {
-        const u32x4 x = row_piece<T>(kr.at(32 * t + n), a.f.table, VE * (2 * u + lane / 32), w.hk, a.size);
-        sc = Op<T>::mma(as_frag<Frag>(x), q[u], sc);
-        if (u % 4 == 3) __builtin_amdgcn_sched_barrier(0);
-      }
-      Frag p[D::FR];
-      step_weigh<T, DP>(a, t, w.len, st, sc, e, exact, p);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int c = lane + 64 * i, piece = c / 8, quad = c % 8;
-        if (PIECES % 8 != 0 && piece >= PIECES) break;
-        u32x4 x[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int key = 32 * t + 4 * quad + r;
-          x[r] = row_piece<T>(vr.at(key), a.f.table, VE * piece, w.hk, a.size);
-          if (key > w.len) x[r] = u32x4{0, 0, 0, 0};
-        }
-        Q::turn(x, mine + Q::at(VE * piece, quad));
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      wave_fence();
-      step_values<T, DP>(mine, lane, st, p);
-      wave_fence();
-    }
-    if (w.last && wave % a.cut.waves_a_head == 0) take_new<T>(a, w, [](int, T, T) {});
-    finish<T, DP>(a.f, w.it, tl, 0, st, e, min(a.f.G, 32));
-  }
+  __shared__ __attribute__((aligned(16))) StepShared<T, DP> sh;
+  step_body<T, DP, W>(a, int(blockIdx.x), sh);
 }
 
 // ----------------------------------------------------------------- rows' join
@@ -515,8 +514,8 @@ __global__ __launch_bounds__(kThreads) void rows_join_kernel(RowsJoinArgs a) {
     const int share = step_share(a.cut, all.total);
     const int at = step_before(a.cut, all, slot) + j.tile % a.cut.tiles_a_slot * turns;
     const int i0 = at / share, i1 = (at + turns - 1) / share;  // workgroups
-    if (turns > 0 && i0 == i1 && a.cut.waves_a_head == 1 && a.parts == 0) return;  // (final already)
-    parts[0] = turns > 0 ? (i1 - i0 + 1) * a.cut.waves_a_head : 0;
+    if (turns > 0 && i0 == i1 && a.parts == 0) return;  // (final already)
+    parts[0] = turns > 0 ? i1 - i0 + 1 : 0;
     if (turns == 0) parts[1] = 0;
     own_rows = min(a.own.G, 32);
     own = step_part(a.cut, j.hk, i0, j.tile);
@@ -594,8 +593,12 @@ struct SeqKernels {
     const unsigned groups = a.whole ? unsigned(a.cut.slots) * unsigned(a.cut.tiles_a_slot) : unsigned(a.cut.shares);
     const dim3 grid((groups + 7) / 8 * 8 * unsigned(a.bundles));
     const dim3 threads(64 * step_waves(DP, sizeof(T)));
-    if (a.vec) hipLaunchKernelGGL((step_kernel<T, DP>), grid, threads, 0, s, a);
-    else hipLaunchKernelGGL((step_elements_kernel<T, DP>), grid, threads, 0, s, a);
+    if (a.width == Op<T>::VE)
+      hipLaunchKernelGGL((step_kernel<T, DP, Op<T>::VE>), grid, threads, 0, s, a);
+    else if (sizeof(T) == 2 && a.width == 4)
+      hipLaunchKernelGGL((step_kernel<T, DP, 4>), grid, threads, 0, s, a);
+    else
+      hipLaunchKernelGGL((step_kernel<T, DP, 1>), grid, threads, 0, s, a);
   }
   static void rows_join(const RowsJoinArgs& a, int joins, hipStream_t s) {
     hipLaunchKernelGGL((rows_join_kernel<T, DP>), dim3(unsigned(joins), DP / 32), dim3(kThreads), 0, s, a);

@@ -41,6 +41,7 @@ CASES = [
     ("64x0e", 64, 1, [300, 0, 700, -1, 40], 701, 0),                         # two tiles of heads, shared out
     ("128x0e+128x1o+128x2e+128x3o", 8, 8, [500, 9, 31, 470], 600, 0),        # 256, shared out
     ("35x0e+21x1o+7x2e", 7, 1, [100, 3, 900, 0, 64], 1000, 0),
+    ("32x0e+32x1o+32x2e", 8, 2, [100, 3, 500, 0, 64], 600, 0),               # runs of 8 bytes in bf16
     ("64x0e", 4, 2, [-1, -1, 300], 300, 0),                                  # nobody
     ("8x0e", 1, 1, [0], 1, 1),
     ("32x0e+32x1o+32x2e", 4, 2, [5, 0, -1, 30, 40], 40, 50),
