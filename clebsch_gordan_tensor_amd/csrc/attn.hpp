@@ -120,6 +120,9 @@ struct RowsJoinArgs {
 // Waves of a step's workgroup: what its shared memory holds of their keys and values.
 constexpr int step_waves(int dp, size_t size) { return dp * int(size) <= 512 ? 4 : 2; }
 
+// Whether one launch takes a step and its rows against the shared ones.
+constexpr bool step_with_joint(int dp, size_t size) { return step_waves(dp, size) == 4; }
+
 // Channels of a context row next to each other: elements off + head * cw on, with the first head of the
 // workgroup for `head`, are elements d on of the workgroup's head j.
 struct alignas(16) StepPiece {
@@ -129,6 +132,9 @@ struct alignas(16) StepPiece {
 // One token a slot on caches of rows [slot][capacity][dim].
 struct StepArgs {
   FwdArgs f;
+  FwdArgs joint;     // against the shared rows: in workgroups of the same launch
+  int joint_blocks;  // (a multiple of 8; 0: none, or launched before), of which this many are items
+  int joint_items;
   StepCut cut;
   const void *k_new, *v_new;
   int64_t ldk, ldv;

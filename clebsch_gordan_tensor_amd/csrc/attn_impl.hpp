@@ -739,15 +739,21 @@ constexpr float kBound = 40.0f;
 // SEQ: key tiles by way of the queries' Reach, and in causal batches the scores of
 // later keys hidden in the tiles where some of the wave's queries see only a part (one
 // or two of a wave's; a wave leaves out the tiles that none of its queries sees).
+template <typename T, int DP, int RT>
+struct FwdShared {
+  u32x4 kb[fwd_ring<T, DP>()][Dims<T, DP>::UNITS * 64], vb[fwd_ring<T, DP>()][Dims<T, DP>::UNITS * 64];
+  float bounds[4], sums[sizeof(T) == 2 ? RT : 1][kThreads];
+};
 template <typename T, int DP, int RT, bool SEQ>
-__global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T, DP>::UNITS)) void fwd_kernel(
-    FwdArgs a) {
+__device__ __forceinline__ void fwd_body(const FwdArgs& a, int item, FwdShared<T, DP, RT>& sh) {
   using D = Dims<T, DP>;
   using Frag = typename Op<T>::Frag;
   constexpr int R = fwd_ring<T, DP>();
-  __shared__ u32x4 kb[R][D::UNITS * 64], vb[R][D::UNITS * 64];
-  __shared__ float bounds[4], sums[sizeof(T) == 2 ? RT : 1][kThreads];
-  const Item it = ldc(a.items + blockIdx.x);
+  auto& kb = sh.kb;
+  auto& vb = sh.vb;
+  auto& bounds = sh.bounds;
+  auto& sums = sh.sums;
+  const Item it = ldc(a.items + item);
   if (it.tiles == 0) return;
   const int lane = int(threadIdx.x) % 64, wave = wave_id(), h = lane / 32;
   const int mine = min(max(it.tiles - wave * RT, 0), RT);  // query tiles of this wave
@@ -889,6 +895,13 @@ __global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T,
       if constexpr (SEQ)
         if (a.causal) redo_rows<T, DP>(a, it, re, tl, wave * RT + r, st[r]);
     }
+}
+
+template <typename T, int DP, int RT, bool SEQ>
+__global__ __launch_bounds__(kThreads, lds_waves(2 * fwd_ring<T, DP>() * Dims<T, DP>::UNITS)) void fwd_kernel(
+    FwdArgs a) {
+  __shared__ FwdShared<T, DP, RT> sh;
+  fwd_body<T, DP, RT, SEQ>(a, int(blockIdx.x), sh);
 }
 
 // At most 32 query rows against a long context (single tokens): the four waves

@@ -197,13 +197,14 @@ struct How {
   bool all_parts = false;  // every result is a part, also that of an unsplit unit
   bool uneven = false;     // the items of a group differ in length (causal queries)
   int part_extra = 5;      // of part_cost
+  int64_t cost = 0;        // largest cost of a part, where it is known
 };
 int64_t build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, int slots, int min_len,
               const How& how = {}) {
   int64_t whole = 0;
   for (const Unit& x : u) whole += int64_t(x.kinds.size()) * groups;
   need_launch(whole);  // (before the lists are laid out)
-  const int64_t cost = part_cost(u, groups, slots, min_len, how.part_extra);
+  const int64_t cost = how.cost ? how.cost : part_cost(u, groups, slots, min_len, how.part_extra);
   struct Group {
     int64_t work = 0, longest = 0;
     std::vector<Item> items;
@@ -324,19 +325,35 @@ int forward_slots(const cgtp_attn_s* at) { return at->DP * int(dtype_size(at->dt
 int part_extra(const cgtp_attn_s* at, int per) { return dtype_size(at->dtype) == 2 && per > 1 ? 24 : 5; }
 
 // The rows of `tokens` tokens in tiles whatever their sample, against shared_tiles key
-// tiles. All units see the same tiles, so they have equally many parts.
-void build_joint(JointPlan& j, const cgtp_attn_s* at, int64_t tokens, int64_t shared_tiles) {
+// tiles, in items of up to `per` tiles of rows. All units see the same tiles, so they have
+// equally many parts: as many as make the turns (about 1 us for 128 elements in bf16, 3.5 us
+// in fp32) and the parts' bytes, written and read, the least (64 tokens on 8000 shared rows: 35 of
+// a device's 62 parts).
+void build_joint(JointPlan& j, const cgtp_attn_s* at, int64_t tokens, int64_t shared_tiles, bool with_step) {
   const Side rows = cut({0, tokens}, at->G);
   const int n = int(rows.tiles.size());
   if (n == 0) return;
-  j.per = n == 1 ? 1 : n >= kWideTiles && wide_forward(at->DP, dtype_size(at->dtype)) ? 8 : 4;
+  const size_t es = dtype_size(at->dtype);
+  j.per = with_step ? 4 : n == 1 ? 1 : n >= kWideTiles && wide_forward(at->DP, es) ? 8 : 4;
   j.units = (n + j.per - 1) / j.per;
   j.tiles.upload(rows.tiles.data(), rows.tiles.size() * sizeof(Tile));
   std::vector<Unit> u;
   for (int t = 0; t < n; t += j.per)
     u.push_back({0, 0, t, std::min(j.per, n - t), 0, int32_t(shared_tiles), 1, {0}});
-  j.parts = int(build(j.list, u, j.per, at->kv_heads, j.per == 8 ? 2 * kCus : forward_slots(at), j.per == 1 ? 8 : 4,
-                      {true, false, part_extra(at, j.per)}));
+  const int slots = j.per == 8 ? 2 * kCus : forward_slots(at);
+  const double turn = (es == 2 ? 1.0 : 3.5) * at->DP / 128 * (j.per == 8 ? 2 : 1);
+  const double part = double(n) * 32 * at->kv_heads * at->DP * 8 / 5e6;  // us
+  How how{true, false, 0, shared_tiles};
+  double best = 1e30;
+  for (int64_t p = 1; p <= std::min<int64_t>(64, (shared_tiles + 1) / 2); ++p) {
+    const int64_t len = (shared_tiles + p - 1) / p, items = int64_t(j.units) * at->kv_heads * p;
+    const double t = double((items + slots - 1) / slots) * double(len + 3) * turn + double(p) * part;
+    if (t < best) {
+      best = t;
+      how.cost = len;
+    }
+  }
+  j.parts = int(build(j.list, u, j.per, at->kv_heads, slots, 1, how));
 }
 
 // Partial results of both sides of a join by rows.
@@ -508,9 +525,14 @@ cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, co
   // workgroups at once: two a compute unit where registers and shared memory allow
   const int es = int(dtype_size(at->dtype)), two = 2 * kCus, one = kCus;
   const int slots = forward_slots(at);
-  // samples of a tile at most, which mostly hold less than 32 rows: their rows go
-  // against the shared rows together
-  if (shared > 0 && few && b->qtiles > (b->nq * at->G + 31) / 32) build_joint(b->joint, at, b->nq, b->shared_tiles);
+  // Samples of a tile at most, which mostly hold less than 32 rows: their rows go against
+  // the shared rows together where that saves enough products of tiles to pay for two more
+  // launches (32-row tiles of heads of 128, us with and without: bf16 56,000 saved 47 and 60,
+  // 14,300 saved 41 and 33; fp32 3600 saved 42 and 55, 900 saved 45 and 31).
+  if (shared > 0 && few) {
+    const int64_t saved = (b->qtiles - (b->nq * at->G + 31) / 32) * b->shared_tiles * g;
+    if (saved * at->DP >= (es == 2 ? 3200000 : 450000)) build_joint(b->joint, at, b->nq, b->shared_tiles, false);
+  }
   const bool joint = b->joint.per > 0;
   const auto forward = [&](WorkList& w, int per, int slots, int min_len, auto&& take) {
     std::vector<Unit> u;
@@ -520,9 +542,34 @@ cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, co
       add_units(u, qs, ks, 0, per, 1, {0}, take);
     build(w, u, per, g, slots, min_len, {joint, causal, b->sequence ? part_extra(at, per) : 5});
   };
-  forward(b->fwd, 4, slots, 4, [&](int n) { return n > 1 && n < wide; });
-  forward(b->wide, 8, two, 4, [&](int n) { return n >= wide; });
-  forward(b->few, 1, slots, 8, [](int n) { return n == 1; });
+  // the items' tiles by a sample's: one, some, many
+  int one_tile = 1, some = 4, many = 8;
+  if (b->sequence && !joint) {
+    // A kernel's launch costs some 10 us more than it does. Samples of one tile with short
+    // contexts go along with those of more (us apart and together: samples of 1 - 60 rows 24
+    // and 14 in bf16, 36 and 22 in fp32); small work of 64 rows a wave goes in 32, which
+    // takes a twelfth longer, and little work beside it in 64.
+    std::vector<Unit> u[3];
+    add_query_units(u[0], sight, 1, 1, 0, false, [](int n) { return n == 1; });
+    add_query_units(u[1], sight, 4, 1, 0, false, [&](int n) { return n > 1 && n < wide; });
+    add_query_units(u[2], sight, 8, 1, 0, false, [&](int n) { return n >= wide; });
+    double us[3] = {0, 0, 0};
+    int64_t longest = 0;
+    for (int i = 0; i < 3; ++i)
+      for (const Unit& x : u[i]) {
+        us[i] += double(x.tiles) * (x.b1 - x.b0) * g * at->DP * 4096 / (es == 2 ? 1e9 : 1.2e8);
+        if (i == 0) longest = std::max<int64_t>(longest, x.b1 - x.b0);
+      }
+    if (!u[1].empty() && !u[2].empty()) {
+      if (us[2] < 120) many = 4;
+      else if (us[1] < 10) some = 8;
+    }
+    if (longest <= 16 && (!u[1].empty() || !u[2].empty())) one_tile = u[1].empty() ? many : some;
+  }
+  const auto kernel = [&](int n) { return n >= wide ? many : n > 1 ? some : n == 1 ? one_tile : 0; };
+  forward(b->fwd, 4, slots, 4, [&](int n) { return kernel(n) == 4; });
+  forward(b->wide, 8, two, 4, [&](int n) { return kernel(n) == 8; });
+  forward(b->few, 1, slots, 8, [&](int n) { return kernel(n) == 1; });
   std::vector<Unit> u;
   const auto all = [](int) { return true; };
   const bool one_kind = one_pass(at->DP, dtype_size(at->dtype));
@@ -585,7 +632,7 @@ cgtp_attn_cache_s* build_attn_cache(cgtp_attn_s* at, int64_t slots, int64_t capa
   // sequences of up to 8000 tokens, heads of 128 in bf16: 133 us, with twice as many 139 us)
   c->shares = int(std::max<int64_t>(1, kCus * step_workgroups(at->DP, es) / c->bundles));
   c->min_turns = 2;
-  need_launch((std::max<int64_t>(c->qtiles, c->shares) + 7) / 8 * 8 * c->bundles);
+  const int64_t workgroups = (std::max<int64_t>(c->qtiles, c->shares) + 7) / 8 * 8 * c->bundles;
   if (step_part_rows(c.get()) > INT32_MAX) throw Error{CGTP_ERR_UNSUPPORTED, "attention: too many partial rows"};
   // a row's pieces of the heads of a workgroup in their order in memory, of 16 bytes, 4
   // channels (where that is less) and one
@@ -618,8 +665,9 @@ cgtp_attn_cache_s* build_attn_cache(cgtp_attn_s* at, int64_t slots, int64_t capa
     c->shared_tiles = int64_t(ks.tiles.size());
     need_launch((c->shared_tiles + 7) / 8 * 8 * at->kv_heads);
     c->shared_tile_mem.upload(ks.tiles.data(), ks.tiles.size() * sizeof(Tile));
-    build_joint(c->joint, at, slots, c->shared_tiles);
+    build_joint(c->joint, at, slots, c->shared_tiles, step_with_joint(at->DP, es));
   }
+  need_launch(workgroups + (c->joint.list.items + 7) / 8 * 8);
   return c.release();
 }
 
@@ -796,9 +844,13 @@ void attn_step_launch(const cgtp_attn_cache_s* c, RowsIn q, RowsIn k, RowsIn v, 
   const cgtp_attn_s* a = c->attn;
   const RowParts w = carve_step(c, ws);
   FwdArgs f = forward_args(a, q, scale, out, lse);
+  FwdArgs shared = f;
   if (c->joint.per) {
-    use_context(f, carve_context(a, c->shared_tiles, const_cast<void*>(context)));
-    joint_launch(a, c->joint, f, w, s);
+    use_context(shared, carve_context(a, c->shared_tiles, const_cast<void*>(context)));
+    shared.qtiles = c->joint.tiles.as<Tile>();
+    shared.items = c->joint.list.item_mem.as<Item>();
+    shared.part = w.joint;
+    shared.part_ml = w.joint_ml;
   }
   f.qtiles = c->qtile_mem.as<Tile>();
   f.joins = c->join_mem.as<Join>();
@@ -828,6 +880,16 @@ void attn_step_launch(const cgtp_attn_cache_s* c, RowsIn q, RowsIn k, RowsIn v, 
     x.width = c->width[i];
     x.pieces = c->pieces[i];
     x.piece = c->piece_mem[i].as<StepPiece>();
+  }
+  if (c->joint.per) {
+    if (step_with_joint(a->DP, dtype_size(a->dtype)) && x.width * dtype_size(a->dtype) == 16) {
+      x.joint = shared;
+      x.joint_items = c->joint.list.items;
+      x.joint_blocks = (x.joint_items + 7) / 8 * 8;
+    } else {
+      a->k.fwd(shared, c->joint.list.items, c->joint.per, s);
+      CGTP_CHECK_HIP(hipGetLastError());
+    }
   }
   a->seq.step(x, s);
   CGTP_CHECK_HIP(hipGetLastError());

@@ -486,6 +486,21 @@ __global__ __launch_bounds__(64 * step_waves(DP, sizeof(T)), (StepShared<T, DP>:
   step_body<T, DP, W>(a, int(blockIdx.x), sh);
 }
 
+// With the rows against those that all slots share in workgroups of the same launch, before the
+// slots' own (neither fills the device: 64 answers on one document 53 us in two launches).
+template <typename T, int DP>
+__global__ __launch_bounds__(kThreads, (StepShared<T, DP>::kWavesASimd)) void step_joint_kernel(StepArgs a) {
+  using F = FwdShared<T, DP, 1>;
+  using S = StepShared<T, DP>;
+  __shared__ __attribute__((aligned(16))) char mem[sizeof(F) > sizeof(S) ? sizeof(F) : sizeof(S)];
+  const int block = int(blockIdx.x);
+  if (block < a.joint_blocks) {
+    if (block < a.joint_items) fwd_body<T, DP, 1, false>(a.joint, block, *reinterpret_cast<F*>(mem));
+  } else {
+    step_body<T, DP, Op<T>::VE>(a, block - a.joint_blocks, *reinterpret_cast<S*>(mem));
+  }
+}
+
 // ----------------------------------------------------------------- rows' join
 //
 // A workgroup takes 32 columns of one tile of rows, a thread 4 of one row: the parts
@@ -591,8 +606,13 @@ struct SeqKernels {
   }
   static void step(const StepArgs& a, hipStream_t s) {
     const unsigned groups = a.whole ? unsigned(a.cut.slots) * unsigned(a.cut.tiles_a_slot) : unsigned(a.cut.shares);
-    const dim3 grid((groups + 7) / 8 * 8 * unsigned(a.bundles));
+    const dim3 grid((groups + 7) / 8 * 8 * unsigned(a.bundles) + unsigned(a.joint_blocks));
     const dim3 threads(64 * step_waves(DP, sizeof(T)));
+    if constexpr (step_with_joint(DP, sizeof(T)))
+      if (a.joint_blocks) {
+        hipLaunchKernelGGL((step_joint_kernel<T, DP>), grid, threads, 0, s, a);
+        return;
+      }
     if (a.width == Op<T>::VE)
       hipLaunchKernelGGL((step_kernel<T, DP, Op<T>::VE>), grid, threads, 0, s, a);
     else if (sizeof(T) == 2 && a.width == 4)

@@ -49,6 +49,10 @@ CASES = [
     ("16x0e", 4, 2, [300, 1, 9], [300, 1, 40], True, 1000),
     ("64x0e", 1, 1, [300, 270, 1], [300, 0, 70], True, 200),                     # 64 rows a wave
     ("64x0e", 2, 2, [70, 10, 5], [33, 2, 0], True, 3),
+    ("128x0e+128x1o", 8, 2, [1, 2, 1, 0] * 8, [1, 20, 0, 7] * 8, True, 9000),    # joined by rows
+    ("128x0e+128x1o+128x2e+128x3o", 16, 4, [1] * 40, [3] * 40, False, 8100),     # joined by rows, 32 a wave
+    ("64x0e", 1, 1, [1, 300, 40, 0, 31], [1, 300, 40, 0, 31], True, 0),          # one kernel for all
+    ("64x0e", 1, 1, [1, 300, 40], [1, 300, 900], True, 0),                       # two
 ]
 
 
