@@ -56,6 +56,7 @@ struct PackArgs {
   float* bias;          // context: 0 or -inf for every key (else NULL)
   float* norms;         // context: largest |k|^2 of every tile and head (or NULL)
   int32_t* flags;       // context: whether a tile has a masked or missing key (or NULL)
+  int32_t* bad;         // whether a tile and head holds an infinity or NaN (SeqTable::pack)
   int G, heads, groups;  // G = 0: context rows
   int ntiles, size;  // size: elements of a head
   bool out_vec;
@@ -172,6 +173,7 @@ struct BwdArgs {
   const Reach* reach;  // as in FwdArgs
   int shared;
   bool causal;
+  const int32_t *k_bad, *q_bad;  // causal: tiles and heads that hold an infinity or NaN
   void *dq, *dk, *dv;
   float *part_q, *part_k, *part_v;
   int64_t ldq, ldk;
@@ -195,10 +197,13 @@ KernelTable kernels_bf16(int dp);
 // Kernels of batches with shared rows or causal queries, and of steps on a cache;
 // inst/attn_seq_*.hip.
 struct SeqTable {
+  void (*pack)(const PackArgs&, hipStream_t);  // for the gradients of causal batches
   void (*fwd)(const FwdArgs&, int items, int tiles, hipStream_t);
   void (*bwd)(const BwdArgs&, int items, hipStream_t);
   void (*step)(const StepArgs&, hipStream_t);
   void (*rows_join)(const RowsJoinArgs&, int joins, hipStream_t);
+  // of `count` query tiles (with the key tiles that they see), for every context head; NULL in fp32
+  void (*delta)(const BwdArgs&, const int4* tiles, int count, float* rows, hipStream_t);
 };
 SeqTable seq_kernels_f32(int dp);
 SeqTable seq_kernels_bf16(int dp);
@@ -254,6 +259,8 @@ struct cgtp_attn_batch_s {
   int64_t shared_tiles = 0;
   cgtp::DevMem reach;                 // Reach [qtiles]
   cgtp::attn::JointPlan joint;        // used where every sample has few rows
+  int few_keys = 0;                   // query tiles that see few keys
+  cgtp::DevMem few_keys_mem;          // int4 [few_keys]: as SeqTable::delta takes them
 };
 
 struct cgtp_attn_cache_s {

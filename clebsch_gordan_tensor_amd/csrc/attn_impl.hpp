@@ -283,7 +283,19 @@ __device__ __forceinline__ void scatter_acc(T* row, const int4* table, bool quer
 // 3.8 TB/s read and written, one of 72,000 rows at 4.9 TB/s. Reading whole cache lines
 // across neighbouring heads instead of one head's runs was no faster (155 us against
 // 143 us): the lines are shared in the die's L2 already.
-template <typename T, int DP, bool VEC, bool GRADS>
+//
+// CHECK: also notes the tiles that hold an infinity or NaN (redo_kernel).
+template <typename T>
+__device__ __forceinline__ bool not_finite(const u32x4& v) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    bad = bad || (v[i] & 0x7f800000u) == 0x7f800000u;
+    if (sizeof(T) == 2) bad = bad || (v[i] & 0x7f80u) == 0x7f80u;
+  }
+  return bad;
+}
+template <typename T, int DP, bool VEC, bool GRADS, bool CHECK = false>
 __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
   using D = Dims<T, DP>;
   constexpr int VE = D::VE, LD = DP + VE;  // an odd count of 16-byte pieces a row: no bank conflicts
@@ -292,6 +304,7 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
   constexpr int B = GRADS ? 1 : 0;  // place of tensor 1
   __shared__ __attribute__((aligned(16))) T sh[B + 1][32 * LD];
   __shared__ float red[32][9];
+  __shared__ int bad[CHECK ? 4 : 1];
   // A head's channels are short runs of a row: the heads of one tile share its
   // cache lines, so they go to one die (workgroup index modulo 8), one after another
   const int turn = int(blockIdx.x) / 8, tile = turn / a.groups * 8 + int(blockIdx.x) % 8, hk = turn % a.groups;
@@ -344,6 +357,13 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
     if (a.t[0].col_frags) *reinterpret_cast<u32x4*>(&sh[0][r * LD + d0]) = v0[c];
     if (a.t[1].col_frags) *reinterpret_cast<u32x4*>(&sh[B][r * LD + d0]) = v1[c];
   }
+  if constexpr (CHECK) {
+    bool found = false;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) found = found || not_finite<T>(v0[c]) || not_finite<T>(v1[c]);
+    const bool some = __any(found);
+    if (lane == 0) bad[wave] = some;
+  }
   if (!GRADS && a.norms) {
     // |k|^2 of every row, the largest of the tile below
     float n2 = 0.0f;
@@ -369,6 +389,8 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackArgs a) {
     red[r][tid % 8] = partial;
   }
   __syncthreads();
+  if constexpr (CHECK)
+    if (tid == 0) a.bad[at] = bad[0] | bad[1] | bad[2] | bad[3];
   if (GRADS && tid % 8 == 0) {
     // log2-domain lse (+inf: the row contributes nothing; NaN stays: every weight of the
     // row is NaN then) and rowsum(grad_out out)
@@ -607,27 +629,48 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
+// The kernel's arguments (its only parameter) read anew: what a branch that is hardly ever
+// taken needs of them would else be held in registers, or spilled, by all that comes before.
+template <typename A>
+__device__ __forceinline__ const A& arguments_anew() {
+  auto p = __builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const A*)(p);
+}
+
+// Lanes whose accumulators hold a NaN.
+template <int DT>
+__device__ __forceinline__ bool any_nan(const f32x16 (&o)[DT]) {
+  bool nan = false;
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) nan = nan || o[d][i] != o[d][i];
+  return nan;
+}
+// The rows (lanes modulo 32) for which `bad` holds in either half.
+__device__ __forceinline__ uint32_t rows_of(bool bad) {
+  const uint64_t b = __ballot(bad);
+  return uint32_t(b) | uint32_t(b >> 32);
+}
+
 // A matrix product adds weight 0 times value for the keys that a causal query does not
 // see, which is NaN where such a value is infinite or NaN. Rows that came out NaN with a
 // finite sum of weights are formed again here, key by key over those they see (lanes
-// along the head's elements), after finish() wrote them.
+// along the head's elements), after finish() wrote them. (The gradients likewise: redo_dq,
+// redo_dkv.)
 template <typename T, int DP>
-__device__ __forceinline__ void redo_rows(const FwdArgs& a, const Item& it, const Reach& re, const Tile& tl,
-                                          int tile_in_item, const Running<DP / 32>& st) {
+__device__ __forceinline__ void redo_rows(const Item& it, const Reach& re, const Tile& tl, int tile_in_item,
+                                          const Running<DP / 32>& st) {
   constexpr int PER = (DP + 63) / 64;
   const int lane = lane_id();
   const float sum = half_sum(st.l);
-  bool nan = false;
-#pragma unroll
-  for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) nan = nan || st.o[d][i] != st.o[d][i];
-  uint64_t rows = __ballot(nan && sum == sum);
-  rows = (rows | rows >> 32) & 0xffffffffu;
+  uint32_t rows = rows_of(any_nan(st.o) && sum == sum);
   if (!rows) return;
+  const FwdArgs& a = arguments_anew<FwdArgs>();
   wait_copies();  // (finish's stores of the same rows come first)
   while (rows) {
-    const int n = __builtin_ctzll(rows);
+    const int n = __builtin_ctz(rows);
     rows &= rows - 1;
     if (n >= tl.n) return;
     const float m = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(st.m), n));
@@ -893,7 +936,7 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, int item, FwdShared<T
       const Tile tl = ldc(a.qtiles + it.a0 + wave * RT + r);
       finish<T, DP>(a, it, tl, wave * RT + r, st[r], sum(r));
       if constexpr (SEQ)
-        if (a.causal) redo_rows<T, DP>(a, it, re, tl, wave * RT + r, st[r]);
+        if (a.causal) redo_rows<T, DP>(it, re, tl, wave * RT + r, st[r]);
     }
 }
 
@@ -1022,7 +1065,7 @@ __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void fwd_few_ke
     e = ml[0][2][lane] + ml[2][2][lane] + (ml[1][2][lane] + ml[3][2][lane]);
     finish<T, DP>(a, it, tl, 0, st, e);
     if constexpr (SEQ)
-      if (a.causal) redo_rows<T, DP>(a, it, re, tl, 0, st);
+      if (a.causal) redo_rows<T, DP>(it, re, tl, 0, st);
   }
 }
 
@@ -1085,6 +1128,31 @@ __device__ __forceinline__ void finish_grad(const BwdArgs& a, const Item& it, co
   if (n >= tl.n) return;
   const int row = tl.row0 + n, G = query ? a.G : 1, token = row / G, head = it.hk * G + row % G;
   scatter_acc(static_cast<T*>(dst) + int64_t(token) * ld, a.table, query, head, quad, h, g, scale);
+}
+
+// Row n of a wave's gradients, formed again (see redo_rows; lanes along the head's
+// elements), over what finish_grad() wrote.
+template <typename T, int DP, int PER>
+__device__ __forceinline__ void put_row(const BwdArgs& a, const Item& it, const Tile& tl, int within, int n, bool query,
+                                        void* dst, int64_t ld, float* part, const float (&g)[PER], float scale) {
+  const int row = tl.row0 + n, G = query ? a.G : 1, token = row / G, head = it.hk * G + row % G;
+  for (int c = 0; c < PER; ++c) {
+    const int d = lane_id() + 64 * c;
+    if (d >= DP) break;
+    if (it.slot >= 0) {
+      part[((int64_t(it.slot) * it.stride + within) * 32 + n) * DP + d] = g[c] * scale;
+      continue;
+    }
+    const int4 at = a.table[d];
+    if (at.w) from_acc(static_cast<T*>(dst)[int64_t(token) * ld + elem(at, query, head)], g[c] * scale);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ float rounded(float v) {
+  T t;
+  from_acc(t, v);
+  return to_acc<float>(t);
 }
 
 // grad_q: as the forward, a wave keeps 32 query rows and walks the key tiles:
@@ -1219,6 +1287,8 @@ __device__ __forceinline__ void dkv_item(const BwdArgs& a, const Item& it, u32x4
     if (WANT_K) v[t] = as_frag<Frag>(unit16(a.kforms<T>(kVRows) + kat, t, lane));
   }
   const float bias = a.bias[int64_t(kt) * 32 + n];
+  // causal: keys that all samples share are seen by every query
+  const bool later = SEQ && a.causal && kt >= a.shared;
   f32x16 dk[WANT_K ? D::DT : 1], dv[WANT_V ? D::DT : 1];
 #pragma unroll
   for (int d = 0; d < D::DT; ++d) {
@@ -1249,8 +1319,6 @@ __device__ __forceinline__ void dkv_item(const BwdArgs& a, const Item& it, u32x4
   for (int t = it.b0; t < it.b1; ++t) {
     const int buf = BUFS == 2 ? (t - it.b0) & 1 : 0;
     if (BUFS == 2 && t + 1 < it.b1) fetch(t + 1, buf ^ 1);
-    // keys that all samples share are seen by every query
-    const bool later = SEQ && a.causal && kt >= a.shared;
     bool some = true, all = true;
     if constexpr (SEQ)
       if (later) {
@@ -1352,6 +1420,133 @@ __global__ __launch_bounds__(kThreads, lds_waves(bwd_units<T, DP>())) void bwd_k
     if (a.dv) dkv_item<T, DP, 1, SEQ>(a, it, pool, rows, hidden);
   } else {
     if (a.dk) dkv_item<T, DP, 2, SEQ>(a, it, pool, rows, hidden);
+  }
+}
+
+template <typename T, int DP>
+__device__ __forceinline__ void redo_dq(const BwdArgs& a, const Item& it, const Reach& re, const Tile& tl, int within,
+                                        int64_t qat, uint32_t rows) {
+  constexpr int PER = (DP + 63) / 64, TILE = Dims<T, DP>::TILE;
+  const int lane = lane_id();
+  for (; rows; rows &= rows - 1) {
+    const int n = __builtin_ctz(rows);
+    if (n >= tl.n) return;
+    const float lse2 = a.rows[qat * 64 + n], delta = a.rows[qat * 64 + 32 + n];
+    if (lse2 != lse2) continue;  // (the formula's is NaN as well)
+    const int hidden = hidden_from(a, re, tl.row0 + n);
+    float q[PER], g[PER], dq[PER];
+#pragma unroll
+    for (int c = 0; c < PER; ++c) {
+      const bool in = lane + 64 * c < DP;
+      q[c] = in ? row_frag_at<T, DP>(a.qforms<T>(kQRows) + qat * TILE, n, lane + 64 * c) : 0.0f;
+      g[c] = in ? row_frag_at<T, DP>(a.qforms<T>(kGRows) + qat * TILE, n, lane + 64 * c) : 0.0f;
+      dq[c] = 0.0f;
+    }
+    for (int t = it.b0; t < it.b1; ++t) {
+      const int tile = key_tile<true>(a, re.skip, t);
+      const T* const kt = a.kforms<T>(kKRows) + (int64_t(tile) * a.groups + it.hk) * TILE;
+      const T* const vt = a.kforms<T>(kVRows) + (int64_t(tile) * a.groups + it.hk) * TILE;
+      const int seen = t < a.shared ? 32 : min(32, hidden - 32 * tile);
+      for (int r = 0; r < seen; ++r) {
+        if (a.bias[int64_t(tile) * 32 + r] < 0.0f) continue;
+        float k[PER], s = 0.0f, dp = 0.0f;
+#pragma unroll
+        for (int c = 0; c < PER; ++c) {
+          const int d = min(lane + 64 * c, DP - 1);
+          k[c] = row_frag_at<T, DP>(kt, r, d);
+          s += lane + 64 * c < DP ? q[c] * k[c] : 0.0f;
+          dp += lane + 64 * c < DP ? g[c] * row_frag_at<T, DP>(vt, r, d) : 0.0f;
+        }
+        const float p = exp2_fast(wave_sum(s) * a.scale2 - lse2);
+        const float ds = rounded<T>(p * (wave_sum(dp) - delta));
+#pragma unroll
+        for (int c = 0; c < PER; ++c) dq[c] += ds * k[c];
+      }
+    }
+    put_row<T, DP, PER>(a, it, tl, within, n, true, a.dq, a.ldq, a.part_q, dq, a.scale);
+  }
+}
+
+template <typename T, int DP>
+__device__ __forceinline__ void redo_dkv(const BwdArgs& a, const Item& it, const Tile& tl, int kt, bool want_k,
+                                         bool want_v, uint32_t rows) {
+  constexpr int PER = (DP + 63) / 64, TILE = Dims<T, DP>::TILE;
+  const int lane = lane_id();
+  const int64_t kat = (int64_t(kt) * a.groups + it.hk) * TILE;
+  for (; rows; rows &= rows - 1) {
+    const int n = __builtin_ctz(rows);
+    if (n >= tl.n) return;
+    if (a.bias[int64_t(kt) * 32 + n] < 0.0f) continue;
+    float k[PER], v[PER], dk[PER], dv[PER];
+#pragma unroll
+    for (int c = 0; c < PER; ++c) {
+      const int d = min(lane + 64 * c, DP - 1);
+      k[c] = row_frag_at<T, DP>(a.kforms<T>(kKRows) + kat, n, d);
+      v[c] = row_frag_at<T, DP>(a.kforms<T>(kVRows) + kat, n, d);
+      dk[c] = dv[c] = 0.0f;
+    }
+    for (int t = it.b0; t < it.b1; ++t) {
+      const int64_t at = int64_t(t) * a.groups + it.hk;
+      const Tile ql = ldc(a.qtiles + t);
+      const Reach re = ldc(a.reach + t);
+      for (int r = 0; r < ql.n; ++r) {
+        if (kt >= a.shared && 32 * kt + n >= hidden_from(a, re, ql.row0 + r)) continue;
+        float q[PER], g[PER], s = 0.0f, dp = 0.0f;
+#pragma unroll
+        for (int c = 0; c < PER; ++c) {
+          const int d = min(lane + 64 * c, DP - 1);
+          q[c] = row_frag_at<T, DP>(a.qforms<T>(kQRows) + at * TILE, r, d);
+          g[c] = row_frag_at<T, DP>(a.qforms<T>(kGRows) + at * TILE, r, d);
+          s += lane + 64 * c < DP ? q[c] * k[c] : 0.0f;
+          dp += lane + 64 * c < DP ? g[c] * v[c] : 0.0f;
+        }
+        const float p = exp2_fast(wave_sum(s) * a.scale2 - a.rows[at * 64 + r]);
+        const float ds = rounded<T>(p * (wave_sum(dp) - a.rows[at * 64 + 32 + r])), pt = rounded<T>(p);
+#pragma unroll
+        for (int c = 0; c < PER; ++c) {
+          dk[c] += ds * q[c];
+          dv[c] += pt * g[c];
+        }
+      }
+    }
+    const int within = kt - it.a0;
+    if (want_v && a.dv) put_row<T, DP, PER>(a, it, tl, within, n, false, a.dv, a.ldk, a.part_v, dv, 1.0f);
+    if (want_k && a.dk) put_row<T, DP, PER>(a, it, tl, within, n, false, a.dk, a.ldk, a.part_k, dk, a.scale);
+  }
+}
+
+// Causal batches: gradients of tiles that some keys or queries with infinities or NaN are
+// hidden from in part, formed again row by row after bwd_kernel wrote them, by workgroups for
+// the same items (hardly ever any: the kernel takes 4 us; a test for NaN at the end of
+// bwd_kernel cost it 10 us of 340 by the registers).
+template <typename T, int DP>
+__global__ __launch_bounds__(kThreads) void redo_kernel(BwdArgs a) {
+  const int wave = wave_id();
+  const Item it = ldc(a.items + blockIdx.x);
+  if (wave >= it.tiles) return;
+  bool bad = false;
+  if (it.kind == kItemQ) {
+    if (!a.dq) return;
+    const int qt = it.a0 + wave;
+    const Reach re = ldc(a.reach + qt);
+    const Tile tl = ldc(a.qtiles + qt);
+    const int part = hidden_from(a, re, tl.row0) >> 5;
+    for (int t = it.b1 - 1; t >= max(it.b0, a.shared); --t) {
+      const int tile = key_tile<true>(a, re.skip, t);
+      if (tile < part) break;
+      bad = bad || ldc(a.k_bad + int64_t(tile) * a.groups + it.hk) != 0;
+    }
+    if (bad) redo_dq<T, DP>(a, it, re, tl, wave, int64_t(qt) * a.groups + it.hk, ~0u);
+  } else {
+    constexpr bool kBoth = one_pass(DP, sizeof(T));
+    const bool want_k = a.dk && (kBoth || it.kind == kItemK), want_v = a.dv && (kBoth || it.kind == kItemV);
+    const int kt = it.a0 + wave;
+    if (kt < a.shared || !(want_k || want_v)) return;
+    for (int t = it.b0; t < it.b1; ++t) {
+      if (32 * kt + 31 < hidden_from(a, ldc(a.reach + t), ldc(a.qtiles + t).row0)) break;
+      bad = bad || ldc(a.q_bad + int64_t(t) * a.groups + it.hk) != 0;
+    }
+    if (bad) redo_dkv<T, DP>(a, it, ldc(a.ktiles + kt), kt, want_k, want_v, ~0u);
   }
 }
 

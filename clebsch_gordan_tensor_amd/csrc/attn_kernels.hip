@@ -32,6 +32,9 @@ constexpr int kCus = 256;
 // head of 128: 1095 us against 1183 us with 32)
 constexpr int kWideTiles = 8;
 
+// Key tiles up to which a query tile's rows see few keys (delta_kernel: a wave each).
+constexpr int kFewKeyTiles = 2;
+
 // One side of a batch cut into 32-row tiles, per sample, after those of `shared` rows
 // that come before the samples'.
 struct Side {
@@ -415,6 +418,7 @@ struct Backward {
   char *kforms, *qforms;  // at strides of kbytes and qbytes
   size_t kbytes, qbytes;
   float *bias, *rows, *part_q, *part_k, *part_v;
+  int32_t *k_bad, *q_bad;
   size_t bytes;
 };
 Backward carve_backward(const cgtp_attn_batch_s* b, void* p) {
@@ -432,6 +436,8 @@ Backward carve_backward(const cgtp_attn_batch_s* b, void* p) {
   x.part_q = static_cast<float*>(c.take(size_t(b->bwd.part_tiles[0]) * 32 * size_t(a->DP) * 4));
   x.part_k = static_cast<float*>(c.take(size_t(b->bwd.part_tiles[1]) * 32 * size_t(a->DP) * 4));
   x.part_v = static_cast<float*>(c.take(size_t(b->bwd.part_tiles[1]) * 32 * size_t(a->DP) * 4));
+  x.k_bad = static_cast<int32_t*>(c.take(b->causal ? size_t(b->ktiles) * g * 4 : 0));
+  x.q_bad = static_cast<int32_t*>(c.take(b->causal ? size_t(b->qtiles) * g * 4 : 0));
   x.bytes = c.used;
   return x;
 }
@@ -572,6 +578,15 @@ cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, co
   forward(b->few, 1, slots, 8, [&](int n) { return kernel(n) == 1; });
   std::vector<Unit> u;
   const auto all = [](int) { return true; };
+  if (b->sequence && at->seq.delta) {
+    std::vector<int4> tiles;
+    add_query_units(u, sight, 1, 1, 0, false, all);
+    for (const Unit& x : u)
+      if (x.b1 > x.b0 && x.b1 - x.b0 <= kFewKeyTiles) tiles.push_back({x.a0, x.b0, x.b1, 0});
+    u.clear();
+    b->few_keys = int(tiles.size());
+    b->few_keys_mem.upload(tiles.data(), tiles.size() * sizeof(int4));
+  }
   const bool one_kind = one_pass(at->DP, dtype_size(at->dtype));
   const std::vector<int32_t> kinds = one_kind ? std::vector<int32_t>{kItemV} : std::vector<int32_t>{kItemV, kItemK};
   if (b->sequence) {
@@ -907,7 +922,8 @@ void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn
     p.t[0].col_frags = dq ? w.kforms + kKCols * w.kbytes : nullptr;
     p.bias = w.bias;
     p.t[1].row_frags = w.kforms + kVRows * w.kbytes;
-    a->k.pack(p, s);
+    p.bad = w.k_bad;
+    (b->causal ? a->seq.pack : a->k.pack)(p, s);
     CGTP_CHECK_HIP(hipGetLastError());
   }
   if (b->qtiles) {
@@ -935,7 +951,8 @@ void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn
     p.heads = a->heads;
     p.groups = a->kv_heads;
     p.ntiles = int(b->qtiles);
-    a->k.pack(p, s);
+    p.bad = w.q_bad;
+    (b->causal ? a->seq.pack : a->k.pack)(p, s);
     CGTP_CHECK_HIP(hipGetLastError());
   }
   BwdArgs x{};
@@ -951,6 +968,8 @@ void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn
   x.reach = b->reach.as<Reach>();
   x.shared = int(b->shared_tiles);
   x.causal = b->causal;
+  x.k_bad = w.k_bad;
+  x.q_bad = w.q_bad;
   x.dq = dq;
   x.dk = dk;
   x.dv = dv;
@@ -968,6 +987,10 @@ void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn
   x.part_v = w.part_v;
   const WorkList& l = b->bwd;
   if (l.items == 0) return;
+  if (b->few_keys && (dq || dk)) {
+    a->seq.delta(x, b->few_keys_mem.as<int4>(), b->few_keys, w.rows, s);
+    CGTP_CHECK_HIP(hipGetLastError());
+  }
   x.items = l.item_mem.as<Item>();
   (b->sequence ? a->seq.bwd : a->k.bwd)(x, l.items, s);
   CGTP_CHECK_HIP(hipGetLastError());

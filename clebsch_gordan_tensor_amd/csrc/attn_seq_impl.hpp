@@ -591,10 +591,64 @@ __global__ __launch_bounds__(kThreads) void rows_join_kernel(RowsJoinArgs a) {
         s.l > 0.0f || s.l != s.l ? (ref + __log2f(s.e)) * 0.69314718055994531f : -INFINITY;
 }
 
+// --------------------------------------------------------------------- delta
+//
+// rowsum(grad_out out) of queries that see few keys, from its other form sum_j P_ij dP_ij:
+// the stored out is rounded to bf16, and where few keys share a row that rounding is as
+// large as the score gradients it is taken from (a causal training batch's grad_q and grad_k 0.0025
+// off, with this 0.0023). A workgroup takes a tile of query rows, a wave one of its key tiles.
+template <typename T, int DP>
+__global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void delta_kernel(BwdArgs a, const int4* tiles,
+                                                                                   float* rows) {
+  using D = Dims<T, DP>;
+  using Frag = typename Op<T>::Frag;
+  __shared__ float sums[4][64];
+  const int4 it = ldc(tiles + blockIdx.x);  // tile, first and end of its key tiles
+  const int hk = int(blockIdx.y), lane = lane_id(), n = lane % 32, h = lane / 32, wave = wave_id();
+  const Tile tl = ldc(a.qtiles + it.x);
+  const Reach re = ldc(a.reach + it.x);
+  const int64_t qat = int64_t(it.x) * a.groups + hk;
+  float sum = 0.0f;
+  if (it.y + wave < it.z) {
+    const int t = it.y + wave, tile = key_tile<true>(a, re.skip, t);
+    const int64_t at = (int64_t(tile) * a.groups + hk) * D::TILE;
+    const float lse2 = a.rows[qat * 64 + n];
+    f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+    for (int u = 0; u < D::KSTEPS; ++u) {
+      s = Op<T>::mma(as_frag<Frag>(unit16(a.kforms<T>(kKRows) + at, u, lane)),
+                     as_frag<Frag>(unit16(a.qforms<T>(kQRows) + qat * D::TILE, u, lane)), s);
+      dp = Op<T>::mma(as_frag<Frag>(unit16(a.kforms<T>(kVRows) + at, u, lane)),
+                      as_frag<Frag>(unit16(a.qforms<T>(kGRows) + qat * D::TILE, u, lane)), dp);
+    }
+    const int hidden = a.causal ? hidden_from(a, re, tl.row0 + min(n, tl.n - 1)) : INT_MAX;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = 8 * (i / 4) + 4 * h + i % 4;
+      const bool seen = (t < a.shared || 32 * tile + r < hidden) && a.bias[int64_t(tile) * 32 + r] >= 0.0f;
+      const float p = exp2_fast(s[i] * a.scale2 - lse2);
+      sum += seen ? p * dp[i] : 0.0f;
+    }
+    sum = half_sum(sum);
+  }
+  sums[wave][lane] = sum;
+  __syncthreads();
+  if (wave == 0 && h == 0) rows[qat * 64 + 32 + n] = sums[0][n] + sums[1][n] + (sums[2][n] + sums[3][n]);
+}
+
 // -------------------------------------------------------------------- launch
 
 template <typename T, int DP>
 struct SeqKernels {
+  static void pack(const PackArgs& a, hipStream_t s) {
+    const bool grads = a.rows_out != nullptr, vec = a.t[0].vec && a.t[1].vec && (!grads || a.out_vec);
+    const auto k = vec ? (grads ? pack_kernel<T, DP, true, true, true> : pack_kernel<T, DP, true, false, true>)
+                       : (grads ? pack_kernel<T, DP, false, true, true> : pack_kernel<T, DP, false, false, true>);
+    hipLaunchKernelGGL(k, dim3(unsigned((a.ntiles + 7) / 8 * 8 * a.groups)), dim3(kThreads), 0, s, a);
+  }
+  static void delta(const BwdArgs& a, const int4* tiles, int count, float* rows, hipStream_t s) {
+    hipLaunchKernelGGL((delta_kernel<T, DP>), dim3(unsigned(count), unsigned(a.groups)), dim3(kThreads), 0, s, a, tiles, rows);
+  }
   static void fwd(const FwdArgs& a, int items, int tiles, hipStream_t s) {
     if (tiles == 1) hipLaunchKernelGGL((fwd_few_kernel<T, DP, true>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
     if (tiles == 4) hipLaunchKernelGGL((fwd_kernel<T, DP, 1, true>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
@@ -603,6 +657,7 @@ struct SeqKernels {
   }
   static void bwd(const BwdArgs& a, int items, hipStream_t s) {
     hipLaunchKernelGGL((bwd_kernel<T, DP, true>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
+    if (a.causal) hipLaunchKernelGGL((redo_kernel<T, DP>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
   }
   static void step(const StepArgs& a, hipStream_t s) {
     const unsigned groups = a.whole ? unsigned(a.cut.slots) * unsigned(a.cut.tiles_a_slot) : unsigned(a.cut.shares);
@@ -623,7 +678,10 @@ struct SeqKernels {
   static void rows_join(const RowsJoinArgs& a, int joins, hipStream_t s) {
     hipLaunchKernelGGL((rows_join_kernel<T, DP>), dim3(unsigned(joins), DP / 32), dim3(kThreads), 0, s, a);
   }
-  static SeqTable table() { return {fwd, bwd, step, rows_join}; }
+  static SeqTable table() {
+    if constexpr (sizeof(T) == 2) return {pack, fwd, bwd, step, rows_join, delta};
+    else return {pack, fwd, bwd, step, rows_join, nullptr};
+  }
 };
 
 }  // namespace attn

@@ -49,8 +49,6 @@ CASES = [
     ("16x0e", 4, 2, [300, 1, 9], [300, 1, 40], True, 1000),
     ("64x0e", 1, 1, [300, 270, 1], [300, 0, 70], True, 200),                     # 64 rows a wave
     ("64x0e", 2, 2, [70, 10, 5], [33, 2, 0], True, 3),
-    ("128x0e+128x1o", 8, 2, [1, 2, 1, 0] * 8, [1, 20, 0, 7] * 8, True, 9000),    # joined by rows
-    ("128x0e+128x1o+128x2e+128x3o", 16, 4, [1] * 40, [3] * 40, False, 8100),     # joined by rows, 32 a wave
     ("64x0e", 1, 1, [1, 300, 40, 0, 31], [1, 300, 40, 0, 31], True, 0),          # one kernel for all
     ("64x0e", 1, 1, [1, 300, 40], [1, 300, 900], True, 0),                       # two
 ]
@@ -102,6 +100,39 @@ def test_sequence_attention(case, dtype):
     a = check(attn, case, dtype, q, k, v, g)
     b = check(attn, case, dtype, q, k, v, g)
     assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("irreps,heads,kv_heads,nq,nk,causal,shared", [
+    ("128x0e+128x1o", 8, 2, [1, 2, 1, 0] * 16, [1, 20, 0, 7] * 16, True, 9000),
+    ("128x0e+128x1o+128x2e+128x3o", 16, 4, [1] * 40, [3] * 40, False, 8100),
+    ("128x0e+128x1o+128x2e+128x3o", 16, 16, [1] * 30, [1, 300, 40] * 10, True, 4000)])
+def test_few_rows_of_many_samples_on_long_shared_rows(irreps, heads, kv_heads, nq, nk, causal, shared, dtype):
+    """(these go against the shared rows together) against the definition in 64 bits"""
+    attn, q, k, v, g = make((irreps, heads, kv_heads, nq, nk, causal, shared), dtype)
+    qp, kp = ptr_of(nq), ptr_of(nk)
+    mask = torch.rand(shared + sum(nk), device="cuda", generator=torch.Generator("cuda").manual_seed(3)) < 0.9
+    batch = attn.batch(layers.Samples(qp), layers.Samples(kp), causal=causal, shared=shared)
+    out, lse = attn.forward(batch, q, k, v, key_mask=mask, need_lse=True)
+    again = attn.forward(batch, q, k, v, key_mask=mask)
+    torch.cuda.synchronize()
+    assert torch.equal(out, again)
+    want, want_lse = torch.zeros(out.shape, dtype=torch.float64, device="cuda"), torch.zeros_like(lse, dtype=torch.float64)
+    kvi = ol.kv_irreps(irreps, heads, kv_heads)
+    for h in range(heads):
+        qc = torch.from_numpy(ol.head_columns(irreps, heads, h)).cuda()
+        kc = torch.from_numpy(ol.head_columns(kvi, kv_heads, h * kv_heads // heads)).cuda()
+        qh, kh, vh = q[:, qc].double(), k[:, kc].double(), v[:, kc].double()
+        for s in range(len(nq)):
+            for i in range(nq[s]):
+                n = max(0, i + nk[s] - nq[s] + 1) if causal else nk[s]
+                keys = torch.cat([torch.arange(shared, device="cuda"), shared + kp[s] + torch.arange(n, device="cuda")])
+                keys = keys[mask[keys]]
+                w = kh[keys] @ qh[qp[s] + i] * attn.scale
+                want[qp[s] + i, qc] = torch.softmax(w, 0) @ vh[keys]
+                want_lse[qp[s] + i, h] = torch.logsumexp(w, 0)
+    assert rel_err(host(out), want.cpu().numpy()) <= TOL[dtype]
+    assert (lse.double() - want_lse).abs().max().item() <= 2e-5
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -166,6 +197,44 @@ def test_what_later_keys_hold_does_not_reach_earlier_queries(irreps, heads, kv_h
             assert torch.equal(lse, want_lse)     # the values have no part in it
         else:
             assert np.isnan(behind).any(1).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("irreps,heads,kv_heads,lens,shared", [
+    ("32x0e+16x1o", 4, 2, [70, 9], 0), ("64x0e", 1, 1, [500, 3], 33), ("64x0e", 2, 2, [1500], 0),
+    ("128x0e+128x1o+128x2e", 8, 4, [50, 90], 0), ("10x0e+6x1o", 2, 1, [40, 9], 7)])
+def test_nan_does_not_reach_gradients_that_do_not_depend_on_it(irreps, heads, kv_heads, lens, shared, dtype):
+    case = (irreps, heads, kv_heads, lens, lens, True, shared)
+    clean = make(case, dtype)
+    attn = clean[0]
+    samples = layers.Samples(ptr_of(lens))
+    batch = attn.batch(samples, samples, causal=True, shared=shared)
+    at = lens[0] - 10                                 # tokens before and behind it share its tile
+
+    def grads(q, k, v, g):
+        out, lse = attn.forward(batch, q, k, v, need_lse=True)
+        return attn.backward(batch, q, k, v, out, lse, g)
+
+    want = grads(*clean[1:])
+    n = sum(lens)
+    rows, keys = torch.arange(n, device="cuda"), torch.arange(shared + n, device="cuda") - shared
+    for which in range(4):                            # q, k, v, grad_out of token `at`
+        args = [t.clone() for t in clean[1:]]
+        args[which][at + (shared if which in (1, 2) else 0), 3] = float("nan")
+        got = grads(*args)
+        torch.cuda.synchronize()
+        if which in (0, 3):                           # a query reaches its own gradient, and the keys that it sees
+            free = (rows != at, keys > at, keys > at)
+        else:                                         # a key reaches the queries that see it, and by them all their keys
+            free = (rows < at, keys >= lens[0], keys >= lens[0])
+            free = ((rows < at) | (rows >= lens[0]),) + free[1:]
+        for i, (a, b, m) in enumerate(zip(got, want, free)):
+            if m.any():
+                # as two results of one type, each off by its tolerance against the formula
+                scale = b.float().abs().max().item()
+                assert (a[m].float() - b[m].float()).abs().max().item() <= 2 * TOL[dtype] * scale, (which, i)
+        bad = (got[0][at], got[0][at:lens[0]], got[0][at:lens[0]], got[1][shared])[which]
+        assert torch.isnan(bad).any()
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
