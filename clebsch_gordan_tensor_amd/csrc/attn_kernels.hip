@@ -199,6 +199,7 @@ void need_launch(int64_t workgroups) {
 struct How {
   bool all_parts = false;  // every result is a part, also that of an unsplit unit
   bool uneven = false;     // the items of a group differ in length (causal queries)
+  bool spread = false;     // and go to the dies one by one, not in runs of a group
   int part_extra = 5;      // of part_cost
   int64_t cost = 0;        // largest cost of a part, where it is known
 };
@@ -249,7 +250,7 @@ int64_t build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, i
 
   // long and short items in turn, so that every run of them has alike shares of both, and
   // then every die's longest first (long causal prompts 782 us without, 744 us with both)
-  if (how.uneven)
+  if (how.uneven && !how.spread)
     for (Group& g : gs) {
       std::vector<size_t> by(g.items.size());
       std::iota(by.begin(), by.end(), size_t(0));
@@ -271,6 +272,21 @@ int64_t build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, i
   std::vector<size_t> order(gs.size());
   std::iota(order.begin(), order.end(), size_t(0));
   std::stable_sort(order.begin(), order.end(), [&](size_t a, size_t b) { return gs[a].longest > gs[b].longest; });
+  // Gradients: the longest item to the least loaded die (us with and without: one fp32
+  // trajectory 510 and 534, a training batch with shared rows 276 and 288; the forward's
+  // chunk after earlier rows 157 and 154)
+  if (how.spread) {
+    std::vector<std::pair<int64_t, const Item*>> all;
+    for (size_t gi : order)
+      for (size_t k = 0; k < gs[gi].items.size(); ++k) all.push_back({gs[gi].costs[k], &gs[gi].items[k]});
+    std::stable_sort(all.begin(), all.end(), [](const auto& a, const auto& b) { return a.first > b.first; });
+    for (const auto& x : all) {
+      const size_t d = size_t(std::min_element(load.begin(), load.end()) - load.begin());
+      queue[d].push_back(*x.second);
+      load[d] += x.first;
+    }
+    order.clear();
+  }
   for (size_t gi : order) {
     const Group& g = gs[gi];
     size_t at = 0;
@@ -286,7 +302,7 @@ int64_t build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, i
       }
     }
   }
-  if (how.uneven)
+  if (how.uneven && !how.spread)
     for (size_t x = 0; x < size_t(kXcds); ++x) {
       std::vector<size_t> by(queue[x].size());
       std::iota(by.begin(), by.end(), size_t(0));
@@ -346,7 +362,7 @@ void build_joint(JointPlan& j, const cgtp_attn_s* at, int64_t tokens, int64_t sh
   const int slots = j.per == 8 ? 2 * kCus : forward_slots(at);
   const double turn = (es == 2 ? 1.0 : 3.5) * at->DP / 128 * (j.per == 8 ? 2 : 1);
   const double part = double(n) * 32 * at->kv_heads * at->DP * 8 / 5e6;  // us
-  How how{true, false, 0, shared_tiles};
+  How how{true, false, false, 0, shared_tiles};
   double best = 1e30;
   for (int64_t p = 1; p <= std::min<int64_t>(64, (shared_tiles + 1) / 2); ++p) {
     const int64_t len = (shared_tiles + p - 1) / p, items = int64_t(j.units) * at->kv_heads * p;
@@ -546,7 +562,7 @@ cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, co
       add_query_units(u, sight, per, 1, 0, joint, take);
     else
       add_units(u, qs, ks, 0, per, 1, {0}, take);
-    build(w, u, per, g, slots, min_len, {joint, causal, b->sequence ? part_extra(at, per) : 5});
+    build(w, u, per, g, slots, min_len, {joint, causal, false, b->sequence ? part_extra(at, per) : 5});
   };
   // the items' tiles by a sample's: one, some, many
   int one_tile = 1, some = 4, many = 8;
@@ -596,7 +612,7 @@ cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, co
     add_units(u, qs, ks, 0, 4, 3, {kItemQ}, all);
     add_units(u, ks, qs, 1, 4, one_kind ? 4 : 3, kinds, all);
   }
-  build(b->bwd, u, 4, g, at->DP * es <= 384 ? two : one, 4, {false, causal, b->sequence ? part_extra(at, 4) : 5});
+  build(b->bwd, u, 4, g, at->DP * es <= 384 ? two : one, 4, {false, causal, causal});
   return b.release();
 }
 
