@@ -104,7 +104,13 @@ struct FwdArgs {
 struct StepCut {
   const int32_t* lengths;  // NULL: no step
   int slots, capacity, tiles_a_slot, waves_a_head, shares, min_turns;
+  // turns before every slot and in all, [slots + 1], written by SeqTable::step_sums where
+  // there are many slots; NULL: every wave adds the lengths up itself
+  int32_t* before;
 };
+// Slots from which a kernel of its own adds the lengths up (4096 short sequences: a join of
+// 16,000 workgroups that each read 16 KB of lengths else).
+constexpr int kStepSumSlots = 256;
 
 // Joins the results of rows against their own context (`own`: the parts of its joins, or
 // of a step) with those against rows that all samples share (parts of tiles of 32
@@ -200,6 +206,7 @@ struct SeqTable {
   void (*pack)(const PackArgs&, hipStream_t);  // for the gradients of causal batches
   void (*fwd)(const FwdArgs&, int items, int tiles, hipStream_t);
   void (*bwd)(const BwdArgs&, int items, hipStream_t);
+  void (*step_sums)(const StepCut&, hipStream_t);
   void (*step)(const StepArgs&, hipStream_t);
   void (*rows_join)(const RowsJoinArgs&, int joins, hipStream_t);
   // of `count` query tiles (with the key tiles that they see), for every context head; NULL in fp32

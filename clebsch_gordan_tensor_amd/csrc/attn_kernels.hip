@@ -793,14 +793,14 @@ void joint_launch(const cgtp_attn_s* a, const JointPlan& j, FwdArgs f, const Row
   CGTP_CHECK_HIP(hipGetLastError());
 }
 
-StepCut step_cut(const cgtp_attn_cache_s* c, const int32_t* lengths) {
-  return {lengths, int(c->slots), int(c->capacity), c->tiles_a_slot, c->waves_a_head, c->shares, c->min_turns};
+StepCut step_cut(const cgtp_attn_cache_s* c, const int32_t* lengths, int32_t* before) {
+  return {lengths,         int(c->slots), int(c->capacity), c->tiles_a_slot,
+          c->waves_a_head, c->shares,     c->min_turns,     before};
 }
 
 void rows_join_launch(const cgtp_attn_s* a, const JointPlan& j, const FwdArgs& own, const RowParts& w, int joins,
-                      const cgtp_attn_cache_s* c, const int32_t* lengths, hipStream_t s) {
-  RowsJoinArgs r{own, w.joint, w.joint_ml, j.units, j.per, j.per ? j.parts : 0, {}};
-  if (c) r.cut = step_cut(c, lengths);
+                      const StepCut& cut, hipStream_t s) {
+  const RowsJoinArgs r{own, w.joint, w.joint_ml, j.units, j.per, j.per ? j.parts : 0, cut};
   a->seq.rows_join(r, joins, s);
   CGTP_CHECK_HIP(hipGetLastError());
 }
@@ -830,7 +830,7 @@ void attn_forward_launch(const cgtp_attn_batch_s* b, RowsIn q, const void* conte
     f.part_ml = w.own_ml;
     a->seq.fwd(f, b->few.items, 1, s);
     CGTP_CHECK_HIP(hipGetLastError());
-    rows_join_launch(a, b->joint, f, w, b->few.joins[0], nullptr, nullptr, s);
+    rows_join_launch(a, b->joint, f, w, b->few.joins[0], {}, s);
     return;
   }
   f.part_ml = static_cast<float4*>(ws);
@@ -860,7 +860,17 @@ RowParts carve_step(const cgtp_attn_cache_s* c, void* ws) {
 }
 }  // namespace
 
-size_t attn_step_ws_bytes(const cgtp_attn_cache_s* c) { return carve_step(c, nullptr).bytes; }
+namespace {
+// StepCut::before, behind the partial results
+bool step_sums(const cgtp_attn_cache_s* c) { return !c->whole && c->slots >= kStepSumSlots; }
+int32_t* step_before(const cgtp_attn_cache_s* c, void* ws) {
+  return step_sums(c) ? reinterpret_cast<int32_t*>(static_cast<char*>(ws) + carve_step(c, nullptr).bytes) : nullptr;
+}
+}  // namespace
+
+size_t attn_step_ws_bytes(const cgtp_attn_cache_s* c) {
+  return carve_step(c, nullptr).bytes + (step_sums(c) ? size_t(c->slots + 1) * 4 : 0);
+}
 
 void attn_share_launch(const cgtp_attn_cache_s* c, RowsIn k, RowsIn v, const uint8_t* mask, void* context,
                        hipStream_t s) {
@@ -896,7 +906,11 @@ void attn_step_launch(const cgtp_attn_cache_s* c, RowsIn q, RowsIn k, RowsIn v, 
   x.k_cache = k_cache;
   x.v_cache = v_cache;
   x.dim = a->krow.dim;
-  x.cut = step_cut(c, lengths);
+  x.cut = step_cut(c, lengths, step_before(c, ws));
+  if (x.cut.before) {
+    a->seq.step_sums(x.cut, s);
+    CGTP_CHECK_HIP(hipGetLastError());
+  }
   x.size = a->D;
   x.heads_a_group = c->heads_a_group;
   x.bundles = c->bundles;
@@ -924,7 +938,7 @@ void attn_step_launch(const cgtp_attn_cache_s* c, RowsIn q, RowsIn k, RowsIn v, 
   }
   a->seq.step(x, s);
   CGTP_CHECK_HIP(hipGetLastError());
-  if (!x.whole) rows_join_launch(a, c->joint, f, w, c->joins, c, lengths, s);
+  if (!x.whole) rows_join_launch(a, c->joint, f, w, c->joins, x.cut, s);
 }
 
 void attn_backward_launch(const cgtp_attn_batch_s* b, RowsIn q, RowsIn k, RowsIn v, const uint8_t* mask, double scale,

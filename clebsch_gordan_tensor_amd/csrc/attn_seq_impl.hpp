@@ -117,6 +117,11 @@ struct StepTurns {
 };
 __device__ __forceinline__ StepTurns step_sum(const StepCut& c) {
   StepTurns s;
+  if (c.before) {
+    s.mine = s.upto = s.each = 0;
+    s.total = ldc(c.before + c.slots);
+    return s;
+  }
   s.each = (c.slots + 63) / 64;
   s.mine = 0;
   const int first = lane_id() * s.each, end = min(first + s.each, c.slots);
@@ -132,6 +137,7 @@ __device__ __forceinline__ int step_share(const StepCut& c, int total) {
 }
 // Turns before slot `slot`.
 __device__ __forceinline__ int step_before(const StepCut& c, const StepTurns& s, int slot) {
+  if (c.before) return ldc(c.before + slot);
   const int run = slot / s.each;
   int n = __builtin_amdgcn_readlane(s.upto - s.mine, run);
   for (int i = run * s.each; i < slot; ++i) n += step_turns(c, ldc(c.lengths + i)) * c.tiles_a_slot;
@@ -139,6 +145,15 @@ __device__ __forceinline__ int step_before(const StepCut& c, const StepTurns& s,
 }
 // The slot that turn `at` (below the total) belongs to, and its first turn.
 __device__ __forceinline__ int2 step_find(const StepCut& c, const StepTurns& s, int at) {
+  if (c.before) {
+    // the last slot that begins at or before it
+    int lo = 0, hi = c.slots;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      (ldc(c.before + mid) <= at ? lo : hi) = mid;
+    }
+    return make_int2(lo, ldc(c.before + lo));
+  }
   const int run = __builtin_ctzll(__ballot(s.upto > at));
   int slot = run * s.each, n = __builtin_amdgcn_readlane(s.upto - s.mine, run);
   while (true) {
@@ -147,6 +162,26 @@ __device__ __forceinline__ int2 step_find(const StepCut& c, const StepTurns& s, 
     n += turns;
     ++slot;
   }
+}
+
+// StepCut::before, by one workgroup.
+constexpr int kSumThreads = 1024;
+static __global__ __launch_bounds__(kSumThreads) void step_sums_kernel(StepCut c) {
+  __shared__ int waves[kSumThreads / 64];
+  const int tid = int(threadIdx.x), each = (c.slots + kSumThreads - 1) / kSumThreads;
+  const int first = min(tid * each, c.slots), end = min(first + each, c.slots);
+  int mine = 0;
+  for (int i = first; i < end; ++i) mine += step_turns(c, c.lengths[i]) * c.tiles_a_slot;
+  const int upto = wave_scan(mine);
+  if (tid % 64 == 63) waves[tid / 64] = upto;
+  __syncthreads();
+  int n = upto - mine;
+  for (int k = 0; k < tid / 64; ++k) n += waves[k];
+  for (int i = first; i < end; ++i) {
+    c.before[i] = n;
+    n += step_turns(c, c.lengths[i]) * c.tiles_a_slot;
+  }
+  if (tid == kSumThreads - 1) c.before[c.slots] = n;
 }
 
 // The part of workgroup `index` and tile of rows qt.
@@ -640,6 +675,9 @@ __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void delta_kern
 
 template <typename T, int DP>
 struct SeqKernels {
+  static void step_sums(const StepCut& c, hipStream_t s) {
+    hipLaunchKernelGGL(step_sums_kernel, dim3(1), dim3(kSumThreads), 0, s, c);
+  }
   static void pack(const PackArgs& a, hipStream_t s) {
     const bool grads = a.rows_out != nullptr, vec = a.t[0].vec && a.t[1].vec && (!grads || a.out_vec);
     const auto k = vec ? (grads ? pack_kernel<T, DP, true, true, true> : pack_kernel<T, DP, true, false, true>)
@@ -679,8 +717,8 @@ struct SeqKernels {
     hipLaunchKernelGGL((rows_join_kernel<T, DP>), dim3(unsigned(joins), DP / 32), dim3(kThreads), 0, s, a);
   }
   static SeqTable table() {
-    if constexpr (sizeof(T) == 2) return {pack, fwd, bwd, step, rows_join, delta};
-    else return {pack, fwd, bwd, step, rows_join, nullptr};
+    if constexpr (sizeof(T) == 2) return {pack, fwd, bwd, step_sums, step, rows_join, delta};
+    else return {pack, fwd, bwd, step_sums, step, rows_join, nullptr};
   }
 };
 

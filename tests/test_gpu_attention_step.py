@@ -42,12 +42,15 @@ CASES = [
     ("128x0e+128x1o+128x2e+128x3o", 8, 8, [500, 9, 31, 470], 600, 0),        # 256, shared out
     ("35x0e+21x1o+7x2e", 7, 1, [100, 3, 900, 0, 64], 1000, 0),
     ("32x0e+32x1o+32x2e", 8, 2, [100, 3, 500, 0, 64], 600, 0),               # runs of 8 bytes in bf16
+    ("64x0e", 4, 2, [0, 130, -1, 7] * 300, 131, 0),                          # lengths added up beforehand
+    ("64x0e", 64, 1, [-1, 40, 200] * 100, 201, 30),
     ("64x0e", 4, 2, [-1, -1, 300], 300, 0),                                  # nobody
     ("8x0e", 1, 1, [0], 1, 1),
     ("32x0e+32x1o+32x2e", 4, 2, [5, 0, -1, 30, 40], 40, 50),
     ("35x0e+21x1o+7x2e", 7, 1, [100, 3], 101, 333),
     ("64x0e", 8, 1, list(range(40)), 64, 700),                               # 64 rows a wave against the shared
     ("128x0e+128x1o+128x2e+128x3o", 16, 4, [3, 70], 100, 1000),
+    ("128x0e+128x1o+128x2e", 8, 4, [3, 70, 200], 300, 200),                  # fp32: two launches
 ]
 
 
