@@ -617,8 +617,6 @@ cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, co
 }
 
 namespace {
-// Key tiles of a cache up to which a slot is one workgroup's.
-constexpr int kWholeTiles = 4;
 // Workgroups of a step that a compute unit holds at once, by their shared memory.
 int64_t step_workgroups(int dp, size_t es) {
   const int64_t bytes = step_waves(dp, es) * 32 * int64_t(dp) * int64_t(es) * 5 / 2;
@@ -650,18 +648,22 @@ cgtp_attn_cache_s* build_attn_cache(cgtp_attn_s* at, int64_t slots, int64_t capa
   const int waves = step_waves(at->DP, es);
   const int64_t tiles = (capacity + 31) / 32;
   if (c->qtiles * tiles > 1 << 30) throw Error{CGTP_ERR_UNSUPPORTED, "attention cache: more than 2^30 tiles of 32 places"};
-  // short caches: a workgroup a slot, in one launch (8 slots of up to 64 places: 16.8 us, with
-  // a share of two workgroups each and the join 18.5 us)
-  c->whole = shared == 0 && tiles <= kWholeTiles;
-  const int whole_waves = tiles >= 4 ? 4 : tiles >= 2 ? 2 : 1;
+  // Short caches of few slots: a workgroup a slot and head or two, in one launch (us so and shared
+  // out: 8 slots of up to 64 places of heads of 72 in fp32 15 and 30; 32 slots of 256 of heads of
+  // 128 in bf16 17 and 20, of 512 21 and 21; 200 slots of 128 38 and 36)
+  const int64_t at_once = kCus * step_workgroups(at->DP, es);
+  const int whole_waves = std::min(waves, tiles >= 4 ? 4 : tiles >= 2 ? 2 : 1);
+  const int whole_heads = std::min(waves / whole_waves, at->kv_heads);
+  c->whole = shared == 0 && tiles <= 2 * waves &&
+             c->qtiles * ((at->kv_heads + whole_heads - 1) / whole_heads) <= at_once / 2;
   // neighbouring heads on the waves of a workgroup; where there are fewer heads than waves,
   // a head's waves take tiles in turn
-  c->heads_a_group = std::min(c->whole ? std::max(1, waves / whole_waves) : waves, at->kv_heads);
-  c->waves_a_head = c->whole ? std::min(waves, whole_waves) : waves / c->heads_a_group;
+  c->heads_a_group = c->whole ? whole_heads : std::min(waves, at->kv_heads);
+  c->waves_a_head = c->whole ? whole_waves : waves / c->heads_a_group;
   c->bundles = (at->kv_heads + c->heads_a_group - 1) / c->heads_a_group;
   // as many workgroups as the device works on at once, each with two turns or more (64
-  // sequences of up to 8000 tokens, heads of 128 in bf16: 133 us, with twice as many 139 us)
-  c->shares = int(std::max<int64_t>(1, kCus * step_workgroups(at->DP, es) / c->bundles));
+  // sequences of up to 8000 tokens, heads of 128 in bf16: 124 us, with twice as many 130 us)
+  c->shares = int(std::max<int64_t>(1, at_once / c->bundles));
   c->min_turns = 2;
   const int64_t workgroups = (std::max<int64_t>(c->qtiles, c->shares) + 7) / 8 * 8 * c->bundles;
   if (step_part_rows(c.get()) > INT32_MAX) throw Error{CGTP_ERR_UNSUPPORTED, "attention: too many partial rows"};
