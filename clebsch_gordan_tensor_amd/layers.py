@@ -1,5 +1,5 @@
 """ctypes binding of the layers on irreps rows (include/cgtp_layers.h): group
-norm with its activation, cross attention to a context, dropout.
+norm with its activation, attention to a context and along sequences, dropout.
 
 As clebsch_gordan_tensor_amd.cgtp: this module checks shapes, dtypes and
 devices, allocates outputs and workspaces with torch when the caller passes

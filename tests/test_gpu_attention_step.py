@@ -210,6 +210,24 @@ def test_captured_steps_count_on(shared):
     assert torch.all(got[2] == 0)
 
 
+def test_caches_of_more_elements_than_32_bits_count():
+    irreps, heads, lens = "128x0e+128x1o+128x2e+128x3o", 16, [5, 300, 20]
+    case = (irreps, heads, heads, lens, 320, 0)
+    attn, cache, q, k, v, lengths, common = setup(case, "bf16")
+    big = attn.cache(3, 400000)                        # 2.5e9 elements each
+    for a, b in ((cache.k, big.k), (cache.v, big.v)):
+        b[:, :320] = a
+    want, got = attn.step(cache, q, k, v, lengths), attn.step(big, q, k, v, lengths)
+    torch.cuda.synchronize()
+    assert rel_err(host(got), host(want)) <= TOL["bf16"]
+    for s, n in enumerate(lens):
+        assert torch.equal(big.k[s, :n + 2], cache.k[s, :n + 2]) and torch.equal(big.v[s, n], v[s])
+    far = torch.tensor([-1, 0, 399999], dtype=torch.int32, device="cuda")
+    attn.step(big, q, k, v, far)                       # the last place of all
+    torch.cuda.synchronize()
+    assert torch.equal(big.k[2, 399999], k[2]) and torch.equal(big.v[1, 0], v[1])
+
+
 def test_two_streams_with_a_cache_each():
     case = ("32x0e+16x1o", 4, 2, [0, 5, 70], 90, 33)
     states = [setup(case, "bf16", seed) for seed in range(2)]

@@ -374,6 +374,36 @@ def test_captured_training_step_and_streams(shared):
         assert all(torch.equal(x, y) for x, y in zip(want, got))
 
 
+def test_a_packed_context_serves_other_queries():
+    case = ("64x0e", 4, 2, [9, 40], [90, 70], True, 33)
+    for dtype in ("f32", "bf16"):
+        attn, q, k, v, g = make(case, dtype)
+        ctx = layers.Samples([0, 90, 160])
+        a = attn.batch(layers.Samples([0, 9, 49]), ctx, causal=True, shared=33)
+        b = attn.batch(layers.Samples([0, 1, 2]), ctx, causal=True, shared=33)
+        packed = attn.pack(a, k, v)
+        whole = attn.forward_packed(a, q, packed)
+        last = attn.forward_packed(b, q[[8, 48]].contiguous(), packed)
+        torch.cuda.synchronize()
+        # (the same keys by another kernel: its sums' order)
+        assert rel_err(host(last), host(whole[[8, 48]])) <= TOL[dtype]
+
+
+def test_batches_without_samples_or_rows():
+    attn = layers.CrossAttention("32x0e", 4)
+    none, empty = layers.Samples([0]), layers.Samples([0, 0, 0])
+    k = torch.ones((3, 32), device="cuda")
+    for samples in (none, empty):
+        for causal in (False, True):
+            b = attn.batch(samples, samples, causal=causal, shared=3)
+            q = torch.zeros((0, 32), device="cuda")
+            out, lse = attn.forward(b, q, k, k, need_lse=True)
+            dq, dk, dv = attn.backward(b, q, k, k, out, lse, q)
+            torch.cuda.synchronize()
+            assert out.shape == (0, 32) and dq.shape == (0, 32)
+            assert torch.all(dk == 0) and torch.all(dv == 0)      # nobody reads the shared rows
+
+
 def test_refusals():
     attn = layers.CrossAttention("32x0e", 4)
     s, t = layers.Samples([0, 5]), layers.Samples([0, 3, 7])
