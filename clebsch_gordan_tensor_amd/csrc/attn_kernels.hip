@@ -143,7 +143,7 @@ int64_t parts_of(const Unit& x, int64_t cost) {
 // partial result and the join (5 of batches whose samples' queries all see the same
 // keys; measured: parts of a ragged batch cut to twice the number cost as much as the better balance gained). Parts have at least
 // min_len tiles, and batches with many more items than places are not split.
-int64_t part_cost(const std::vector<Unit>& u, int groups, int slots, int min_len, int part_extra) {
+int64_t part_cost(const std::vector<Unit>& u, int groups, int slots, int min_len, int part_extra, bool sequence) {
   int64_t longest = 1, count = 0;
   int weight = 1;
   for (const Unit& x : u) {
@@ -178,6 +178,8 @@ int64_t part_cost(const std::vector<Unit>& u, int groups, int slots, int min_len
       best_end = end;
       best = cost;
     }
+    // (sequences: near enough to an even share of everything; long prompts are planned in 0.75 ms so)
+    if (sequence && best_end * slots * 32 <= std::accumulate(costs.begin(), costs.end(), int64_t(0)) * 33) break;
   }
   return best;
 }
@@ -202,13 +204,14 @@ struct How {
   bool spread = false;     // and go to the dies one by one, not in runs of a group
   int part_extra = 5;      // of part_cost
   int64_t cost = 0;        // largest cost of a part, where it is known
+  bool sequence = false;   // of a sequence batch
 };
 int64_t build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, int slots, int min_len,
               const How& how = {}) {
   int64_t whole = 0;
   for (const Unit& x : u) whole += int64_t(x.kinds.size()) * groups;
   need_launch(whole);  // (before the lists are laid out)
-  const int64_t cost = how.cost ? how.cost : part_cost(u, groups, slots, min_len, how.part_extra);
+  const int64_t cost = how.cost ? how.cost : part_cost(u, groups, slots, min_len, how.part_extra, how.sequence);
   struct Group {
     int64_t work = 0, longest = 0;
     std::vector<Item> items;
@@ -321,12 +324,12 @@ int64_t build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, i
   while (!items.empty() && items.back().tiles == 0) items.pop_back();
   need_launch(int64_t(items.size()));
   w.items = int(items.size());
-  w.item_mem.upload(items.data(), items.size() * sizeof(Item));
+  if (!items.empty()) w.item_mem.upload(items.data(), items.size() * sizeof(Item));
   for (int k = 0; k < 2; ++k) {
     w.part_tiles[k] = nslot[k] * stride;
     if (w.part_tiles[k] > INT32_MAX / 32) throw Error{CGTP_ERR_UNSUPPORTED, "attention: too many partial tiles"};
     w.joins[k] = int(joins[k].size());
-    w.join_mem[k].upload(joins[k].data(), joins[k].size() * sizeof(Join));
+    if (!joins[k].empty()) w.join_mem[k].upload(joins[k].data(), joins[k].size() * sizeof(Join));
   }
   return most;
 }
@@ -562,7 +565,7 @@ cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, co
       add_query_units(u, sight, per, 1, 0, joint, take);
     else
       add_units(u, qs, ks, 0, per, 1, {0}, take);
-    build(w, u, per, g, slots, min_len, {joint, causal, false, b->sequence ? part_extra(at, per) : 5});
+    build(w, u, per, g, slots, min_len, {joint, causal, false, b->sequence ? part_extra(at, per) : 5, 0, b->sequence});
   };
   // the items' tiles by a sample's: one, some, many
   int one_tile = 1, some = 4, many = 8;
@@ -601,7 +604,7 @@ cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, co
       if (x.b1 > x.b0 && x.b1 - x.b0 <= kFewKeyTiles) tiles.push_back({x.a0, x.b0, x.b1, 0});
     u.clear();
     b->few_keys = int(tiles.size());
-    b->few_keys_mem.upload(tiles.data(), tiles.size() * sizeof(int4));
+    if (!tiles.empty()) b->few_keys_mem.upload(tiles.data(), tiles.size() * sizeof(int4));
   }
   const bool one_kind = one_pass(at->DP, dtype_size(at->dtype));
   const std::vector<int32_t> kinds = one_kind ? std::vector<int32_t>{kItemV} : std::vector<int32_t>{kItemV, kItemK};
@@ -612,7 +615,7 @@ cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, co
     add_units(u, qs, ks, 0, 4, 3, {kItemQ}, all);
     add_units(u, ks, qs, 1, 4, one_kind ? 4 : 3, kinds, all);
   }
-  build(b->bwd, u, 4, g, at->DP * es <= 384 ? two : one, 4, {false, causal, causal});
+  build(b->bwd, u, 4, g, at->DP * es <= 384 ? two : one, 4, {false, causal, causal, 5, 0, b->sequence});
   return b.release();
 }
 
@@ -701,6 +704,9 @@ cgtp_attn_cache_s* build_attn_cache(cgtp_attn_s* at, int64_t slots, int64_t capa
     build_joint(c->joint, at, slots, c->shared_tiles, step_with_joint(at->DP, es));
   }
   need_launch(workgroups + (c->joint.list.items + 7) / 8 * 8);
+  // short caches behind long shared rows: no more shares than the device holds beside those
+  if (c->joint.per && c->qtiles * tiles <= 8 * int64_t(c->shares) * c->waves_a_head)
+    c->shares = int(std::max<int64_t>(1, std::max(at_once / 4, at_once - c->joint.list.items) / c->bundles));
   return c.release();
 }
 

@@ -148,8 +148,9 @@ cgtp_status cgtp_attn_batch_create(cgtp_attn attn, cgtp_samples queries, cgtp_sa
  *   (nk = nq: a whole prompt; nk > nq: its next rows after nk - nq earlier ones;
  *   nk < nq: the first nq - nk queries see no own key). What later keys hold,
  *   infinities and NaN included, does not reach out and lse of a query that does not
- *   see them (but for their last bits: the kernels choose how scores are kept from
- *   overflowing by the norms of 32-row tiles).
+ *   see them, nor what queries hold the gradients of keys that they do not see (but for
+ *   last bits: the kernels choose how scores are kept from overflowing by the norms of
+ *   32-row tiles).
  * Errors: as above, INVALID_ARG for shared < 0, UNSUPPORTED for shared + context rows
  * beyond 2^31 or a causal batch beyond 2^30 rows. */
 cgtp_status cgtp_attn_batch_create_seq(cgtp_attn attn, cgtp_samples queries, cgtp_samples context, int causal,
@@ -201,7 +202,8 @@ cgtp_status cgtp_attn_backward(cgtp_attn_batch batch, const void* q, int64_t ldq
  * all sequences see before their own (one document, one surrounding). Keeps copies
  * of nothing but the layout: attn must outlive it. Host work and a synchronous upload.
  * Errors: INVALID_ARG (slots or shared < 0, capacity < 1), UNSUPPORTED (slots x heads,
- * capacity or shared beyond 2^31, or slots x kv_heads beyond 2^24). */
+ * capacity or shared beyond 2^31, slots x capacity beyond 2^35, or slots x kv_heads
+ * beyond 2^24). */
 cgtp_status cgtp_attn_cache_create(cgtp_attn attn, int64_t slots, int64_t capacity, int64_t shared,
                                    cgtp_attn_cache* out);
 cgtp_status cgtp_attn_cache_destroy(cgtp_attn_cache cache);
