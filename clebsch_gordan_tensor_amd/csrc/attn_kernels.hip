@@ -639,10 +639,12 @@ cgtp_attn_cache_s* build_attn_cache(cgtp_attn_s* at, int64_t slots, int64_t capa
   c->capacity = capacity;
   c->shared = shared;
   c->device = current_device();
-  if (capacity > INT32_MAX - 64 || slots > INT32_MAX || shared > INT32_MAX - 64)
-    throw Error{CGTP_ERR_UNSUPPORTED, "attention cache: more than 2^31 rows"};
+  // (places are counted in 32 bits, beyond the end of a sequence's last turn)
+  if (capacity > 1 << 30 || slots > INT32_MAX || shared > INT32_MAX - 64)
+    throw Error{CGTP_ERR_UNSUPPORTED, "attention cache: more than 2^30 places a slot, or 2^31 slots or shared rows"};
   std::vector<int64_t> ptr;
   if (slots * at->G > INT32_MAX - 64) throw Error{CGTP_ERR_UNSUPPORTED, "attention: rows x heads beyond 2^31"};
+  need_launch(slots * ((at->G + 31) / 32) * at->kv_heads);  // (before the lists are laid out)
   for (int64_t s = 0; s <= slots; ++s) ptr.push_back(s);
   const Side qs = cut(ptr, at->G);
   c->qtiles = int64_t(qs.tiles.size());

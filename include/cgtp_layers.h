@@ -187,7 +187,9 @@ cgtp_status cgtp_attn_forward_packed(cgtp_attn_batch batch, const void* q, int64
  *   grad_v = P^T grad_out,  dS = P (grad_out v^T - rowsum(grad_out out)),
  *   grad_q = scale dS k,    grad_k = scale dS^T q,
  * grad_k and grad_v summed over the query heads that share a context head.
- * (out as stored: in bf16 its rounding is in grad_q and grad_k, most with few keys.)
+ * (out as stored: in bf16 its rounding is in grad_q and grad_k, most with few keys;
+ * of sequence batches in bf16, queries that see at most two tiles of 32 keys take that
+ * sum from the weights instead.)
  * Gradients are contiguous rows. The summation orders are fixed. */
 cgtp_status cgtp_attn_backward(cgtp_attn_batch batch, const void* q, int64_t ldq, const void* k, int64_t ldk,
                                const void* v, int64_t ldv, const uint8_t* key_mask, double scale, const void* out,
@@ -201,9 +203,9 @@ cgtp_status cgtp_attn_backward(cgtp_attn_batch batch, const void* q, int64_t ldq
  * (a prompt's rows), copies and cuts as any tensor; and optionally `shared` rows that
  * all sequences see before their own (one document, one surrounding). Keeps copies
  * of nothing but the layout: attn must outlive it. Host work and a synchronous upload.
- * Errors: INVALID_ARG (slots or shared < 0, capacity < 1), UNSUPPORTED (slots x heads,
- * capacity or shared beyond 2^31, slots x capacity beyond 2^35, or slots x kv_heads
- * beyond 2^24). */
+ * Errors: INVALID_ARG (slots or shared < 0, capacity < 1), UNSUPPORTED (slots x heads
+ * or shared beyond 2^31, capacity beyond 2^30, slots x capacity beyond 2^35, or slots x
+ * kv_heads beyond 2^24). */
 cgtp_status cgtp_attn_cache_create(cgtp_attn attn, int64_t slots, int64_t capacity, int64_t shared,
                                    cgtp_attn_cache* out);
 cgtp_status cgtp_attn_cache_destroy(cgtp_attn_cache cache);
@@ -216,9 +218,10 @@ cgtp_status cgtp_attn_cache_share(cgtp_attn_cache cache, const void* k, int64_t 
  *   k_cache[s][n] = k[s], v_cache[s][n] = v[s],
  *   out[s] = attention of q[s] over the shared rows and places 0 .. n,
  * lse as in cgtp_attn_forward. A slot whose length lies outside 0 .. capacity - 1
- * (not in use, or full) takes no part: nothing of it is read or written, its out is 0
- * and its lse -inf. Places behind n are not used, whatever they hold. lengths is only read: the caller counts
- * on. Rows of q, k and v with strides as in cgtp_attn_forward (not rows of the caches); caches are contiguous.
+ * (not in use, or full) takes no part: nothing of its cache is read or written, its out is 0
+ * and its lse -inf. Places behind n are not used, whatever they hold. lengths is only
+ * read: the caller counts on. Rows of q, k and v with strides as in cgtp_attn_forward
+ * (not rows of the caches); caches are contiguous.
  * `context`: the packed shared rows (NULL where shared = 0). */
 cgtp_status cgtp_attn_step(cgtp_attn_cache cache, const void* q, int64_t ldq, const void* k, int64_t ldk,
                            const void* v, int64_t ldv, void* k_cache, void* v_cache, const int32_t* lengths,

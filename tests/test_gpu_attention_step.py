@@ -135,6 +135,13 @@ def test_strided_and_misaligned_rows(dtype):
         for t, x in zip(views, (q, k, v)):
             t.copy_(x)
         assert torch.equal(want, attn.step(cache, *views, lengths))
+    for shift in (1, 4):                              # caches that begin inside another tensor
+        for name in ("k", "v"):
+            old = getattr(cache, name)
+            flat = torch.zeros(old.numel() + shift, dtype=old.dtype, device="cuda")
+            flat[shift:] = old.flatten()
+            setattr(cache, name, flat[shift:].view(old.shape))
+        assert torch.equal(want, attn.step(cache, q, k, v, lengths))
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -248,7 +255,7 @@ def test_refusals():
         with pytest.raises(cgtp.CgtpError) as e:
             attn.cache(bad[0], bad[1], shared=bad[2])
         assert e.value.status == 1
-    for bad in ((2, 1 << 31, 0), (1 << 31, 4, 0), (2, 4, 1 << 31)):
+    for bad in ((2, 1 << 31, 0), (1, (1 << 30) + 1, 0), (1 << 31, 4, 0), (2, 4, 1 << 31), (1 << 20, 1 << 20, 0), (1 << 29, 1, 0)):
         with pytest.raises(cgtp.CgtpError) as e:
             attn.cache(bad[0], bad[1], shared=bad[2])
         assert e.value.status == 3
