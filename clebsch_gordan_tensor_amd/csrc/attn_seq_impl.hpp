@@ -600,9 +600,12 @@ __global__ __launch_bounds__(kThreads) void rows_join_kernel(RowsJoinArgs a) {
     sums_of[tid] = s;
     __syncthreads();
     if (turn > 0) return;
+    // (turn 0's own top, not ref: that is 0 where its parts hold no key, and 2^(0 - all) times its
+    // sums of 0 would be NaN for references below -128)
+    const float own_top = s.m;
     for (int k = 1; k < turns; ++k) s.m = fmaxf(s.m, sums_of[tid + 8 * lanes * k].m);
     const float all = s.m == -INFINITY ? 0.0f : s.m;
-    float w = exp2_fast(ref - all);
+    float w = exp2_fast(own_top - all);
     ref = all;
     s.l *= w;
     s.e *= w;
