@@ -611,24 +611,6 @@ __device__ __forceinline__ void finish(const FwdArgs& a, const Item& it, const T
     a.lse[int64_t(token) * a.heads + head] = l > 0.0f || l != l ? (st.m + __log2f(e)) * 0.69314718055994531f : -INFINITY;
 }
 
-// Element d of row r of a packed tile.
-template <typename T, int DP>
-__device__ __forceinline__ float row_frag_at(const T* tile, int r, int d) {
-  constexpr int VE = Op<T>::VE;
-  return to_acc<float>(tile[(d / (2 * VE) * 64 + d / VE % 2 * 32 + r) * VE + d % VE]);
-}
-template <typename T, int DP>
-__device__ __forceinline__ float col_frag_at(const T* tile, int r, int d) {
-  constexpr int VE = Op<T>::VE, FR = 16 / VE;
-  const int reg = r / 8 * 4 + r % 4, h = r / 4 % 2;
-  return to_acc<float>(tile[((d / 32 * FR + reg / VE) * 64 + 32 * h + d % 32) * VE + reg % VE]);
-}
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 1; off < 64; off *= 2) v += lane_fetch(v, (int(threadIdx.x & 63) ^ off) << 2);
-  return v;
-}
-
 // The kernel's arguments (its only parameter) read anew: what a branch that is hardly ever
 // taken needs of them would else be held in registers, or spilled, by all that comes before.
 template <typename A>
@@ -654,71 +636,173 @@ __device__ __forceinline__ uint32_t rows_of(bool bad) {
   return uint32_t(b) | uint32_t(b >> 32);
 }
 
-// A matrix product adds weight 0 times value for the keys that a causal query does not
-// see, which is NaN where such a value is infinite or NaN. Rows that came out NaN with a
-// finite sum of weights are formed again here, key by key over those they see (lanes
-// along the head's elements), after finish() wrote them. (The gradients likewise: redo_dq,
-// redo_dkv.)
+// A matrix product adds weight 0 times what a row does not see, which is NaN where that is
+// infinite or NaN. Rows that this reaches are formed again with products that leave it out
+// (redo_rows, redo_kernel): infinities and NaN go into the product as 1 with their sign, and what
+// they add to a result is counted beside it by two more products, a of the signs of the infinities
+// and of the weights, b of the infinities and NaN and the rows that see them. Where b = 0 there are
+// none; where |a| = b all are infinities that add one sign; else there is a NaN among them,
+// or infinities of both signs or with weight 0. Both counts are at most 32 a tile and kept as a + 128 b.
+// Everything here is on a branch that is hardly ever taken, so it takes 32 columns of a head at a time, with
+// all products of the scores again for each: its registers must not cost the kernels around it their
+// waves (all columns at once: 156 for heads of 32 in bf16, where the forward has 76).
+
+// The weights of a tile (0 where not seen) as operands.
+template <typename T>
+struct SeenWeights {
+  static constexpr int VE = Op<T>::VE, FR = 16 / VE;
+  using Frag = typename Op<T>::Frag;
+  Frag w[FR];
+  uint32_t seen;  // bit i: the row sees what accumulator register i stands for
+  __device__ __forceinline__ float sign(int f, int j) const {
+    const float x = static_cast<float>(w[f][j]);
+    return x > 0.0f ? 1.0f : x < 0.0f ? -1.0f : 0.0f;
+  }
+  __device__ __forceinline__ float one(int f, int j) const { return float(seen >> (VE * f + j) & 1); }
+};
+// acc += columns 32 d .. of a packed tile times weights, of seen pairs alone.
+template <typename T>
+__device__ __forceinline__ void add_seen(f32x16& acc, const T* columns, int d, const SeenWeights<T>& s) {
+  constexpr int VE = Op<T>::VE, FR = 16 / VE;
+  using Frag = typename Op<T>::Frag;
+  using E = std::remove_reference_t<decltype(Frag{}[0])>;
+  bool bad = false;
+#pragma unroll
+  for (int f = 0; f < FR; ++f) {
+    const u32x4 bits = unit16(columns, d * FR + f, lane_id());
+    bad = bad || not_finite<T>(bits);
+    Frag x = as_frag<Frag>(bits);
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+      const float v = static_cast<float>(x[j]);
+      x[j] = fabsf(v) < INFINITY ? x[j] : static_cast<E>(copysignf(1.0f, v));
+    }
+    acc = Op<T>::mma(x, s.w[f], acc);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if (!__any(bad)) return;
+  f32x16 count = zero16();
+#pragma unroll
+  for (int f = 0; f < FR; ++f) {
+    const Frag x = as_frag<Frag>(unit16(columns, d * FR + f, lane_id()));
+    Frag y, w;
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+      const float v = static_cast<float>(x[j]);
+      y[j] = static_cast<E>(fabsf(v) == INFINITY ? copysignf(1.0f, v) : 0.0f);
+      w[j] = static_cast<E>(s.sign(f, j));
+    }
+    count = Op<T>::mma(y, w, count);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+      y[j] = static_cast<E>(fabsf(static_cast<float>(x[j])) < INFINITY ? 0.0f : 128.0f);
+      w[j] = static_cast<E>(s.one(f, j));
+    }
+    count = Op<T>::mma(y, w, count);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float b = rintf(count[i] * 0.0078125f), a = count[i] - 128.0f * b;
+    acc[i] += b == 0.0f ? 0.0f : fabsf(a) == b ? copysignf(INFINITY, a) : NAN;
+  }
+}
+// Bits of a lane's accumulator registers whose places, of the 32 from `first` on, lie below `end`.
+__device__ __forceinline__ uint32_t seen_below(int first, int end, int h) {
+  uint32_t seen = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) seen |= (first + 8 * (i / 4) + 4 * h + i % 4 < end ? 1u : 0u) << i;
+  return seen;
+}
+// Elements 32 d + 8 b + 4 h .. + 3 of a lane's row from accumulators g times scale (as scatter_acc).
+template <typename T>
+__device__ __forceinline__ void scatter_columns(T* row, const int4* table, bool query, int head, int h, int d,
+                                                const f32x16& g, float scale) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int4 e = table[32 * d + 8 * (i / 4) + 4 * h + i % 4];
+    if (e.w) from_acc(row[elem(e, query, head)], g[i] * scale);
+    if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+  }
+}
+__device__ __forceinline__ void store_columns(float* o, int h, const f32x16& g, float scale) {
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+    *reinterpret_cast<f32x4*>(o + 8 * b + 4 * h) =
+        f32x4{g[4 * b] * scale, g[4 * b + 1] * scale, g[4 * b + 2] * scale, g[4 * b + 3] * scale};
+}
+
+// Rows of a causal forward that came out NaN with a finite sum of weights, where values in
+// tiles that some of the rows see only a part of may be why: formed again after finish() wrote
+// them, with the reference that they had, from the wave's tiles in memory (1500 rows, 4 heads of
+// 128, one NaN among the values: 89 us for 42 in bf16, 187 us for 63 in fp32; NaN in all of
+// them 142 and 216 us).
 template <typename T, int DP>
 __device__ __forceinline__ void redo_rows(const Item& it, const Reach& re, const Tile& tl, int tile_in_item,
                                           const Running<DP / 32>& st) {
-  constexpr int PER = (DP + 63) / 64;
-  const int lane = lane_id();
+  using D = Dims<T, DP>;
+  using Frag = typename Op<T>::Frag;
   const float sum = half_sum(st.l);
-  uint32_t rows = rows_of(any_nan(st.o) && sum == sum);
+  const uint32_t rows = rows_of(any_nan(st.o) && sum == sum);
   if (!rows) return;
   const FwdArgs& a = arguments_anew<FwdArgs>();
+  const int lane = lane_id(), n = lane % 32, h = lane / 32;
+  const auto tile_of = [&](const void* src, int tile) {
+    return static_cast<const T*>(src) + (int64_t(tile) * a.groups + it.hk) * D::TILE;
+  };
+  bool bad = false;
+  const int part = hidden_from(a, re, tl.row0) >> 5;
+  for (int t = it.b1 - 1; t >= max(it.b0, a.shared); --t) {
+    const int tile = key_tile<true>(a, re.skip, t);
+    if (tile < part) break;
+#pragma unroll 1
+    for (int u = 0; u < D::UNITS; ++u) bad = bad || not_finite<T>(unit16(tile_of(a.vf, tile), u, lane));
+  }
+  if (!__any(bad)) return;
   wait_copies();  // (finish's stores of the same rows come first)
-  while (rows) {
-    const int n = __builtin_ctz(rows);
-    rows &= rows - 1;
-    if (n >= tl.n) return;
-    const float m = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(st.m), n));
-    const float ref = m == -INFINITY ? 0.0f : m;
-    const int row = tl.row0 + n, token = row / a.G, head = it.hk * a.G + row % a.G;
-    const int hidden = hidden_from(a, re, row);
-    float q[PER], o[PER], l = 0.0f;
-#pragma unroll
-    for (int c = 0; c < PER; ++c) {
-      const int4 at = a.table[min(lane + 64 * c, DP - 1)];
-      T x = static_cast<const T*>(a.q)[int64_t(token) * a.ldq + elem(at, true, head)];
-      q[c] = lane + 64 * c < DP && at.w ? (a.q_sign ? -to_acc<float>(x) : to_acc<float>(x)) : 0.0f;
-      o[c] = 0.0f;
-    }
+  const int row = tl.row0 + min(n, tl.n - 1), token = row / a.G, head = it.hk * a.G + row % a.G;
+  const int hidden = hidden_from(a, re, row);
+  const bool mine = n < tl.n && (rows >> n & 1);
+  const float m = st.m;
+#pragma unroll 1
+  for (int d = 0; d < D::DT; ++d) {
+    Running<1> again;
+    float e = 0.0f;
+    again.m = m;
+    again.o[0] = zero16();
+#pragma unroll 1
     for (int t = it.b0; t < it.b1; ++t) {
       const int tile = key_tile<true>(a, re.skip, t);
-      const int64_t at = (int64_t(tile) * a.groups + it.hk) * Dims<T, DP>::TILE;
-      const T *kt = static_cast<const T*>(a.kf) + at, *vt = static_cast<const T*>(a.vf) + at;
-      const int seen = t < a.shared ? 32 : min(32, hidden - 32 * tile);
-      for (int r = 0; r < seen; ++r) {
-        if (a.bias[int64_t(tile) * 32 + r] < 0.0f) continue;
-        float s = 0.0f;
+      f32x16 s = zero16();
+      {
+        Frag q[D::KSTEPS];
+        load_queries<T, DP>(a, tl, it.hk, lane, q);
 #pragma unroll
-        for (int c = 0; c < PER; ++c)
-          if (lane + 64 * c < DP) s += q[c] * row_frag_at<T, DP>(kt, r, lane + 64 * c);
-        const float w = exp2_fast(fmaf(wave_sum(s), a.scale2, -ref));
-        T wt;
-        from_acc(wt, w);
-        const float p = to_acc<float>(wt);
-        l += p;
+        for (int u = 0; u < D::KSTEPS; ++u) {
+          s = Op<T>::mma(as_frag<Frag>(unit16(tile_of(a.kf, tile), u, lane)), q[u], s);
+          if (u % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      if (ldc(a.flags + tile)) mask_scores(s, a.bias + int64_t(tile) * 32, h);
+      SeenWeights<T> x;
+      x.seen = t < a.shared ? 0xffffu : seen_below(32 * tile, hidden, h);
 #pragma unroll
-        for (int c = 0; c < PER; ++c)
-          if (lane + 64 * c < DP) o[c] += p * col_frag_at<T, DP>(vt, r, lane + 64 * c);
-      }
+      for (int i = 0; i < 16; ++i) s[i] = x.seen >> i & 1 ? s[i] : -INFINITY;
+      weigh<T, true>(again, s, a.scale2, 0.0f, e, false, x.w);
+      __builtin_amdgcn_sched_barrier(0);
+      add_seen(again.o[0], tile_of(a.vf, tile), d, x);
     }
-    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-    const int64_t part = (int64_t(it.slot) * it.stride + tile_in_item) * 32 + n;
-    for (int c = 0; c < PER; ++c) {
-      const int d = lane + 64 * c;
-      if (d >= DP) break;
-      if (it.slot >= 0) {
-        a.part[part * DP + d] = o[c];
-        continue;
-      }
-      const int4 at = a.table[d];
-      if (at.w) from_acc(static_cast<T*>(a.out)[int64_t(token) * a.ldo + elem(at, true, head)], o[c] * inv);
+    const float l = half_sum(again.l);
+    if (!mine) continue;
+    if (it.slot >= 0) {
+      const int64_t r = (int64_t(it.slot) * it.stride + tile_in_item) * 32 + n;
+      store_columns(a.part + r * DP + 32 * d, h, again.o[0], 1.0f);
+      if (h == 0) a.part_ml[r].y = l;  // (reference and exact sum stay)
+    } else {
+      scatter_columns(static_cast<T*>(a.out) + int64_t(token) * a.ldo, a.table, true, head, h, d, again.o[0],
+                      l > 0.0f || l != l ? 1.0f / l : 0.0f);
     }
-    if (lane == 0 && it.slot >= 0) a.part_ml[part].y = l;  // (reference and exact sum stay)
   }
 }
 
@@ -1130,31 +1214,6 @@ __device__ __forceinline__ void finish_grad(const BwdArgs& a, const Item& it, co
   scatter_acc(static_cast<T*>(dst) + int64_t(token) * ld, a.table, query, head, quad, h, g, scale);
 }
 
-// Row n of a wave's gradients, formed again (see redo_rows; lanes along the head's
-// elements), over what finish_grad() wrote.
-template <typename T, int DP, int PER>
-__device__ __forceinline__ void put_row(const BwdArgs& a, const Item& it, const Tile& tl, int within, int n, bool query,
-                                        void* dst, int64_t ld, float* part, const float (&g)[PER], float scale) {
-  const int row = tl.row0 + n, G = query ? a.G : 1, token = row / G, head = it.hk * G + row % G;
-  for (int c = 0; c < PER; ++c) {
-    const int d = lane_id() + 64 * c;
-    if (d >= DP) break;
-    if (it.slot >= 0) {
-      part[((int64_t(it.slot) * it.stride + within) * 32 + n) * DP + d] = g[c] * scale;
-      continue;
-    }
-    const int4 at = a.table[d];
-    if (at.w) from_acc(static_cast<T*>(dst)[int64_t(token) * ld + elem(at, query, head)], g[c] * scale);
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ float rounded(float v) {
-  T t;
-  from_acc(t, v);
-  return to_acc<float>(t);
-}
-
 // grad_q: as the forward, a wave keeps 32 query rows and walks the key tiles:
 // S^T = K Q^T, P^T = exp2(S^T - lse), dP^T = V dO^T, dS^T = P^T (dP^T - delta),
 // dQ^T += K^T dS^T. Three packed forms of a tile pass through shared memory: K
@@ -1423,130 +1482,165 @@ __global__ __launch_bounds__(kThreads, lds_waves(bwd_units<T, DP>())) void bwd_k
   }
 }
 
+// Columns 32 d .. of a wave's gradient: a part, or final rows (as finish_grad).
 template <typename T, int DP>
-__device__ __forceinline__ void redo_dq(const BwdArgs& a, const Item& it, const Reach& re, const Tile& tl, int within,
-                                        int64_t qat, uint32_t rows) {
-  constexpr int PER = (DP + 63) / 64, TILE = Dims<T, DP>::TILE;
-  const int lane = lane_id();
-  for (; rows; rows &= rows - 1) {
-    const int n = __builtin_ctz(rows);
-    if (n >= tl.n) return;
-    const float lse2 = a.rows[qat * 64 + n], delta = a.rows[qat * 64 + 32 + n];
-    if (lse2 != lse2) continue;  // (the formula's is NaN as well)
-    const int hidden = hidden_from(a, re, tl.row0 + n);
-    float q[PER], g[PER], dq[PER];
-#pragma unroll
-    for (int c = 0; c < PER; ++c) {
-      const bool in = lane + 64 * c < DP;
-      q[c] = in ? row_frag_at<T, DP>(a.qforms<T>(kQRows) + qat * TILE, n, lane + 64 * c) : 0.0f;
-      g[c] = in ? row_frag_at<T, DP>(a.qforms<T>(kGRows) + qat * TILE, n, lane + 64 * c) : 0.0f;
-      dq[c] = 0.0f;
-    }
-    for (int t = it.b0; t < it.b1; ++t) {
-      const int tile = key_tile<true>(a, re.skip, t);
-      const T* const kt = a.kforms<T>(kKRows) + (int64_t(tile) * a.groups + it.hk) * TILE;
-      const T* const vt = a.kforms<T>(kVRows) + (int64_t(tile) * a.groups + it.hk) * TILE;
-      const int seen = t < a.shared ? 32 : min(32, hidden - 32 * tile);
-      for (int r = 0; r < seen; ++r) {
-        if (a.bias[int64_t(tile) * 32 + r] < 0.0f) continue;
-        float k[PER], s = 0.0f, dp = 0.0f;
-#pragma unroll
-        for (int c = 0; c < PER; ++c) {
-          const int d = min(lane + 64 * c, DP - 1);
-          k[c] = row_frag_at<T, DP>(kt, r, d);
-          s += lane + 64 * c < DP ? q[c] * k[c] : 0.0f;
-          dp += lane + 64 * c < DP ? g[c] * row_frag_at<T, DP>(vt, r, d) : 0.0f;
-        }
-        const float p = exp2_fast(wave_sum(s) * a.scale2 - lse2);
-        const float ds = rounded<T>(p * (wave_sum(dp) - delta));
-#pragma unroll
-        for (int c = 0; c < PER; ++c) dq[c] += ds * k[c];
-      }
-    }
-    put_row<T, DP, PER>(a, it, tl, within, n, true, a.dq, a.ldq, a.part_q, dq, a.scale);
+__device__ __forceinline__ void put_columns(const BwdArgs& a, const Item& it, const Tile& tl, int within, bool query,
+                                            int d, void* dst, int64_t ld, float* part, const f32x16& g, float scale) {
+  const int n = lane_id() % 32, h = lane_id() / 32;
+  if (it.slot >= 0) {
+    store_columns(part + ((int64_t(it.slot) * it.stride + within) * 32 + n) * DP + 32 * d, h, g, scale);
+  } else if (n < tl.n) {
+    const int row = tl.row0 + n, G = query ? a.G : 1;
+    scatter_columns(static_cast<T*>(dst) + int64_t(row / G) * ld, a.table, query, it.hk * G + row % G, h, d, g, scale);
   }
 }
-
+// s += A B^T of two packed tiles' rows.
 template <typename T, int DP>
-__device__ __forceinline__ void redo_dkv(const BwdArgs& a, const Item& it, const Tile& tl, int kt, bool want_k,
-                                         bool want_v, uint32_t rows) {
-  constexpr int PER = (DP + 63) / 64, TILE = Dims<T, DP>::TILE;
-  const int lane = lane_id();
-  const int64_t kat = (int64_t(kt) * a.groups + it.hk) * TILE;
-  for (; rows; rows &= rows - 1) {
-    const int n = __builtin_ctz(rows);
-    if (n >= tl.n) return;
-    if (a.bias[int64_t(kt) * 32 + n] < 0.0f) continue;
-    float k[PER], v[PER], dk[PER], dv[PER];
+__device__ __forceinline__ void row_products(f32x16& s, const T* a, const T* b) {
+  using Frag = typename Op<T>::Frag;
+#pragma unroll 4
+  for (int u = 0; u < Dims<T, DP>::KSTEPS; ++u)
+    s = Op<T>::mma(as_frag<Frag>(unit16(a, u, lane_id())), as_frag<Frag>(unit16(b, u, lane_id())), s);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Columns 32 d .. of grad_q of tile `within` of an item once more, as dq_item, of seen pairs alone.
+template <typename T, int DP>
+__device__ __forceinline__ void redo_dq(const BwdArgs& a, const Item& it, int within, int d) {
+  using D = Dims<T, DP>;
+  const int n = lane_id() % 32, h = lane_id() / 32;
+  const Tile tl = ldc(a.qtiles + it.a0 + within);
+  const Reach re = ldc(a.reach + it.a0 + within);
+  const int64_t qat = int64_t(it.a0 + within) * a.groups + it.hk;
+  const float lse2 = a.rows[qat * 64 + n], delta = a.rows[qat * 64 + 32 + n];
+  // (where these are NaN, so is the row)
+  if (!__any(n < tl.n && lse2 == lse2 && delta == delta)) return;
+  const int hidden = hidden_from(a, re, tl.row0 + min(n, tl.n - 1));
+  f32x16 dq = zero16();
+#pragma unroll 1
+  for (int t = it.b0; t < it.b1; ++t) {
+    const int tile = key_tile<true>(a, re.skip, t);
+    const int64_t kat = (int64_t(tile) * a.groups + it.hk) * D::TILE;
+    f32x16 s = zero16(), dp = zero16();
+    row_products<T, DP>(s, a.kforms<T>(kKRows) + kat, a.qforms<T>(kQRows) + qat * D::TILE);
+    row_products<T, DP>(dp, a.kforms<T>(kVRows) + kat, a.qforms<T>(kGRows) + qat * D::TILE);
+    SeenWeights<T> x;
+    x.seen = t < a.shared ? 0xffffu : seen_below(32 * tile, hidden, h);
 #pragma unroll
-    for (int c = 0; c < PER; ++c) {
-      const int d = min(lane + 64 * c, DP - 1);
-      k[c] = row_frag_at<T, DP>(a.kforms<T>(kKRows) + kat, n, d);
-      v[c] = row_frag_at<T, DP>(a.kforms<T>(kVRows) + kat, n, d);
-      dk[c] = dv[c] = 0.0f;
+    for (int i = 0; i < 16; ++i) {
+      const float bias = a.bias[int64_t(tile) * 32 + 8 * (i / 4) + 4 * h + i % 4];
+      const float p = exp2_fast(fmaf(s[i], a.scale2, bias) - lse2);
+      s[i] = x.seen >> i & 1 ? p * (dp[i] - delta) : 0.0f;
     }
-    for (int t = it.b0; t < it.b1; ++t) {
-      const int64_t at = int64_t(t) * a.groups + it.hk;
-      const Tile ql = ldc(a.qtiles + t);
-      const Reach re = ldc(a.reach + t);
-      for (int r = 0; r < ql.n; ++r) {
-        if (kt >= a.shared && 32 * kt + n >= hidden_from(a, re, ql.row0 + r)) continue;
-        float q[PER], g[PER], s = 0.0f, dp = 0.0f;
 #pragma unroll
-        for (int c = 0; c < PER; ++c) {
-          const int d = min(lane + 64 * c, DP - 1);
-          q[c] = row_frag_at<T, DP>(a.qforms<T>(kQRows) + at * TILE, r, d);
-          g[c] = row_frag_at<T, DP>(a.qforms<T>(kGRows) + at * TILE, r, d);
-          s += lane + 64 * c < DP ? q[c] * k[c] : 0.0f;
-          dp += lane + 64 * c < DP ? g[c] * v[c] : 0.0f;
-        }
-        const float p = exp2_fast(wave_sum(s) * a.scale2 - a.rows[at * 64 + r]);
-        const float ds = rounded<T>(p * (wave_sum(dp) - a.rows[at * 64 + 32 + r])), pt = rounded<T>(p);
-#pragma unroll
-        for (int c = 0; c < PER; ++c) {
-          dk[c] += ds * q[c];
-          dv[c] += pt * g[c];
-        }
-      }
-    }
-    const int within = kt - it.a0;
-    if (want_v && a.dv) put_row<T, DP, PER>(a, it, tl, within, n, false, a.dv, a.ldk, a.part_v, dv, 1.0f);
-    if (want_k && a.dk) put_row<T, DP, PER>(a, it, tl, within, n, false, a.dk, a.ldk, a.part_k, dk, a.scale);
+    for (int f = 0; f < D::FR; ++f) x.w[f] = Op<T>::from_acc(s, f);
+    __builtin_amdgcn_sched_barrier(0);
+    add_seen(dq, a.kforms<T>(kKCols) + kat, d, x);
   }
+  put_columns<T, DP>(a, it, tl, within, true, d, a.dq, a.ldq, a.part_q, dq, a.scale);
+}
+
+// Columns 32 d .. of grad_v, or of grad_k where `key`, as dkv_item.
+template <typename T, int DP>
+__device__ __forceinline__ void redo_dkv(const BwdArgs& a, const Item& it, int within, bool key, int d) {
+  using D = Dims<T, DP>;
+  const int n = lane_id() % 32, h = lane_id() / 32, kt = it.a0 + within;
+  const Tile tl = ldc(a.ktiles + kt);
+  const int64_t kat = (int64_t(kt) * a.groups + it.hk) * D::TILE;
+  const float bias = a.bias[int64_t(kt) * 32 + n];
+  f32x16 g = zero16();
+#pragma unroll 1
+  for (int t = it.b0; t < it.b1; ++t) {
+    const int64_t at = int64_t(t) * a.groups + it.hk, qat = at * D::TILE;
+    const Tile ql = ldc(a.qtiles + t);
+    const Reach re = ldc(a.reach + t);
+    f32x16 s = zero16(), dp = zero16();
+    row_products<T, DP>(s, a.qforms<T>(kQRows) + qat, a.kforms<T>(kKRows) + kat);
+    if (key) row_products<T, DP>(dp, a.qforms<T>(kGRows) + qat, a.kforms<T>(kVRows) + kat);
+    SeenWeights<T> x;
+    x.seen = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = 8 * (i / 4) + 4 * h + i % 4;
+      const bool seen = 32 * kt + n < hidden_from(a, re, ql.row0 + min(r, ql.n - 1));
+      x.seen |= (seen ? 1u : 0u) << i;
+      const float p = exp2_fast(fmaf(s[i], a.scale2, bias) - a.rows[at * 64 + r]);
+      s[i] = !seen ? 0.0f : key ? p * (dp[i] - a.rows[at * 64 + 32 + r]) : p;
+    }
+#pragma unroll
+    for (int f = 0; f < D::FR; ++f) x.w[f] = Op<T>::from_acc(s, f);
+    __builtin_amdgcn_sched_barrier(0);
+    add_seen(g, a.qforms<T>(key ? kQCols : kGCols) + qat, d, x);
+  }
+  if (bias < 0.0f) g = zero16();  // (as in dkv_item)
+  put_columns<T, DP>(a, it, tl, within, false, d, key ? a.dk : a.dv, a.ldk, key ? a.part_k : a.part_v, g,
+                     key ? a.scale : 1.0f);
 }
 
 // Causal batches: gradients of tiles that some keys or queries with infinities or NaN are
-// hidden from in part, formed again row by row after bwd_kernel wrote them, by workgroups for
-// the same items (hardly ever any: the kernel takes 4 us; a test for NaN at the end of
-// bwd_kernel cost it 10 us of 340 by the registers).
+// hidden from in part, formed again after bwd_kernel wrote them. A wave looks at the flags of
+// 2^shift tiles of the items, all at once, and the workgroup's waves take what has to be formed again, hardly
+// ever any, in turn, 32 columns at a time: 4.6 us (ragged batch; one tile a wave, whatever their
+// number, 13 us; a test for NaN at the end of bwd_kernel cost that 10 us of 340 by the registers). With NaN in all
+// of grad_out a backward of 1500 rows, 4 heads of 128, takes 215 us for 66 in bf16 and 810 us for 168 in fp32.
 template <typename T, int DP>
-__global__ __launch_bounds__(kThreads) void redo_kernel(BwdArgs a) {
-  const int wave = wave_id();
-  const Item it = ldc(a.items + blockIdx.x);
-  if (wave >= it.tiles) return;
+__global__ __launch_bounds__(kThreads, 2) void redo_kernel(BwdArgs a, int items, int shift) {
+  constexpr bool kBoth = one_pass(DP, sizeof(T));
+  constexpr int DT = DP / 32;
+  __shared__ uint32_t found[4];
+  const int lane = lane_id(), wave = wave_id(), per = 1 << shift, lanes = 64 >> shift;
+  const int first = int(blockIdx.x) * 4 * per, mine = first + wave * per + lane / lanes, sub = lane % lanes;
+  const auto wants = [&](const Item& it, bool key) {
+    return key ? a.dk && (kBoth || it.kind == kItemK) : a.dv && (kBoth || it.kind == kItemV);
+  };
+  // the first place hidden from a query tile's first row
+  const auto hidden_first = [&](int tile) { return hidden_from(a, a.reach[tile], a.qtiles[tile].row0); };
   bool bad = false;
-  if (it.kind == kItemQ) {
-    if (!a.dq) return;
-    const int qt = it.a0 + wave;
-    const Reach re = ldc(a.reach + qt);
-    const Tile tl = ldc(a.qtiles + qt);
-    const int part = hidden_from(a, re, tl.row0) >> 5;
-    for (int t = it.b1 - 1; t >= max(it.b0, a.shared); --t) {
-      const int tile = key_tile<true>(a, re.skip, t);
-      if (tile < part) break;
-      bad = bad || ldc(a.k_bad + int64_t(tile) * a.groups + it.hk) != 0;
+  if (mine < 4 * items) {
+    const Item it = a.items[mine / 4];
+    const int at = it.a0 + mine % 4;
+    if (mine % 4 >= it.tiles) {
+    } else if (it.kind == kItemQ) {
+      if (a.dq) {
+        const int part = hidden_first(at) >> 5, skip = a.reach[at].skip;
+        for (int t = it.b1 - 1 - sub; t >= max(it.b0, a.shared) && !bad; t -= lanes) {
+          const int tile = key_tile<true>(a, skip, t);
+          if (tile < part) break;
+          bad = a.k_bad[int64_t(tile) * a.groups + it.hk] != 0;
+        }
+      }
+    } else if (at >= a.shared && (wants(it, false) || wants(it, true))) {
+      for (int t = it.b0 + sub; t < it.b1 && !bad; t += lanes) {
+        if (32 * at + 31 < hidden_first(t)) break;
+        bad = a.q_bad[int64_t(t) * a.groups + it.hk] != 0;
+      }
     }
-    if (bad) redo_dq<T, DP>(a, it, re, tl, wave, int64_t(qt) * a.groups + it.hk, ~0u);
-  } else {
-    constexpr bool kBoth = one_pass(DP, sizeof(T));
-    const bool want_k = a.dk && (kBoth || it.kind == kItemK), want_v = a.dv && (kBoth || it.kind == kItemV);
-    const int kt = it.a0 + wave;
-    if (kt < a.shared || !(want_k || want_v)) return;
-    for (int t = it.b0; t < it.b1; ++t) {
-      if (32 * kt + 31 < hidden_from(a, ldc(a.reach + t), ldc(a.qtiles + t).row0)) break;
-      bad = bad || ldc(a.q_bad + int64_t(t) * a.groups + it.hk) != 0;
+  }
+  const uint64_t which_bad = __ballot(bad);
+  uint32_t some = 0;
+  for (int e = 0; e < per; ++e) some |= (which_bad >> (lanes * e) & (~uint64_t(0) >> (64 - lanes)) ? 1u : 0u) << e;
+  if (lane == 0) found[wave] = some;
+  __syncthreads();
+  int turn = 0;
+  for (uint32_t left = found[0] | found[1] << per | found[2] << 2 * per | found[3] << 3 * per; left; left &= left - 1) {
+    const int which = first + __builtin_amdgcn_readfirstlane(__builtin_ctz(left)), w = which % 4;
+    const Item it = ldc(a.items + which / 4);
+    if (it.kind == kItemQ) {
+#pragma unroll 1
+      for (int d = 0; d < DT; ++d)
+        if (turn++ % 4 == wave) redo_dq<T, DP>(a, it, w, d);
+      continue;
     }
-    if (bad) redo_dkv<T, DP>(a, it, ldc(a.ktiles + kt), kt, want_k, want_v, ~0u);
+    // (a query whose lse is NaN makes NaN of all keys that it sees: nothing to mend where all see one)
+    bool nan = false;
+    for (int t = it.b1 - 1; t >= it.b0 && 32 * (it.a0 + w) + 31 < hidden_first(t) && !nan; --t) {
+      const float lse2 = a.rows[(int64_t(t) * a.groups + it.hk) * 64 + lane % 32];
+      nan = __any(lse2 != lse2);
+    }
+    if (nan) continue;
+#pragma unroll 1
+    for (int d = 0; d < 2 * DT; ++d)
+      if (wants(it, d >= DT) && turn++ % 4 == wave) redo_dkv<T, DP>(a, it, w, d >= DT, d % DT);
   }
 }
 

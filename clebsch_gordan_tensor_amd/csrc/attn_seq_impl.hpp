@@ -698,7 +698,10 @@ struct SeqKernels {
   }
   static void bwd(const BwdArgs& a, int items, hipStream_t s) {
     hipLaunchKernelGGL((bwd_kernel<T, DP, true>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
-    if (a.causal) hipLaunchKernelGGL((redo_kernel<T, DP>), dim3(unsigned(items)), dim3(kThreads), 0, s, a);
+    if (!a.causal) return;
+    // four tiles an item, four waves a workgroup: one tile a wave, and more from 768 workgroups on
+    const int shift = items <= 768 ? 0 : items <= 2 * 768 ? 1 : items <= 4 * 768 ? 2 : 3, per = 1 << shift;
+    hipLaunchKernelGGL((redo_kernel<T, DP>), dim3(unsigned((items + per - 1) / per)), dim3(kThreads), 0, s, a, items, shift);
   }
   static void step(const StepArgs& a, hipStream_t s) {
     const unsigned groups = a.whole ? unsigned(a.cut.slots) * unsigned(a.cut.tiles_a_slot) : unsigned(a.cut.shares);
