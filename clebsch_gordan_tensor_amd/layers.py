@@ -287,10 +287,17 @@ class AttentionCache(_Handle):
     """Keys and values of ``slots`` sequences for CrossAttention.step
     (cgtp_attn_cache_create); made by CrossAttention.cache. ``k`` and ``v`` are
     ordinary tensors of irreps rows [slots, capacity, dim_kv], to be filled with a
-    prompt's rows, copied or cut like any other."""
+    prompt's rows, copied or cut like any other. ``device`` is the current one (whose
+    memory the handle's tables lie in); tensors of another are refused."""
 
     def __init__(self, attn, slots, capacity, shared=0, device="cuda"):
         torch = _torch()
+        device = torch.device(device)
+        if device.type != "cuda":
+            raise ValueError("a cache lies in device memory, not on %s" % device)
+        self._index = torch.cuda.current_device()
+        if device.index not in (None, self._index):
+            raise ValueError("a cache is made on the current device (%d), not on %s" % (self._index, device))
         self.attn, self.slots, self.capacity, self.shared = attn, int(slots), int(capacity), int(shared)
         h = _vp()
         _check(_lib.cgtp_attn_cache_create(attn._h, self.slots, self.capacity, self.shared, ctypes.byref(h)),
@@ -304,9 +311,16 @@ class AttentionCache(_Handle):
         self.v = torch.zeros(shape, dtype=attn.torch_dtype, device=device)
         self._context = None
 
+    def _here(self, **tensors):
+        """All of a call's tensors have to be on the cache's device (one stream and one handle serve them)."""
+        for name, t in tensors.items():
+            if t is not None and t.get_device() != self._index:
+                raise ValueError("%s is on %s, the cache on device %d" % (name, t.device, self._index))
+
     def share(self, k, v, key_mask=None):
         """Lays out the rows that all sequences see before their own (cgtp_attn_cache_share)."""
         a = self.attn
+        self._here(k=k, v=v, key_mask=key_mask, cache_k=self.k)
         pk, ldk = a._rows(k, self.shared, a.dim_kv, "k")
         pv, ldv = a._rows(v, self.shared, a.dim_kv, "v")
         mask = a._mask(key_mask, self.shared)
@@ -458,6 +472,7 @@ class CrossAttention(_Handle):
         n, dt = cache.slots, self.torch_dtype
         if cache.shared and cache._context is None:
             raise ValueError("the cache's shared rows have not been laid out (share)")
+        cache._here(q=q, k=k, v=v, lengths=lengths, out=out, lse=lse, ws=ws, cache_k=cache.k, cache_v=cache.v)
         pq, ldq = self._rows(q, n, self.dim_q, "q")
         pk, ldk = self._rows(k, n, self.dim_kv, "k")
         pv, ldv = self._rows(v, n, self.dim_kv, "v")
