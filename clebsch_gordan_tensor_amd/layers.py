@@ -318,7 +318,9 @@ class AttentionCache(_Handle):
                 raise ValueError("%s is on %s, the cache on device %d" % (name, t.device, self._index))
 
     def share(self, k, v, key_mask=None):
-        """Lays out the rows that all sequences see before their own (cgtp_attn_cache_share)."""
+        """Lays out the rows that all sequences see before their own (cgtp_attn_cache_share), on the
+        current stream. Called again it writes the same memory: steps on other streams (and replays of
+        captured ones) that read the rows before or after are ordered by the caller."""
         a = self.attn
         self._here(k=k, v=v, key_mask=key_mask, cache_k=self.k)
         pk, ldk = a._rows(k, self.shared, a.dim_kv, "k")

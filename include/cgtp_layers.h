@@ -211,7 +211,8 @@ cgtp_status cgtp_attn_cache_create(cgtp_attn attn, int64_t slots, int64_t capaci
 cgtp_status cgtp_attn_cache_destroy(cgtp_attn_cache cache);
 /* Bytes of the packed shared rows and of the workspace of a step. */
 cgtp_status cgtp_attn_cache_query(cgtp_attn_cache cache, size_t* shared_bytes, size_t* ws_bytes);
-/* Lay the shared rows out once, as cgtp_attn_pack (k, v: shared rows). */
+/* Lay the shared rows out once, as cgtp_attn_pack (k, v: shared rows). Work on `stream` writes
+ * `context`; steps on other streams that read it, before or after, are ordered by the caller. */
 cgtp_status cgtp_attn_cache_share(cgtp_attn_cache cache, const void* k, int64_t ldk, const void* v, int64_t ldv,
                                   const uint8_t* key_mask, void* context, size_t context_bytes, void* stream);
 /* One token of every slot s, with n = lengths[s] (DEVICE, int32) tokens in its cache:
