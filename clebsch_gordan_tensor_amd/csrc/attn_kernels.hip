@@ -42,10 +42,23 @@ struct Side {
   std::vector<int32_t> first;  // first tile of each sample, [S + 1]
 };
 
-Side cut(const std::vector<int64_t>& ptr, int64_t G, int64_t shared = 0) {
+// One launch takes all workgroups of a kernel.
+void need_launch(int64_t workgroups) {
+  if (workgroups > kMaxWorkgroups)
+    throw Error{CGTP_ERR_UNSUPPORTED, "attention: more tiles x context heads than one launch takes"};
+}
+// That of the packing: checked before the tiles are laid out.
+void need_packing(int64_t tiles, int64_t kv_heads) { need_launch((tiles + 7) / 8 * 8 * kv_heads); }
+
+// `kv_heads` > 0: the side is packed by one launch.
+Side cut(const std::vector<int64_t>& ptr, int64_t G, int64_t shared = 0, int64_t kv_heads = 0) {
   Side s;
   if (ptr.back() * G + shared > INT32_MAX - 64)
     throw Error{CGTP_ERR_UNSUPPORTED, "attention: rows x heads beyond 2^31"};
+  int64_t tiles = (shared + 31) / 32;
+  for (size_t i = 0; i + 1 < ptr.size(); ++i) tiles += ((ptr[i + 1] - ptr[i]) * G + 31) / 32;
+  need_packing(tiles, kv_heads);
+  s.tiles.reserve(size_t(tiles));
   for (int64_t r = 0; r < shared; r += 32) s.tiles.push_back({int32_t(r), int32_t(std::min<int64_t>(32, shared - r))});
   for (size_t i = 0; i + 1 < ptr.size(); ++i) {
     s.first.push_back(int32_t(s.tiles.size()));
@@ -182,12 +195,6 @@ int64_t part_cost(const std::vector<Unit>& u, int groups, int slots, int min_len
     if (sequence && best_end * slots * 32 <= std::accumulate(costs.begin(), costs.end(), int64_t(0)) * 33) break;
   }
   return best;
-}
-
-// One launch takes all workgroups of a kernel.
-void need_launch(int64_t workgroups) {
-  if (workgroups > kMaxWorkgroups)
-    throw Error{CGTP_ERR_UNSUPPORTED, "attention: more tiles x context heads than one launch takes"};
 }
 
 // Splits long units (of at most `stride` tiles) and lays the items out for the
@@ -520,7 +527,7 @@ cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, co
   b->nk = shared + k->rows;
   b->device = current_device();
   if (b->nk > INT32_MAX - 64) throw Error{CGTP_ERR_UNSUPPORTED, "attention: context of more than 2^31 rows"};
-  const Side qs = cut(q->ptr, at->G), ks = cut(k->ptr, 1, shared);
+  const Side qs = cut(q->ptr, at->G, 0, at->kv_heads), ks = cut(k->ptr, 1, shared, at->kv_heads);
   b->qtiles = int64_t(qs.tiles.size());
   b->ktiles = int64_t(ks.tiles.size());
   b->shared_tiles = (shared + 31) / 32;
@@ -529,7 +536,6 @@ cgtp_attn_batch_s* build_attn_batch(cgtp_attn_s* at, const cgtp_samples_s* q, co
   // tokens and places (32 a tile) are compared in 32 bits
   if (causal && (b->nq > 1 << 30 || 32 * b->ktiles > 1 << 30))
     throw Error{CGTP_ERR_UNSUPPORTED, "attention: a causal batch of more than 2^30 rows"};
-  need_launch((std::max(b->qtiles, b->ktiles) + 7) / 8 * 8 * at->kv_heads);  // of the packing
   b->qtile_mem.upload(qs.tiles.data(), qs.tiles.size() * sizeof(Tile));
   b->ktile_mem.upload(ks.tiles.data(), ks.tiles.size() * sizeof(Tile));
   const int g = at->kv_heads;
@@ -644,7 +650,8 @@ cgtp_attn_cache_s* build_attn_cache(cgtp_attn_s* at, int64_t slots, int64_t capa
     throw Error{CGTP_ERR_UNSUPPORTED, "attention cache: more than 2^30 places a slot, or 2^31 slots or shared rows"};
   std::vector<int64_t> ptr;
   if (slots * at->G > INT32_MAX - 64) throw Error{CGTP_ERR_UNSUPPORTED, "attention: rows x heads beyond 2^31"};
-  need_launch(slots * ((at->G + 31) / 32) * at->kv_heads);  // (before the lists are laid out)
+  need_launch(slots * ((at->G + 31) / 32) * at->kv_heads);  // (before the lists are laid out, as the next)
+  need_packing((shared + 31) / 32, at->kv_heads);
   for (int64_t s = 0; s <= slots; ++s) ptr.push_back(s);
   const Side qs = cut(ptr, at->G);
   c->qtiles = int64_t(qs.tiles.size());
@@ -701,7 +708,6 @@ cgtp_attn_cache_s* build_attn_cache(cgtp_attn_s* at, int64_t slots, int64_t capa
   if (shared > 0) {
     const Side ks = cut({0}, 1, shared);
     c->shared_tiles = int64_t(ks.tiles.size());
-    need_launch((c->shared_tiles + 7) / 8 * 8 * at->kv_heads);
     c->shared_tile_mem.upload(ks.tiles.data(), ks.tiles.size() * sizeof(Tile));
     build_joint(c->joint, at, slots, c->shared_tiles, step_with_joint(at->DP, es));
   }

@@ -151,8 +151,8 @@ cgtp_status cgtp_attn_batch_create(cgtp_attn attn, cgtp_samples queries, cgtp_sa
  *   see them, nor what queries hold the gradients of keys that they do not see (but for
  *   last bits: the kernels choose how scores are kept from overflowing by the norms of
  *   32-row tiles).
- * Errors: as above, INVALID_ARG for shared < 0, UNSUPPORTED for shared + context rows
- * beyond 2^31 or a causal batch beyond 2^30 rows. */
+ * Errors: as above (the context's tiles with those of the shared rows), INVALID_ARG for shared < 0,
+ * UNSUPPORTED for shared + context rows beyond 2^31 or a causal batch beyond 2^30 rows. */
 cgtp_status cgtp_attn_batch_create_seq(cgtp_attn attn, cgtp_samples queries, cgtp_samples context, int causal,
                                        int64_t shared, cgtp_attn_batch* out);
 cgtp_status cgtp_attn_batch_destroy(cgtp_attn_batch batch);
@@ -203,9 +203,11 @@ cgtp_status cgtp_attn_backward(cgtp_attn_batch batch, const void* q, int64_t ldq
  * (a prompt's rows), copies and cuts as any tensor; and optionally `shared` rows that
  * all sequences see before their own (one document, one surrounding). Keeps copies
  * of nothing but the layout: attn must outlive it. Host work and a synchronous upload.
- * Errors: INVALID_ARG (slots or shared < 0, capacity < 1), UNSUPPORTED (slots x heads
- * or shared beyond 2^31, capacity beyond 2^30, slots x capacity beyond 2^35, or slots x
- * kv_heads beyond 2^24). */
+ * Errors: INVALID_ARG (slots or shared < 0, capacity < 1), UNSUPPORTED: with G = heads / kv_heads
+ * and tiles of 32 (rounded up for every slot: its G query rows, its places), slots x G beyond
+ * 2^31; capacity beyond 2^30; slots x ceil(G / 32) x ceil(capacity / 32) beyond 2^30; slots x
+ * ceil(G / 32) x kv_heads, ceil(shared / 32) x kv_heads, or what a step takes in one launch (the
+ * workgroups that the slots' places and the shared rows are shared out to) beyond 2^24. */
 cgtp_status cgtp_attn_cache_create(cgtp_attn attn, int64_t slots, int64_t capacity, int64_t shared,
                                    cgtp_attn_cache* out);
 cgtp_status cgtp_attn_cache_destroy(cgtp_attn_cache cache);

@@ -249,3 +249,39 @@ def test_infinities_and_nan_cost_a_few_times_a_call_at_most(dtype):
         got += (us(lambda: attn.backward(b, q, k, v, out, lse, y)),)
         print("us", dtype, rows, bad, "clean", clean, "got", got, flush=True)
         assert got[0] <= 16 * clean[0] and max(got[1:]) <= 16 * clean[1]
+
+
+def refused_fast(make):
+    """The call is refused as unsupported, without lists laid out for it before: 67 million tiles take half a
+    second and half a gigabyte, a refusal some microseconds."""
+    import time
+    best = 1e9
+    for _ in range(3):
+        start = time.perf_counter()
+        with pytest.raises(cgtp.CgtpError) as e:
+            make()
+        best = min(best, time.perf_counter() - start)
+        assert e.value.status == 3
+    assert best < 0.02, best
+
+
+@pytest.mark.parametrize("kv_heads", [1, 4])
+def test_more_shared_rows_than_one_launch_packs_are_refused_before_they_are_laid_out(kv_heads):
+    attn = layers.CrossAttention("32x0e", 4, kv_heads=kv_heads, dtype="bf16")
+    tiles = ((1 << 24) - 1) // kv_heads // 8 * 8                 # the packing rounds up to eight
+    s = layers.Samples([0, 1])
+    for shared in (32 * tiles + 1, (1 << 31) - 200):
+        refused_fast(lambda: attn.cache(2, 4, shared=shared))
+        refused_fast(lambda: attn.batch(s, s, shared=shared))
+
+
+def test_the_largest_caches_by_their_tiles():
+    """With 64 heads on one context head a slot has two tiles of query rows."""
+    attn = layers.CrossAttention("64x0e", 64, kv_heads=1, dtype="bf16")
+    for slots, capacity in (((1 << 23), 1), (1 << 10, (1 << 24) + 1)):
+        refused_fast(lambda: attn.cache(slots, capacity))
+    refused_fast(lambda: attn.cache(1, (1 << 30) + 1))
+    h = layers._vp()
+    # (the handle alone: no caches of that size)
+    status = layers._lib.cgtp_attn_cache_create(attn._h, 1 << 10, 1 << 24, 0, layers.ctypes.byref(h))
+    assert status == 0 and layers._lib.cgtp_attn_cache_destroy(h) == 0
