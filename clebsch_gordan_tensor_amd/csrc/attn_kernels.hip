@@ -346,7 +346,7 @@ int64_t build(WorkList& w, const std::vector<Unit>& u, int stride, int groups, i
 int forward_slots(const cgtp_attn_s* at) { return at->DP * int(dtype_size(at->dtype)) <= 512 ? 2 * kCus : kCus; }
 
 // A part's start, end, partial result and join in tiles of its keys, for sequence
-// batches. In bf16 the partial result of 128 or 256 rows (64 KB for every 32 columns of 128
+// batches. In bf16 the partial result of 128 or 256 rows (16 KB for every 32 columns of 128
 // rows, written and read) costs as much as some twenty tiles' products (us with 5, 12, 24: long
 // causal prompts 744, 679, 677; a chunk after earlier rows 202, 202, 154; prompts with a shared
 // beginning 335, 335, 318); products in fp32 take eight times as long, and the rows of one

@@ -196,7 +196,6 @@ struct StepWork {
   int index, bundle, at, end;
   int slot, before;  // the slot of turn `at` and the turns before it
   int qt, len, t0, t1;  // key tiles t0 .. t1 - 1
-  bool last;            // the slot's last places are among them
   Item it;
 };
 // False: the workgroup has nothing to do.
@@ -237,7 +236,6 @@ __device__ __forceinline__ bool step_next(const StepArgs& a, int wave, StepWork&
     const int turns = step_turns(a.cut, w.len);
     w.t0 = 0;
     w.t1 = turns > 0 ? w.len / 32 + 1 : 0;
-    w.last = turns > 0;
     w.it = {w.qt, 1, w.t0, w.t1, w.hk, -1, 1, 0};
     return true;
   }
@@ -255,7 +253,6 @@ __device__ __forceinline__ bool step_next(const StepArgs& a, int wave, StepWork&
   w.qt = w.slot * a.cut.tiles_a_slot + tile;
   w.t0 = first * wph;
   w.t1 = min(last * wph, w.len / 32 + 1);
-  w.last = last == turns;
   const bool alone = first == 0 && last == turns && !a.joined;
   w.it = {w.qt, 1, w.t0, w.t1, w.hk, alone ? -1 : step_part(a.cut, w.hk, w.index, w.qt), 1, 0};
   return true;
