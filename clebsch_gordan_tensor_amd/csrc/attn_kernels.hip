@@ -349,9 +349,14 @@ int forward_slots(const cgtp_attn_s* at) { return at->DP * int(dtype_size(at->dt
 // batches. In bf16 the partial result of 128 or 256 rows (16 KB for every 32 columns of 128
 // rows, written and read) costs as much as some twenty tiles' products (us with 5, 12, 24: long
 // causal prompts 744, 679, 677; a chunk after earlier rows 202, 202, 154; prompts with a shared
-// beginning 335, 335, 318); products in fp32 take eight times as long, and the rows of one
-// tile are few.
-int part_extra(const cgtp_attn_s* at, int per) { return dtype_size(at->dtype) == 2 && per > 1 ? 24 : 5; }
+// beginning 335, 335, 318; a chunk of heads of 96 118, 117, 114, of 192 172, 171, 158; prompts of heads of
+// 256 341, 246, 246), but for narrow heads, whose exponentials take as long as wide ones' beside
+// smaller parts, less (heads of 16, 48 and 64 with 12 and 24: a chunk 58 and 73, 87 and 89, 90 and 91;
+// prompts with a shared beginning 141 and 171, 217 and 256, 222 and 255). Products in fp32 take
+// eight times as long, and the rows of one tile are few.
+int part_extra(const cgtp_attn_s* at, int per) {
+  return dtype_size(at->dtype) != 2 || per == 1 ? 5 : at->DP <= 64 ? 12 : 24;
+}
 
 // The rows of `tokens` tokens in tiles whatever their sample, against shared_tiles key
 // tiles, in items of up to `per` tiles of rows. All units see the same tiles, so they have
