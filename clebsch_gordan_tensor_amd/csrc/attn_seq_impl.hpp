@@ -631,7 +631,7 @@ __global__ __launch_bounds__(kThreads) void rows_join_kernel(RowsJoinArgs a) {
 // rowsum(grad_out out) of queries that see few keys, from its other form sum_j P_ij dP_ij:
 // the stored out is rounded to bf16, and where few keys share a row that rounding is as
 // large as the score gradients it is taken from (a causal training batch's grad_q and grad_k 0.0025
-// off, with this 0.0023). A workgroup takes a tile of query rows, a wave one of its key tiles.
+// off, with this 0.0024). A workgroup takes a tile of query rows, a wave one of its key tiles.
 template <typename T, int DP>
 __global__ __launch_bounds__(kThreads, few_waves(DP, sizeof(T))) void delta_kernel(BwdArgs a, const int4* tiles,
                                                                                    float* rows) {
