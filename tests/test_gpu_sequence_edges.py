@@ -37,9 +37,9 @@ SEEN = [(0, 100), (150, 250), (400, 500), (2200, 2300), (3000, 3100), (4400, 450
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("causal,scale", [(False, 1.0), (True, 1.0), (True, -1.0)])
 @pytest.mark.parametrize("seen", SEEN)
-def test_few_rows_whose_parts_see_no_shared_key(seen, causal, dtype):
+def test_few_rows_whose_parts_see_no_shared_key(seen, causal, scale, dtype):
     """Samples of a tile at most on long shared rows, joined by rows: 1 - 16 rows a sample,
     with no own keys, masked ones, and some that count."""
     shared, nq = 4500, [1] * 150 + [2] * 30 + [9] * 10 + [16] * 10
@@ -53,12 +53,12 @@ def test_few_rows_whose_parts_see_no_shared_key(seen, causal, dtype):
     for s in range(3, len(nk), 8):                            # own keys of every other sample that has 40
         mask[shared + kp[s]:shared + kp[s + 1]] = True
     batch = attn.batch(layers.Samples(qp), layers.Samples(kp), causal=causal, shared=shared)
-    out, lse = attn.forward(batch, q, k, v, scale=1.0, key_mask=mask, need_lse=True)
+    out, lse = attn.forward(batch, q, k, v, scale=scale, key_mask=mask, need_lse=True)
     torch.cuda.synchronize()
     hm = mask.cpu().numpy()
-    ro, rl = ol.seq_forward("128x0e", heads, heads, qp, kp, host(q), host(k), host(v), hm, 1.0, causal, shared)
+    ro, rl = ol.seq_forward("128x0e", heads, heads, qp, kp, host(q), host(k), host(v), hm, scale, causal, shared)
     assert np.isfinite(host(out)).all() and np.isfinite(host(lse)).all()
-    assert rl.max() < -150.0
+    assert np.abs(rl).min() > 150.0
     assert rel_err(host(out), ro) <= FAR_TOL[dtype]
     assert np.abs(host(lse) - rl).max() <= FAR_LSE
 
